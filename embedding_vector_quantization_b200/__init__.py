@@ -16,7 +16,8 @@ import fails.
 from . import _lib
 from ._lib import (  # noqa: F401  (the C ABI, same names)
     TQ_BF16, TQ_EINVAL, TQ_ECAPACITY, TQ_ECUDA, TQ_ENOMEM, TQ_ETIMEOUT, TQ_EUNSUPPORTED, TQ_F16, TQ_F32, TQ_OK,
-    TQError, make_cache, tq_append, tq_attn_decode, tq_attn_decode_noalloc, tq_decode_step, tq_attn_workspace_bytes, tq_code_bytes, tq_codebook_host,
+    TQError, make_cache, make_head_prep, make_paged_batch, make_paged_cache, tq_append, tq_append_paged, tq_attn_paged,
+    tq_attn_paged_workspace_bytes, tq_attn_decode, tq_attn_decode_noalloc, tq_decode_step, tq_attn_workspace_bytes, tq_code_bytes, tq_codebook_host,
     tq_create, tq_create_polar, tq_create_prod, tq_destroy, tq_get_polar_codebook, tq_polar_codebook_host,
     tq_polar_info, tq_encode, tq_get_codebook, tq_get_info, tq_get_rotation,
     tq_last_error, tq_last_status, tq_pack_indices, tq_rotation_host, tq_score, tq_score_workspace_bytes,
@@ -195,4 +196,152 @@ def attn_decode(hk, hv, q, kcache, vcache, len_, scale, out=None, workspace=None
                                 dtype=torch.uint8, device=q.device)
     tq_attn_decode(hk.ptr, hv.ptr, q.contiguous(), B, Hq, kcache.Hkv, kcache.struct, vcache.struct, len_, scale,
                    out, workspace, stream)
+    return out
+
+
+# ------------------------------------------------------------------ paged caches
+
+
+def _need(ok, what):
+    if not ok:
+        raise TQError(TQ_EINVAL, "paged", what)
+
+
+class PagedCache:
+    """A quantized K or V cache [num_pages][Hkv][page_size] for one handle (tensors + ABI struct).
+
+    ``tensors`` wraps existing storage: a dict with "codes", "norms" and, for prod handles, "signs" and "rnorms",
+    contiguous and of these shapes. New storage starts as zeros.
+    """
+
+    def __init__(self, handle, num_pages, Hkv, page_size, device="cuda", tensors=None):
+        torch = _torch()
+        self.handle, self.num_pages, self.Hkv, self.page_size = handle, num_pages, Hkv, page_size
+        shape = (num_pages, Hkv, page_size)
+        if tensors is None:
+            tensors = {k: None if t is None else t.zero_() for k, t in handle.alloc_rows(shape, device).items()}
+        want = {"codes": (handle.codes_B, torch.uint8), "norms": (0, handle.norm_torch_dtype()),
+                "signs": (handle.signs_B, torch.uint8),
+                "rnorms": (0, torch.float16) if handle.prod and not handle.qjl_only else None}
+        for name, w in want.items():
+            t = tensors.get(name)
+            if w is None or (name in ("codes", "signs") and not w[0]):
+                t = None
+            else:
+                _need(t is not None and t.dtype == w[1] and t.is_contiguous() and t.is_cuda
+                      and tuple(t.shape) == shape + ((w[0],) if w[0] else ()),
+                      f"{name}: contiguous {w[1]} {list(shape) + ([w[0]] if w[0] else [])} on the GPU wanted")
+            setattr(self, name, t)
+        self.device = self.norms.device
+        _need(all(t is None or t.device == self.device for t in (self.codes, self.signs, self.rnorms)),
+              "the cache's tensors must be on one device")
+        self.struct = make_paged_cache(self.codes, self.signs, self.norms, self.rnorms, num_pages, page_size)
+
+
+class PagedBatch:
+    """A ragged batch: token rows q_start[b] .. q_start[b+1] - 1 are the newest tokens of sequence b, which has len[b]
+    tokens in the cache once they are in it; block_table [B, max_pages] names its pages. int32 tensors on the GPU, read
+    when the work runs. ``ntok``: token rows of the call's tensors (rows past q_start[B] are padding); ``max_q``: no
+    sequence has more token rows (default: ntok)."""
+
+    def __init__(self, q_start, len_, block_table, ntok, max_q=None):
+        torch = _torch()
+        for name, t, n in (("q_start", q_start, 1), ("len", len_, 1), ("block_table", block_table, 2)):
+            _need(t.dtype == torch.int32 and t.dim() == n and t.is_contiguous() and t.is_cuda and t.device == len_.device,
+                  f"{name}: contiguous int32 tensor of {n} dimension(s) on the GPU wanted")
+        _need(q_start.shape[0] == len_.shape[0] + 1 and block_table.shape[0] == len_.shape[0],
+              "q_start [B + 1], len [B] and block_table [B, max_pages] disagree")
+        self.q_start, self.len, self.block_table, self.ntok = q_start, len_, block_table, int(ntok)
+        self.device = len_.device
+        self.struct = make_paged_batch(q_start, len_, block_table, ntok, ntok if max_q is None else max_q)
+
+
+class HeadPrep:
+    """What each head goes through first: an RMS norm with ``weight`` [d] and ``eps``, then the rotation of its first
+    cos_sin.shape[1] coordinates by the token's position (row of ``cos_sin`` [max_pos, rot_dim] fp32: rot_dim / 2 cosines,
+    then the sines); pairs (i, i + rot_dim / 2), or (2 i, 2 i + 1) if ``interleaved``. ``pos`` int32 [ntok]: positions to
+    rotate by (default: the positions in the cache)."""
+
+    def __init__(self, cos_sin=None, interleaved=False, pos=None, weight=None, eps=1e-6):
+        torch = _torch()
+        if cos_sin is not None:
+            _need(cos_sin.dtype == torch.float32 and cos_sin.dim() == 2 and cos_sin.is_contiguous() and cos_sin.is_cuda,
+                  "cos_sin: contiguous float32 [max_pos, rot_dim] on the GPU wanted")
+        if pos is not None:
+            _need(cos_sin is not None, "pos without cos_sin")
+            _need(pos.dtype == torch.int32 and pos.dim() == 1 and pos.is_contiguous() and pos.is_cuda,
+                  "pos: contiguous int32 [ntok] on the GPU wanted")
+        if weight is not None:
+            _need(weight.dtype in (torch.float32, torch.float16, torch.bfloat16) and weight.dim() == 1
+                  and weight.is_contiguous() and weight.is_cuda, "weight: contiguous [d] on the GPU wanted")
+        self.cos_sin, self.pos, self.weight = cos_sin, pos, weight
+        self.devices = {t.device for t in (cos_sin, pos, weight) if t is not None}
+        self.struct = make_head_prep(cos_sin, pos, weight, interleaved, eps)
+
+
+def _head_rows(x, name, ntok, d):
+    """x [ntok, H, d] with contiguous heads and 16-byte token strides; copied (on the current stream) if it is laid out
+    otherwise."""
+    _need(x.is_cuda and x.dim() == 3 and x.shape[0] == ntok and x.shape[2] == d, f"{name}: [ntok, heads, {d}] on the GPU wanted")
+    if (x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != d) or x.stride(0) < x.shape[1] * d
+            or x.stride(0) * x.element_size() % 16 or x.data_ptr() % 16):
+        x = x.clone(memory_format=_torch().contiguous_format)
+    return x
+
+
+def _check_paged(kcache, vcache, batch, prep, d):
+    _need(kcache.Hkv == vcache.Hkv, "the caches differ in Hkv")
+    _need(kcache.device == vcache.device == batch.device, "caches and batch are on different devices")
+    if prep is not None:
+        _need(prep.devices <= {kcache.device}, "prep is on another device")
+        _need(prep.weight is None or prep.weight.shape[0] == d, "weight: one value for each of the head's coordinates wanted")
+        _need(prep.pos is None or prep.pos.shape[0] >= batch.ntok, "pos: one position for each token row wanted")
+
+
+def _on(stream, device):
+    """The stream a call runs on, made current: what the call allocates or copies belongs to it too."""
+    torch = _torch()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    return torch.cuda.stream(stream)
+
+
+def append_paged(hk, hv, k, v, kcache, vcache, batch, prep=None, stream=None):
+    """Quantizes the batch's keys (after ``prep``) and values k, v [ntok, Hkv, d] into their sequences' pages."""
+    if stream is not None:
+        with _on(stream, kcache.device):
+            return append_paged(hk, hv, k, v, kcache, vcache, batch, prep)
+    _check_paged(kcache, vcache, batch, prep, hk.d)
+    k, v = _head_rows(k, "k", batch.ntok, hk.d), _head_rows(v, "v", batch.ntok, hk.d)
+    _need(k.shape[1] == v.shape[1] == kcache.Hkv, "k and v need one head for each of the caches'")
+    _need(k.device == v.device == kcache.device, "k, v and the caches are on different devices")
+    tq_append_paged(hk.ptr, hv.ptr, k, v, kcache.Hkv, batch.struct, None if prep is None else prep.struct, kcache.struct,
+                    vcache.struct, _torch().cuda.current_stream(kcache.device))
+
+
+def attn_paged(hk, hv, q, kcache, vcache, batch, scale, causal=True, window=0, prep=None, out=None, workspace=None,
+               stream=None):
+    """Attention of the batch's queries q [ntok, Hq, d] (after ``prep``) over their sequences' pages -> [ntok, Hq, d] of
+    q's dtype. causal: each token over the positions up to its own (the last ``window`` of them if window > 0); not
+    causal: over all len[b] cached tokens (cross attention). Rows of padding keep what ``out`` held (new: zeros)."""
+    if stream is not None:
+        with _on(stream, kcache.device):
+            return attn_paged(hk, hv, q, kcache, vcache, batch, scale, causal, window, prep, out, workspace)
+    torch = _torch()
+    _check_paged(kcache, vcache, batch, prep, hk.d)
+    q = _head_rows(q, "q", batch.ntok, hk.d)
+    Hq = q.shape[1]
+    _need(q.device == kcache.device, "q and the caches are on different devices")
+    if out is None:
+        out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+    else:
+        _need(out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous() and out.device == q.device,
+              "out: contiguous, of q's shape, dtype and device wanted")
+    if workspace is None:
+        size = tq_attn_paged_workspace_bytes(hk.ptr, hv.ptr, batch.struct, Hq, kcache.Hkv, kcache.struct)
+        workspace = torch.empty(max(16, size), dtype=torch.uint8, device=q.device)
+    else:
+        _need(workspace.is_cuda and workspace.device == q.device and workspace.is_contiguous(), "workspace on another device")
+    tq_attn_paged(hk.ptr, hv.ptr, q, Hq, kcache.Hkv, batch.struct, None if prep is None else prep.struct, kcache.struct,
+                  vcache.struct, scale, causal, window, out, workspace, torch.cuda.current_stream(q.device))
     return out

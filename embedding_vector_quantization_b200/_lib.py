@@ -38,11 +38,28 @@ class tq_cache(ctypes.Structure):
                 ("rnorms", ctypes.c_void_p), ("L_cap", ctypes.c_int64)]
 
 
+class tq_paged_cache(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("signs", ctypes.c_void_p), ("norms", ctypes.c_void_p),
+                ("rnorms", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32)]
+
+
+class tq_paged_batch(ctypes.Structure):
+    _fields_ = [("q_start", ctypes.c_void_p), ("len", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("B", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("ntok", ctypes.c_int64), ("max_q", ctypes.c_int32)]
+
+
+class tq_head_prep(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("max_pos", ctypes.c_int64), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
 _vp, _i, _i64, _u64, _sz, _f = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint64,
                                 ctypes.c_size_t, ctypes.c_float)
 _dp = ctypes.POINTER(ctypes.c_double)
 _ip = ctypes.POINTER(ctypes.c_int)
 _cp = ctypes.POINTER(tq_cache)
+_pcp, _pbp, _hpp = ctypes.POINTER(tq_paged_cache), ctypes.POINTER(tq_paged_batch), ctypes.POINTER(tq_head_prep)
 
 _SIGS = {
     "tq_codebook_host": (_i, [_i, _i, _dp, _dp]),
@@ -70,6 +87,9 @@ _SIGS = {
     "tq_attn_decode_noalloc": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _cp, _cp, _vp, _f, _vp, _vp]),
     "tq_decode_step": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _cp, _cp, _vp, _f, _vp, _vp, _sz, _vp]),
     "tq_search_topk": (_i, [_vp, _vp, _i, _vp, _vp, _i64, _i, _vp, _vp, _vp, _sz, _vp]),
+    "tq_append_paged": (_i, [_vp, _vp, _vp, _vp, _i, _i64, _i64, _i, _pbp, _hpp, _pcp, _pcp, _vp]),
+    "tq_attn_paged_workspace_bytes": (_sz, [_vp, _vp, _pbp, _i, _i, _pcp]),
+    "tq_attn_paged": (_i, [_vp, _vp, _vp, _i, _i64, _i, _i, _pbp, _hpp, _pcp, _pcp, _f, _i, _i, _vp, _vp, _sz, _vp]),
     "tq_timer_enable": (_i, [_i]),
     "tq_timer_read": (_i, [ctypes.c_char_p, ctypes.POINTER(ctypes.c_double), _ip, _i]),
     "tq_last_status": (_i, [_vp, _vp]),
@@ -272,6 +292,45 @@ def tq_search_topk(h, q, nq, codes, norms, n, k, idx, score, workspace, stream=N
     check(lib.tq_search_topk(h, _ptr(q), nq, _ptr(codes), _ptr(norms), n, k, _ptr(idx), _ptr(score),
                              _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)),
           "tq_search_topk")
+
+
+def make_paged_cache(codes, signs, norms, rnorms, num_pages, page_size) -> tq_paged_cache:
+    return tq_paged_cache(_ptr(codes), _ptr(signs), _ptr(norms), _ptr(rnorms), int(num_pages), int(page_size))
+
+
+def make_paged_batch(q_start, len_, block_table, ntok, max_q) -> tq_paged_batch:
+    return tq_paged_batch(_ptr(q_start), _ptr(len_), _ptr(block_table), len_.shape[0], block_table.shape[1], int(ntok),
+                          int(max_q))
+
+
+def make_head_prep(cos_sin, pos, weight, interleaved, eps) -> tq_head_prep:
+    return tq_head_prep(_ptr(cos_sin), _ptr(pos), _ptr(weight), 0 if cos_sin is None else cos_sin.shape[0],
+                        0 if cos_sin is None else cos_sin.shape[1], int(interleaved),
+                        TQ_F32 if weight is None else _dtype_code(weight), float(eps))
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
+def tq_append_paged(hk, hv, k_new, v_new, Hkv, batch, prep, kcache, vcache, stream=None):
+    """k_new, v_new [ntok, Hkv, d] with contiguous heads (the token stride is the tensors' own)."""
+    if k_new.dtype != v_new.dtype:
+        raise TQError(TQ_EINVAL, "tq_append_paged", "k_new and v_new must have one dtype")
+    check(lib.tq_append_paged(hk, hv, _ptr(k_new), _ptr(v_new), _dtype_code(k_new), k_new.stride(0), v_new.stride(0), Hkv,
+                              _ref(batch), _ref(prep), _ref(kcache), _ref(vcache), _stream(stream)), "tq_append_paged")
+
+
+def tq_attn_paged_workspace_bytes(hk, hv, batch, Hq, Hkv, kcache):
+    return lib.tq_attn_paged_workspace_bytes(hk, hv, ctypes.byref(getattr(batch, "struct", batch)), Hq, Hkv,
+                                             ctypes.byref(kcache))
+
+
+def tq_attn_paged(hk, hv, q, Hq, Hkv, batch, prep, kcache, vcache, scale, causal, window, out, workspace, stream=None):
+    """q [ntok, Hq, d] with contiguous heads (the token stride is the tensor's own), out contiguous of q's dtype."""
+    check(lib.tq_attn_paged(hk, hv, _ptr(q), _dtype_code(q), q.stride(0), Hq, Hkv, _ref(batch), _ref(prep), _ref(kcache),
+                            _ref(vcache), scale, int(bool(causal)), window, _ptr(out), _ptr(workspace),
+                            workspace.numel() * workspace.element_size(), _stream(stream)), "tq_attn_paged")
 
 
 def tq_timer_enable(on):

@@ -11,3 +11,27 @@ struct tq_handle;
 // scores buffer of the two-kernel attention, used only when the workspace holds it).
 extern "C" __attribute__((visibility("hidden"))) size_t tq_internal_attn_workspace_min_bytes(
     const tq_handle* hk, const tq_handle* hv, int B, int Hq, int Hkv, int64_t L_cap);
+
+#include <cuda_runtime.h>
+
+// What the other translation units may know of a handle (device pointers stay the handle's).
+struct tq_view {
+  int d, bits, m, norm_dtype, codes_B, signs_B, device, polar;
+  const float *PiT, *Pi, *MT, *ST, *S, *cent, *bnd;   // fp32: [d][d], [d][d], [d][m], [d][m], [m][d], centroids, boundaries
+  const double* t64;       // d <= 256: Pi [d][d], S [m][d], M [m][d], 16 boundaries (+inf padded), 16 centroids
+  const uint8_t* ops16;    // d = 64 or 128 (m = 0 or d): f16 operands, see ops16_* in paged_tc.cuh; NULL otherwise
+  float m_abs, m_norm;     // largest row of M in the 1-norm and the 2-norm
+  int* err;                // device error word
+  const double *cent_h, *bnd_h;   // host copies
+};
+__attribute__((visibility("hidden"))) void tq_internal_view(const tq_handle* h, tq_view* v);
+__attribute__((visibility("hidden"))) int tq_internal_ok();
+__attribute__((visibility("hidden"))) bool tq_internal_fault(const char* what);
+// TQ_FAULT=timeout for a call on h (no lengths to check).
+__attribute__((visibility("hidden"))) int tq_internal_pre_launch(const tq_handle* h, cudaStream_t s);
+// Brackets one kernel launch with timer events while the timer is on (KernelScope of tq_api.cu).
+struct tq_launch_scope {
+  void* impl;
+  __attribute__((visibility("hidden"))) tq_launch_scope(const char* name, cudaStream_t s);
+  __attribute__((visibility("hidden"))) ~tq_launch_scope();
+};

@@ -61,6 +61,9 @@ struct tq_handle {
   float* dbnd = nullptr;  // [2^bits - 1]
   int* derr = nullptr;    // device error word
   uint8_t* dOps = nullptr; // d = 128: pre-swizzled 16-bit hi/lo operands of the tensor-core encode
+  double* d64 = nullptr;    // d <= 256: fp64 tables of the paged operators (layout: tq_view in internal.h)
+  uint8_t* dOps16 = nullptr; // d = 64 or 128: f16 operands of the paged operators (layout: tq_view in internal.h)
+  float m_abs = 0.f, m_norm = 0.f;  // largest row of M = S Pi^T in the 1-norm and the 2-norm
   uint16_t* dPiB = nullptr; // MSE, d % 256 = 0, 256 <= d <= 4096: Pi as a bf16 pair, [2][d][d] (hi rows, lo rows)
   // recursive polar transform handles (tq_create_polar): per-level angle codebooks
   int polar = 0;
@@ -193,6 +196,10 @@ void free_device(tq_handle* h) {
   cudaFree(h->dOps);
   cudaFree(h->dPiB);
   h->dPiB = nullptr;
+  cudaFree(h->d64);
+  cudaFree(h->dOps16);
+  h->d64 = nullptr;
+  h->dOps16 = nullptr;
   cudaFree(h->dTab);
   h->dPi = h->dPiT = h->dS = h->dST = h->dMT = h->dcent = h->dbnd = nullptr;
   h->derr = nullptr;
@@ -328,8 +335,25 @@ int create_common(int d, int bits_mse, int m, uint64_t seed, int norm_dtype, tq_
       pib[(size_t)d * d + i] = bf16((float)(h->Pi[i] - (double)hf));
     }
   }
+  // paged operators: fp64 Pi, S, M, then 16 boundaries (padded with +inf) and 16 centroids
+  std::vector<double> t64;
+  std::vector<uint8_t> ops16;
+  if (d <= 256) {
+    t64 = h->Pi;
+    t64.insert(t64.end(), h->S.begin(), h->S.end());
+    t64.insert(t64.end(), M.begin(), M.end());
+    for (int i = 0; i < 16; ++i) t64.push_back(i < L - 1 ? h->bnd[i] : INFINITY);
+    for (int i = 0; i < 16; ++i) t64.push_back(i < L ? h->cent[i] : 0.0);
+    for (int i = 0; i < m; ++i) {
+      double a1 = 0.0, a2 = 0.0;
+      for (int k = 0; k < d; ++k) a1 += std::fabs(M[(size_t)i * d + k]), a2 += M[(size_t)i * d + k] * M[(size_t)i * d + k];
+      h->m_abs = std::max(h->m_abs, (float)a1);
+      h->m_norm = std::max(h->m_norm, (float)std::sqrt(a2));
+    }
+  }
   int st = TQ_OK;
-  if ((st = upload(&h->dPi, Pi, "Pi")) || (st = upload(&h->dPiT, PiT, "PiT")) ||
+  if ((st = upload(&h->d64, t64, "fp64 tables")) || (st = upload(&h->dOps16, ops16, "f16 operands")) ||
+      (st = upload(&h->dPi, Pi, "Pi")) || (st = upload(&h->dPiT, PiT, "PiT")) ||
       (st = upload(&h->dS, S, "S")) || (st = upload(&h->dST, ST, "ST")) || (st = upload(&h->dMT, MT, "MT")) ||
       (st = upload(&h->dcent, cent, "centroids")) || (st = upload(&h->dbnd, bnd, "bounds")) ||
       (st = upload(&h->dOps, ops, "tensor-core operands")) || (st = upload(&h->dPiB, pib, "bf16 rotation pair"))) {
@@ -1029,6 +1053,21 @@ int pre_launch(const tq_handle* h, const int32_t* len, int B, int64_t L_cap, cud
 }
 
 }  // namespace
+
+void tq_internal_view(const tq_handle* h, tq_view* v) {
+  v->d = h->d, v->bits = h->bits, v->m = h->m, v->norm_dtype = h->norm_dtype;
+  v->codes_B = h->codes_B, v->signs_B = h->signs_B, v->device = h->device, v->polar = h->polar;
+  v->PiT = h->dPiT, v->Pi = h->dPi, v->MT = h->dMT, v->ST = h->dST, v->S = h->dS, v->cent = h->dcent, v->bnd = h->dbnd;
+  v->t64 = h->d64, v->ops16 = h->dOps16, v->m_abs = h->m_abs, v->m_norm = h->m_norm, v->err = h->derr;
+  v->cent_h = h->cent.data(), v->bnd_h = h->bnd.data();
+}
+int tq_internal_ok() { return ok(); }
+bool tq_internal_fault(const char* what) { return fault_is(what); }
+int tq_internal_pre_launch(const tq_handle* h, cudaStream_t s) { return pre_launch(h, nullptr, 0, 0, s); }
+// Nothing is allocated while the timer is off.
+tq_launch_scope::tq_launch_scope(const char* name, cudaStream_t s)
+    : impl(g_timer_on.load(std::memory_order_relaxed) ? new KernelScope(name, s) : nullptr) {}
+tq_launch_scope::~tq_launch_scope() { delete static_cast<KernelScope*>(impl); }
 
 // ============================================================================
 extern "C" {
@@ -1787,6 +1826,8 @@ int tq_last_status(const tq_handle* h, void* stream) {
   }
   if (word & tqk::kErrInternal) return fail(TQ_ECUDA, "a kernel found its shared memory misaligned");
   if (word & tqk::kErrBounds) return fail(TQ_EINVAL, "a length len[b] outside 0 .. L_cap (found by TQ_CHECK=1)");
+  if (word & tqk::kErrPaged)
+    return fail(TQ_EINVAL, "a paged batch named a page, a position or a rotation position out of range (its rows were skipped)");
   if (word & tqk::kErrTimeout) return fail(TQ_ETIMEOUT, "a bounded device wait timed out");
   if (word & tqk::kErrCapacity) return fail(TQ_ECAPACITY, "append skipped a full sequence (len == L_cap)");
   return ok();

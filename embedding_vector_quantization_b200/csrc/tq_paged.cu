@@ -1,0 +1,316 @@
+// C ABI of the paged operators (declared in include/tq.h): argument checks, workspace layout and launches of
+// tq_append_paged and tq_attn_paged.
+
+#include <cuda_runtime.h>
+#include <nvtx3/nvToolsExt.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstdlib>
+#include <cstring>
+
+#include "tq.h"
+#include "internal.h"
+#include "common.cuh"
+#include "paged_common.cuh"
+#include "paged_append.cuh"
+#include "paged_attn_simt.cuh"
+
+namespace {
+
+using namespace tqk::paged;
+
+#define fail tq_internal_fail
+
+struct Nvtx {
+  explicit Nvtx(const char* n) { nvtxRangePushA(n); }
+  ~Nvtx() { nvtxRangePop(); }
+};
+
+// The handle's device for the duration of a call.
+struct DeviceGuard {
+  int was = -1;
+  cudaError_t err = cudaSuccess;
+  explicit DeviceGuard(int dev) {
+    int cur = 0;
+    err = cudaGetDevice(&cur);
+    if (err == cudaSuccess && cur != dev) {
+      err = cudaSetDevice(dev);
+      if (err == cudaSuccess) was = cur;
+    }
+  }
+  ~DeviceGuard() {
+    if (was >= 0) cudaSetDevice(was);
+  }
+};
+
+bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+int elem_bytes(int dt) { return dt == TQ_F32 ? 4 : 2; }
+bool valid_dtype(int dt) { return dt == TQ_F32 || dt == TQ_F16 || dt == TQ_BF16; }
+
+int launched(const char* what) {
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(TQ_ECUDA, "%s: %s", what, cudaGetErrorString(e));
+  return tq_internal_ok();
+}
+
+// Raises a kernel's shared memory limit once per device.
+template <typename K>
+int allow_smem(K kernel, size_t bytes, int device, std::atomic<uint64_t>& seen) {
+  if (device >= 0 && device < 64 && (seen.load(std::memory_order_acquire) >> device & 1)) return TQ_OK;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e != cudaSuccess) return fail(TQ_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+  if (device >= 0 && device < 64) seen.fetch_or(1ull << device, std::memory_order_release);
+  return TQ_OK;
+}
+
+Quant quant_of(const tq_view& v) {
+  Quant q{};
+  q.d = v.d, q.bits = v.bits, q.m = v.m, q.norm_dtype = v.norm_dtype, q.codes_B = v.codes_B, q.signs_B = v.signs_B;
+  q.PiT = v.PiT, q.Pi = v.Pi, q.MT = v.MT, q.ST = v.ST, q.S = v.S, q.cent = v.cent, q.bnd = v.bnd, q.t64 = v.t64;
+  q.m_abs = v.m_abs, q.m_norm = v.m_norm;
+  return q;
+}
+
+int check_handles(const tq_handle* hk, const tq_handle* hv, tq_view* k, tq_view* v) {
+  if (!hk || !hv) return fail(TQ_EINVAL, "handle is NULL");
+  tq_internal_view(hk, k);
+  tq_internal_view(hv, v);
+  if (k->polar || v->polar) return fail(TQ_EUNSUPPORTED, "polar handles have no paged operators");
+  if (k->d != v->d) return fail(TQ_EINVAL, "key d=%d, value d=%d", k->d, v->d);
+  if (k->d > 256 || k->m > 256 || v->m > 256) return fail(TQ_EUNSUPPORTED, "paged operators need d <= 256 and m <= 256");
+  if (k->device != v->device) return fail(TQ_EINVAL, "the handles are on devices %d and %d", k->device, v->device);
+  return TQ_OK;
+}
+
+// What can be said of a cache without its handle.
+int check_pages(const tq_paged_cache* c, const char* name) {
+  if (!c) return fail(TQ_EINVAL, "%s cache is NULL", name);
+  if (c->page_size < 16 || c->page_size > 1024 || c->page_size % 16)
+    return fail(TQ_EINVAL, "%s page_size=%d (a multiple of 16, 16..1024)", name, c->page_size);
+  if (c->num_pages < 1 || c->num_pages > (int64_t)1 << 31) return fail(TQ_EINVAL, "%s num_pages=%lld", name, (long long)c->num_pages);
+  if (!c->norms) return fail(TQ_EINVAL, "%s cache: NULL norms", name);
+  if (!aligned(c->norms, 16) || !aligned(c->codes, 16) || !aligned(c->signs, 16) || !aligned(c->rnorms, 16))
+    return fail(TQ_EINVAL, "%s cache: pointers need 16-byte alignment", name);
+  return TQ_OK;
+}
+
+int check_pages(const tq_paged_cache* k, const tq_paged_cache* v) {
+  int st;
+  if ((st = check_pages(k, "key")) || (st = check_pages(v, "value"))) return st;
+  if (k->page_size != v->page_size || k->num_pages != v->num_pages)
+    return fail(TQ_EINVAL, "the key and value caches share one block table: page_size and num_pages must agree");
+  return TQ_OK;
+}
+
+int check_cache(const tq_view& h, const tq_paged_cache* c, const char* name) {
+  if (h.codes_B > 0 && !c->codes) return fail(TQ_EINVAL, "%s cache: NULL codes", name);
+  if (h.m > 0 && (!c->signs || (h.bits > 0 && !c->rnorms))) return fail(TQ_EINVAL, "%s cache: prod rows need signs and rnorms", name);
+  return TQ_OK;
+}
+
+int check_batch(const tq_paged_batch* b, const tq_paged_cache* k, Batch* out) {
+  if (!b) return fail(TQ_EINVAL, "batch is NULL");
+  if (b->B < 0 || b->B > 65536) return fail(TQ_EINVAL, "B=%d outside 0..65536", b->B);
+  if (b->ntok < 0 || b->ntok > (1 << 24)) return fail(TQ_EINVAL, "ntok=%lld outside 0..2^24", (long long)b->ntok);
+  if (b->max_pages < 1 || (int64_t)b->max_pages * (k ? k->page_size : 1) > 0x40000000)
+    return fail(TQ_EINVAL, "max_pages=%d (at least 1, at most 2^30 positions)", b->max_pages);
+  if (b->max_q < 0 || b->max_q > b->ntok) return fail(TQ_EINVAL, "max_q=%d outside 0..ntok", b->max_q);
+  if (b->B > 0 && (!b->q_start || !b->len || !b->block_table)) return fail(TQ_EINVAL, "batch: NULL array");
+  if (!aligned(b->q_start, 4) || !aligned(b->len, 4) || !aligned(b->block_table, 4)) return fail(TQ_EINVAL, "batch: misaligned array");
+  out->q_start = b->q_start, out->len = b->len, out->table = b->block_table;
+  out->B = b->B, out->max_pages = b->max_pages, out->max_q = b->max_q, out->ntok = b->ntok;
+  out->page_size = k ? k->page_size : 16, out->num_pages = k ? k->num_pages : 0;
+  return TQ_OK;
+}
+
+int check_prep(const tq_head_prep* p, Prep* out) {
+  *out = Prep{};
+  if (!p) return TQ_OK;
+  if (p->cos_sin) {
+    if (p->rot_dim < 8 || p->rot_dim % 8) return fail(TQ_EINVAL, "rot_dim=%d (a multiple of 8, 8..d)", p->rot_dim);
+    if (p->max_pos < 1) return fail(TQ_EINVAL, "max_pos=%lld", (long long)p->max_pos);
+    if (p->interleaved != 0 && p->interleaved != 1) return fail(TQ_EINVAL, "interleaved=%d (0 or 1)", p->interleaved);
+    if (!aligned(p->cos_sin, 16) || !aligned(p->pos, 4)) return fail(TQ_EINVAL, "cos_sin or pos misaligned");
+    out->cos_sin = p->cos_sin, out->pos = p->pos, out->max_pos = p->max_pos, out->rot_dim = p->rot_dim;
+    out->interleaved = p->interleaved;
+  }
+  if (p->weight) {
+    if (!valid_dtype(p->weight_dtype)) return fail(TQ_EINVAL, "weight dtype %d", p->weight_dtype);
+    if (!(p->eps > 0.f) || !std::isfinite(p->eps)) return fail(TQ_EINVAL, "eps must be positive");
+    if (!aligned(p->weight, elem_bytes(p->weight_dtype))) return fail(TQ_EINVAL, "weight misaligned");
+    out->weight = p->weight, out->weight_dtype = p->weight_dtype, out->eps = p->eps;
+  }
+  return TQ_OK;
+}
+
+int check_rows(const void* x, int dtype, int64_t stride, int H, int d, const char* name) {
+  if (!x) return fail(TQ_EINVAL, "%s is NULL", name);
+  if (!aligned(x, 16)) return fail(TQ_EINVAL, "%s misaligned (16 bytes)", name);
+  if (stride < (int64_t)H * d || stride * elem_bytes(dtype) % 16) return fail(TQ_EINVAL, "%s stride %lld", name, (long long)stride);
+  return TQ_OK;
+}
+
+CacheView view_of(const tq_view& h, const tq_paged_cache* c) {
+  CacheView v{};
+  v.codes = h.codes_B > 0 ? c->codes : nullptr;
+  v.signs = h.m > 0 ? c->signs : nullptr;
+  v.norms = c->norms;
+  v.rnorms = h.m > 0 && h.bits > 0 ? static_cast<__half*>(c->rnorms) : nullptr;
+  return v;
+}
+
+int device_sms(int device) {
+  static std::atomic<int> sms[64];
+  if (device < 0 || device >= 64) return 148;
+  int n = sms[device].load();
+  if (!n) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || n < 1) n = 148;
+    sms[device].store(n);
+  }
+  return n;
+}
+
+// ---------------------------------------------------------------- append
+
+template <int R>
+int append_simt(const AppendArgs& a, int device, cudaStream_t s) {
+  static std::atomic<uint64_t> seen{0};
+  if (int st = allow_smem(paged_append_kernel<R>, append_smem_bytes(256, 256, R), device, seen)) return st;
+  const int m = std::max(a.q[0].m, a.q[1].m);
+  const unsigned groups = (unsigned)((a.bt.ntok * a.Hkv + R - 1) / R);
+  tq_launch_scope scope("append_paged", s);
+  paged_append_kernel<R><<<dim3(groups, 2), kAppThreads, append_smem_bytes(a.q[0].d, m, R), s>>>(a);
+  return launched("paged_append_kernel");
+}
+
+// ---------------------------------------------------------------- attention, general kernels
+
+struct SimtPlan {
+  int64_t tiles;      // upper bound over the batches that fit the arguments
+  int nsplit;
+  size_t qr, part, total;
+};
+
+SimtPlan simt_plan(const tq_view& k, const tq_view& v, const Batch& b, int Hq, int Hkv, int sms) {
+  SimtPlan p{};
+  const int G = Hq / Hkv;
+  p.tiles = std::min<int64_t>(b.ntok * G / kTileRows + b.B, (int64_t)b.B * (((int64_t)b.max_q * G + kTileRows - 1) / kTileRows));
+  p.tiles = std::max<int64_t>(p.tiles, 1);
+  const int64_t keys = (int64_t)b.max_pages * b.page_size;
+  p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>((8 * sms) / (p.tiles * Hkv), (keys + 255) / 256));
+  p.qr = 0;
+  p.part = up((size_t)b.ntok * Hq * (k.d + k.m) * 4, 256);
+  // tiles * Hkv * nsplit <= max(tiles * Hkv, 8 sms): a smaller batch never needs more than a larger one
+  p.total = p.part + up((size_t)std::max<int64_t>(p.tiles * Hkv, 8 * sms) * kTileRows * (v.d + v.m + 2) * 4, 256) + 256;
+  return p;
+}
+
+int attn_simt(AttnArgs& a, const tq_view& k, const tq_view& v, const SimtPlan& p, char* ws, int device, cudaStream_t s) {
+  static std::atomic<uint64_t> s1{0}, s2{0}, s3{0};
+  constexpr int R = 8;
+  const size_t combine = (size_t)R * (256 + 256 + 2 * 256) * 4 + (size_t)kAppThreads * R * 4;
+  int st;
+  if ((st = allow_smem(paged_qprep_kernel<R>, qprep_smem_bytes(256, 256, R), device, s1)) ||
+      (st = allow_smem(paged_attn_simt_kernel, attn_simt_smem_bytes(512, 512), device, s2)) ||
+      (st = allow_smem(paged_combine_simt_kernel, combine, device, s3)))
+    return st;
+  a.qr = reinterpret_cast<float*>(ws + p.qr);
+  a.part = reinterpret_cast<float*>(ws + p.part);
+  a.nsplit = p.nsplit;
+  a.tile_rows = kTileRows;
+  {
+    tq_launch_scope scope("paged_qprep", s);
+    paged_qprep_kernel<R><<<(unsigned)((a.bt.ntok * a.Hq + R - 1) / R), kAppThreads, qprep_smem_bytes(k.d, k.m, R), s>>>(a);
+  }
+  if ((st = launched("paged_qprep_kernel"))) return st;
+  {
+    tq_launch_scope scope("paged_attn", s);
+    paged_attn_simt_kernel<<<dim3((unsigned)p.tiles, (unsigned)a.Hkv, (unsigned)p.nsplit), kAttThreads,
+                             attn_simt_smem_bytes(k.d + k.m, v.d + v.m), s>>>(a);
+  }
+  if ((st = launched("paged_attn_simt_kernel"))) return st;
+  tq_launch_scope scope("paged_combine", s);
+  paged_combine_simt_kernel<<<dim3((unsigned)p.tiles, (unsigned)a.Hkv), kAppThreads, combine, s>>>(a);
+  return launched("paged_combine_simt_kernel");
+}
+
+}  // namespace
+
+extern "C" {
+
+int tq_append_paged(const tq_handle* hk, const tq_handle* hv, const void* k_new, const void* v_new, int x_dtype,
+                    int64_t k_stride, int64_t v_stride, int Hkv, const tq_paged_batch* batch, const tq_head_prep* prep,
+                    const tq_paged_cache* k, const tq_paged_cache* v, void* stream) {
+  Nvtx nvtx("tq_append_paged");
+  tq_view kw, vw;
+  AppendArgs a{};
+  int st;
+  if (Hkv < 1 || Hkv > 1024) return fail(TQ_EINVAL, "Hkv=%d outside 1..1024", Hkv);
+  if (!valid_dtype(x_dtype)) return fail(TQ_EINVAL, "x dtype %d", x_dtype);
+  if ((st = check_pages(k, v)) || (st = check_batch(batch, k, &a.bt)) || (st = check_prep(prep, &a.prep))) return st;
+  if ((st = check_handles(hk, hv, &kw, &vw)) || (st = check_cache(kw, k, "key")) || (st = check_cache(vw, v, "value"))) return st;
+  if (a.prep.rot_dim > kw.d) return fail(TQ_EINVAL, "rot_dim=%d, d=%d", a.prep.rot_dim, kw.d);
+  if (batch->B == 0 || batch->ntok == 0) return tq_internal_ok();
+  if ((st = check_rows(k_new, x_dtype, k_stride, Hkv, kw.d, "k_new")) || (st = check_rows(v_new, x_dtype, v_stride, Hkv, kw.d, "v_new")))
+    return st;
+  if (tq_internal_fault("launch")) return fail(TQ_ECUDA, "injected launch failure (TQ_FAULT=launch)");
+  DeviceGuard dev(kw.device);
+  if (dev.err != cudaSuccess) return fail(TQ_ECUDA, "device %d: %s", kw.device, cudaGetErrorString(dev.err));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((st = tq_internal_pre_launch(hk, s))) return st;
+  a.x[0] = k_new, a.x[1] = v_new, a.stride[0] = k_stride, a.stride[1] = v_stride;
+  a.x_dtype = x_dtype, a.Hkv = Hkv;
+  a.q[0] = quant_of(kw), a.q[1] = quant_of(vw);
+  a.c[0] = view_of(kw, k), a.c[1] = view_of(vw, v);
+  a.err = kw.err;
+  const int64_t rows = batch->ntok * Hkv;
+  if (rows <= device_sms(kw.device)) return append_simt<1>(a, kw.device, s);
+  return append_simt<8>(a, kw.device, s);
+}
+
+size_t tq_attn_paged_workspace_bytes(const tq_handle* hk, const tq_handle* hv, const tq_paged_batch* batch, int Hq, int Hkv,
+                                     const tq_paged_cache* k) {
+  tq_view kw, vw;
+  Batch b{};
+  if (check_handles(hk, hv, &kw, &vw) || check_pages(k, "key") || Hkv < 1 || Hq < 1 || Hq % Hkv || check_batch(batch, k, &b)) return 0;
+  return simt_plan(kw, vw, b, Hq, Hkv, device_sms(kw.device)).total;
+}
+
+int tq_attn_paged(const tq_handle* hk, const tq_handle* hv, const void* q, int q_dtype, int64_t q_stride, int Hq, int Hkv,
+                  const tq_paged_batch* batch, const tq_head_prep* prep, const tq_paged_cache* k, const tq_paged_cache* v,
+                  float scale, int causal, int window, void* out, void* workspace, size_t ws_bytes, void* stream) {
+  Nvtx nvtx("tq_attn_paged");
+  tq_view kw, vw;
+  AttnArgs a{};
+  int st;
+  if (Hkv < 1 || Hkv > 1024 || Hq < 1 || Hq % Hkv || Hq / Hkv > 256) return fail(TQ_EINVAL, "Hq=%d Hkv=%d", Hq, Hkv);
+  if (!valid_dtype(q_dtype)) return fail(TQ_EINVAL, "q dtype %d", q_dtype);
+  if (!std::isfinite(scale)) return fail(TQ_EINVAL, "scale is not finite");
+  if (causal != 0 && causal != 1) return fail(TQ_EINVAL, "causal=%d (0 or 1)", causal);
+  if (window < 0 || (window > 0 && !causal)) return fail(TQ_EINVAL, "window=%d (>= 0, and 0 without causal)", window);
+  if ((st = check_pages(k, v)) || (st = check_batch(batch, k, &a.bt)) || (st = check_prep(prep, &a.prep))) return st;
+  if (!causal && a.prep.cos_sin && !a.prep.pos) return fail(TQ_EINVAL, "a rotation without causal needs prep->pos");
+  if ((st = check_handles(hk, hv, &kw, &vw)) || (st = check_cache(kw, k, "key")) || (st = check_cache(vw, v, "value"))) return st;
+  if (a.prep.rot_dim > kw.d) return fail(TQ_EINVAL, "rot_dim=%d, d=%d", a.prep.rot_dim, kw.d);
+  if (batch->B == 0 || batch->ntok == 0 || batch->max_q == 0) return tq_internal_ok();
+  if ((st = check_rows(q, q_dtype, q_stride, Hq, kw.d, "q"))) return st;
+  if (!out || !aligned(out, 16)) return fail(TQ_EINVAL, "out is NULL or misaligned (16 bytes)");
+  if (!workspace || !aligned(workspace, 16)) return fail(TQ_EINVAL, "workspace is NULL or misaligned (16 bytes)");
+  const SimtPlan plan = simt_plan(kw, vw, a.bt, Hq, Hkv, device_sms(kw.device));
+  if (ws_bytes < plan.total) return fail(TQ_EINVAL, "workspace of %zu bytes, %zu needed", ws_bytes, plan.total);
+  if (tq_internal_fault("launch")) return fail(TQ_ECUDA, "injected launch failure (TQ_FAULT=launch)");
+  DeviceGuard dev(kw.device);
+  if (dev.err != cudaSuccess) return fail(TQ_ECUDA, "device %d: %s", kw.device, cudaGetErrorString(dev.err));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((st = tq_internal_pre_launch(hk, s))) return st;
+  a.q = q, a.q_stride = q_stride, a.q_dtype = q_dtype, a.Hq = Hq, a.Hkv = Hkv, a.G = Hq / Hkv;
+  a.k = quant_of(kw), a.v = quant_of(vw), a.kc = view_of(kw, k), a.vc = view_of(vw, v);
+  a.scale = scale, a.causal = causal, a.window = window, a.out = out, a.err = kw.err;
+  char* ws = reinterpret_cast<char*>(up(reinterpret_cast<size_t>(workspace), 256));
+  return attn_simt(a, kw, vw, plan, ws, kw.device, s);
+}
+
+}  // extern "C"

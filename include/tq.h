@@ -284,6 +284,94 @@ int tq_search_topk(const tq_handle* h, const float* q, int nq, const uint8_t* co
                    void* workspace, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Paged caches: ragged batches of new tokens, append and attention
+ * ------------------------------------------------------------------------ */
+
+/* One quantized cache (K or V) cut into pages. All pointers are device pointers, row-major in the
+ * order [num_pages][Hkv][page_size] (then the packed row); rows, norms and NULLs as in tq_cache
+ * (bases 16-byte aligned). Which pages a sequence has, and in which order, is the batch's block table. */
+typedef struct tq_paged_cache {
+  uint8_t* codes;    /* [num_pages][Hkv][page_size][codes_B]          */
+  uint8_t* signs;    /* [num_pages][Hkv][page_size][signs_B] or NULL  */
+  void* norms;       /* [num_pages][Hkv][page_size], handle's dtype   */
+  void* rnorms;      /* [num_pages][Hkv][page_size] fp16, or NULL     */
+  int64_t num_pages;
+  int32_t page_size; /* a multiple of 16, 16 .. 1024                  */
+} tq_paged_cache;
+
+/* A ragged batch of B sequences with `ntok` tokens: token rows q_start[b] .. q_start[b+1] - 1 are the
+ * newest tokens of sequence b, in order. len[b] counts the tokens sequence b has in the cache once these
+ * are in it, so token i of its n is at position len[b] - n + i; position p lives in page
+ * block_table[b][p / page_size], slot p % page_size. The arrays are read on the device, when the work runs
+ * (a captured call sees the values of each replay). Token rows from q_start[B] on, up to ntok, are padding:
+ * not read, and what belongs to them is left as it was. */
+typedef struct tq_paged_batch {
+  const int32_t* q_start;     /* device [B + 1], ascending from q_start[0] >= 0  */
+  const int32_t* len;         /* device [B]                                      */
+  const int32_t* block_table; /* device [B][max_pages]; entries past a sequence's pages are not read */
+  int32_t B, max_pages;
+  int64_t ntok;               /* token rows of the arrays (>= q_start[B])        */
+  int32_t max_q;              /* no sequence has more token rows than this       */
+} tq_paged_batch;
+
+/* What is done to each head of a new key (tq_append_paged) or a query (tq_attn_paged) before it is used,
+ * without an intermediate rounding: x = x / sqrt(mean(x^2) + eps) * weight, if weight is not NULL; then,
+ * if cos_sin is not NULL, the rotation of its first rot_dim coordinates by the token's position: pairs
+ * (i, i + rot_dim / 2), or (2 i, 2 i + 1) if interleaved, pair i by the angle whose cosine and sine are
+ * cos_sin[position][i] and cos_sin[position][rot_dim / 2 + i]. */
+typedef struct tq_head_prep {
+  const float* cos_sin;   /* device [max_pos][rot_dim] fp32, 16-byte aligned, or NULL      */
+  const int32_t* pos;     /* device [ntok] rotation positions; NULL: positions in the cache */
+  const void* weight;     /* device [d] of weight_dtype, or NULL                            */
+  int64_t max_pos;
+  int32_t rot_dim;        /* a multiple of 8, 8 .. d                                        */
+  int32_t interleaved;    /* 0 or 1                                                         */
+  int32_t weight_dtype;   /* TQ_F32, TQ_F16 or TQ_BF16                                      */
+  float eps;              /* > 0 with a weight                                              */
+} tq_head_prep;
+
+/* Appends the batch's keys (after `prep`; NULL: as they are) and values to a paged K and V cache
+ * [TQ6x Stage 1 and 2: online arrival with a fixed codebook]: each vector's row as tq_encode defines it.
+ *  k_new, v_new  device [ntok][Hkv][d] of x_dtype, 16-byte aligned; k_stride, v_stride: elements from one
+ *                token to the next (multiples of 16 bytes, >= Hkv * d), so that both may be slices of one
+ *                projection's output
+ *  hk, hv        MSE, prod or QJL-only handles of one d <= 256 (m <= 256), on one device
+ * The indices and signs are those of exact arithmetic: a coordinate that lies within the rounding of the fast
+ * path of a border is computed again in 64 bits, so a token's bytes depend neither on the batch it came in
+ * nor on the kernel that wrote it.
+ * A token whose page (outside 0 .. num_pages - 1, position outside 0 .. max_pages * page_size - 1) or rotation
+ * position (outside 0 .. max_pos - 1) is out of range is skipped and recorded in hk's error word (TQ_EINVAL
+ * from tq_last_status). Two tokens with the same place race; which one stays is undefined. */
+int tq_append_paged(const tq_handle* hk, const tq_handle* hv, const void* k_new, const void* v_new, int x_dtype,
+                    int64_t k_stride, int64_t v_stride, int Hkv, const tq_paged_batch* batch,
+                    const tq_head_prep* prep, const tq_paged_cache* k, const tq_paged_cache* v, void* stream);
+
+/* Workspace (bytes) of tq_attn_paged for batches of at most this B, ntok, max_q and max_pages; never 0 for a
+ * valid call. */
+size_t tq_attn_paged_workspace_bytes(const tq_handle* hk, const tq_handle* hv, const tq_paged_batch* batch, int Hq,
+                                     int Hkv, const tq_paged_cache* k);
+
+/* Attention of the batch's tokens over their sequences' pages [DEEP "Scaled dot-product attention"]: the query of
+ * head h at position p attends over KV head h / (Hq / Hkv), out = softmax(scale * s) V_hat with s and V_hat as in
+ * tq_attn_decode.
+ *  causal = 1: keys at positions <= p (the token's own row included: append first); with window > 0 only keys at
+ *              positions > p - window.
+ *  causal = 0: every key of the sequence, whatever its position (cross attention to cached encoder states:
+ *              len[b] counts the states, the tokens are not among them); window must be 0. prep->pos is then
+ *              needed for a rotation.
+ *  q           device [ntok][Hq][d] of q_dtype, q_stride elements from token to token (as k_stride)
+ *  out         device [ntok][Hq][d] of q_dtype, contiguous, 16-byte aligned
+ *  workspace   device scratch, 16-byte aligned; calls that overlap need one each
+ * A query that sees no key (len[b] == 0, or a position < 0) gets zeros, as does one whose rotation position is out
+ * of range (recorded as above); keys on a page out of range are not seen (recorded). Padding rows of out keep what
+ * they held. Arithmetic: fp32 queries in fp32 throughout; 16-bit queries with f16 operands on the tensor cores where
+ * the formats allow (d 64 or 128, m 0 or d), sums and softmax statistics in fp32. */
+int tq_attn_paged(const tq_handle* hk, const tq_handle* hv, const void* q, int q_dtype, int64_t q_stride, int Hq,
+                  int Hkv, const tq_paged_batch* batch, const tq_head_prep* prep, const tq_paged_cache* k,
+                  const tq_paged_cache* v, float scale, int causal, int window, void* out, void* workspace,
+                  size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Kernel timer (tracing; off by default, no cost when off)
  * ------------------------------------------------------------------------ */
 
