@@ -43,7 +43,7 @@ __device__ __forceinline__ Tile warp_find_tile(const Batch& bt, int G, int tile_
   int before = 0;
   for (int b0 = 0; b0 < bt.B; b0 += 32) {
     const int b = b0 + lane;
-    const int n = b < bt.B ? max(0, bt.q_start[b + 1] - bt.q_start[b]) : 0;
+    const int n = b < bt.B ? seq_tokens(bt, b) : 0;
     const int nt = (n * G + tile_rows - 1) / tile_rows;
     int incl = nt;
     for (int o = 1; o < 32; o <<= 1) {

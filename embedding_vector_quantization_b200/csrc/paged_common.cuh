@@ -57,6 +57,12 @@ __device__ __forceinline__ int warp_find_seq(const Batch& bt, int64_t t) {
   return ended;
 }
 
+// Token rows of sequence b; none if its bounds lie outside the batch's rows.
+__device__ __forceinline__ int seq_tokens(const Batch& bt, int b) {
+  const int lo = bt.q_start[b], hi = bt.q_start[b + 1];
+  return lo >= 0 && hi > lo && hi <= bt.ntok ? hi - lo : 0;
+}
+
 // Row index of (position p, head h) of sequence b in a cache [page][Hkv][slot], -1 if its page is out of range.
 __device__ __forceinline__ int64_t place_of(const Batch& bt, int b, int64_t p, int h, int Hkv) {
   if (p < 0 || p >= (int64_t)bt.max_pages * bt.page_size) return -1;

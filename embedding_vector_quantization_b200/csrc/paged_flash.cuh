@@ -1,0 +1,1047 @@
+// Attention of chunks of new tokens over paged caches on the tcgen05 tensor cores: d = 64 or 128, any MSE bits, with or
+// without d signs, 16-bit queries.
+//
+// A chunk of n tokens reads each cached row n * G times (G query heads share a KV head), so each row is decoded once:
+//   plan    one CTA lists the sequences that come here (more than `small_rows` query rows), their key tiles of 128 tokens
+//           and their items of 256 query rows, with the running sum of the items' key tiles;
+//   expand  key tiles -> f16 rows x_hat = Pi^T c[idx] + rnorm / norm * sqrt(pi/2) / m S^T (2 sigma - 1), as a
+//           128 x d x (d + m) contraction per tile on the tensor cores, times norm 2^-E with 2^E >= every norm of the tile,
+//           so that f16 holds any norm; stored as the very shared-memory images the attention wants, 32 KB a tile;
+//   flash   softmax(scale q k^T) v over those tiles with the running maximum and sum of each row;
+//   merge   items that several CTAs shared.
+// Keys and values come back in the original basis, so queries and outputs need no rotation, and signs cost no wider
+// contraction: 4 d flops per (query row, key) for every format, where contracting the codes themselves would take
+// 2 (2 d + m_k + m_v). The f16 rows are written and read once through L2 (512 B per token and head at d = 128).
+//
+// Roundings: c[idx], Pi, S, rnorm / norm, x_hat, the prepared query (scaled by a power of two below 1) and the weights
+// to f16 (11 bits; outputs have 8 or 11); every sum, maximum and exponent in fp32.
+#pragma once
+
+#include <climits>
+
+#include "encode_tc.cuh"
+#include "paged_attn_simt.cuh"
+
+namespace tqk {
+namespace paged {
+
+using etc::bar_arrive;
+using etc::bulk_load;
+using etc::expect_tx;
+using etc::lds128;
+using etc::mma_commit;
+using etc::mma_f16;
+using etc::named_sync;
+using etc::sts128;
+using etc::sw128_desc;
+using etc::tc_fence_after;
+using etc::tc_fence_before;
+using etc::tmem_ld32;
+using etc::tmem_wait_ld;
+using etc::wait_bar;
+
+constexpr int kKT = 128;          // tokens of a key tile
+constexpr int kItemRows = 256;    // query rows of an item: two tiles of 128
+constexpr int kItemCost = 3;      // an item's fixed cost in key tiles (query preparation, epilogue)
+constexpr uint32_t kAtomRows = 128 * 128;   // 128 rows of 64 f16: one swizzle atom column
+
+// Plan, in the workspace (ints): what plan_kernel writes.
+struct Plan {
+  int* head;         // [0] key tiles, [1] items, [2] units of one head
+  int* tile_start;   // [B + 1] first key tile of a sequence
+  int* item_start;   // [B + 1] first item of a sequence
+  int* unit;         // [items + 1] running sum of the items' costs, within one head
+  int* ke;           // [heads of a round][max_tiles] exponents of key tiles
+  int* ve;           // ... of value tiles
+  uint32_t* seen;    // [max_tiles][4] tokens of the tile that exist and lie on a valid page
+  uint8_t* krows;    // [heads of a round][max_tiles] f16 key tiles
+  uint8_t* vrows;
+  float* part;       // [2 * CTAs][256 rows][d + 2] results of cut items
+  int max_tiles, max_items;
+};
+
+struct FlashArgs {
+  const void* q;
+  int64_t q_stride;
+  int q_dtype, Hq, Hkv, G, head0, heads;   // this round's KV heads: head0 .. head0 + heads - 1
+  Batch bt;
+  Prep prep;
+  Quant kq, vq;
+  CacheView kc, vc;
+  const uint8_t *kops, *vops;
+  float scale;
+  int causal, window, small_rows, ctas;
+  Plan p;
+  void* out;
+  int* err;
+};
+
+__device__ __forceinline__ int seq_rows(const FlashArgs& a, int b) {
+  const int n = seq_tokens(a.bt, b);
+  return n * a.G > a.small_rows ? n : 0;   // tokens of the sequences that come here
+}
+
+// Keys [lo, hi) of tokens i0 .. i1 of sequence b, of n.
+__device__ __forceinline__ void flash_range(const FlashArgs& a, int b, int i0, int i1, int n, int& lo, int& hi) {
+  key_range(a.bt, b, i0, i1, n, a.causal, a.window, lo, hi);
+}
+
+constexpr int kPlanThreads = 1024;
+
+// Exclusive running sum of v over the CTA, and the total.
+__device__ __forceinline__ int block_scan(int v, int* warp_s, int& total) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int incl = v;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  __syncthreads();
+  if (lane == 31) warp_s[warp] = incl;
+  __syncthreads();
+  if (warp == 0) {
+    int w = warp_s[lane];
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += u;
+    }
+    warp_s[lane] = w;
+  }
+  __syncthreads();
+  total = warp_s[31];
+  return incl - v + (warp ? warp_s[warp - 1] : 0);
+}
+
+// The last index i of start[0 .. n] with start[i] <= x, below n.
+__device__ __forceinline__ int last_at_or_before(const int* start, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (start[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(FlashArgs a) {
+  __shared__ int warp_s[32];
+  const int tid = threadIdx.x;
+  int tiles = 0, items = 0, total;
+  for (int b0 = 0; b0 < a.bt.B; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    int nt = 0, ni = 0;
+    if (b < a.bt.B) {
+      const int n = seq_rows(a, b);
+      if (n > 0) {
+        int lo, hi;
+        flash_range(a, b, 0, n - 1, n, lo, hi);
+        nt = hi > lo ? (hi + kKT - 1) / kKT - lo / kKT : 0;
+        ni = (n * a.G + kItemRows - 1) / kItemRows;
+      }
+    }
+    const int t = block_scan(nt, warp_s, total);
+    const int tiles_now = total;
+    const int i = block_scan(ni, warp_s, total);
+    if (b < a.bt.B) a.p.tile_start[b] = tiles + t, a.p.item_start[b] = items + i;
+    tiles += tiles_now, items += total;
+  }
+  if (tiles > a.p.max_tiles || items > a.p.max_items) {   // q_start is not ascending: nothing is computed
+    if (tid == 0) {
+      report_error(a.err, kErrPaged);
+      a.p.head[0] = a.p.head[1] = a.p.head[2] = 0;
+    }
+    return;
+  }
+  if (tid == 0) a.p.tile_start[a.bt.B] = tiles, a.p.item_start[a.bt.B] = items;
+  __syncthreads();
+  int units = 0;
+  for (int i0 = 0; i0 < items; i0 += kPlanThreads) {
+    const int i = i0 + tid;
+    int w = 0;
+    if (i < items) {
+      const int b = last_at_or_before(a.p.item_start, a.bt.B, i);
+      const int n = seq_rows(a, b), row0 = (i - a.p.item_start[b]) * kItemRows;
+      int lo, hi;
+      flash_range(a, b, row0 / a.G, (min(n * a.G, row0 + kItemRows) - 1) / a.G, n, lo, hi);
+      w = kItemCost + (hi > lo ? (hi + kKT - 1) / kKT - lo / kKT : 0);
+    }
+    const int u = block_scan(w, warp_s, total);
+    if (i < items) a.p.unit[i] = units + u;
+    units += total;
+  }
+  if (tid == 0) {
+    a.p.unit[items] = units;
+    a.p.head[0] = tiles, a.p.head[1] = items, a.p.head[2] = units;
+  }
+}
+
+// ---------------------------------------------------------------- expand
+
+constexpr int kExThreads = 288;   // warps 0-3 write operands, 4-7 read results, 8 issues
+
+template <int D>
+struct ExLayout {
+  static constexpr uint32_t kOpBytes = 2 * (D / 64) * D * 128;          // Pi^T and S^T, K-major
+  static constexpr uint32_t kAStage = 2 * (D / 64) * kAtomRows;         // operand rows of 128 tokens (codes, signs)
+  static constexpr uint32_t kA = kOpBytes;
+  static constexpr uint32_t kLut = kA + 2 * kAStage;                    // 32 KB
+  static constexpr uint32_t kScale = kLut + 32768;                      // float [2][128]
+  static constexpr uint32_t kBars = kScale + 1024;                      // op_full, a_full[2], a_empty[2], d_full[2], d_empty[2]
+  static constexpr uint32_t kMisc = kBars + 9 * 8;                      // tmem slot, abort, maxima[4]
+  static constexpr uint32_t kBytes = kMisc + 32;
+};
+static_assert(ExLayout<128>::kBytes <= 232448, "expand layout exceeds the shared memory of one CTA");
+
+// One token's packed row, loaded ahead.
+template <int D>
+struct Row {
+  uint32_t code[D / 8];   // 4 bits: all of them
+  uint32_t sign[D / 32];
+  float norm, ratio;      // ratio: what a sign weighs relative to the norm
+  bool ok;
+};
+
+template <int D>
+__device__ __forceinline__ void load_row(const Quant& Q, const CacheView& c, int64_t at, Row<D>& r) {
+  r.ok = at >= 0;
+  r.norm = 0.f, r.ratio = 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) r.code[i] = 0;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) r.sign[i] = 0;
+  if (at < 0) return;
+  r.norm = load_norm(c.norms, Q.norm_dtype, at);
+  const uint2* w = reinterpret_cast<const uint2*>(c.codes + at * Q.codes_B);   // rows are multiples of 8 bytes
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i)
+    if (8 * i < Q.codes_B) {
+      const uint2 v = __ldg(w + i);
+      r.code[2 * i] = v.x, r.code[2 * i + 1] = v.y;
+    }
+  if (Q.m > 0) {
+    const uint2* s = reinterpret_cast<const uint2*>(c.signs + at * Q.signs_B);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      const uint2 v = __ldg(s + i);
+      r.sign[2 * i] = v.x, r.sign[2 * i + 1] = v.y;
+    }
+    r.ratio = 1.f;
+    if (Q.bits > 0) r.ratio = r.norm != 0.f ? __half2float(c.rnorms[at]) / r.norm : 0.f;
+  }
+}
+
+// Table of f16 centroids for one packed byte (3 bits: for one pair of fields), a copy for each bank so that no two lanes
+// of a phase meet: 4 bits 4 B x 32 copies, 2 bits 8 B x 16, 1 bit 16 B x 8, 3 bits 64 pairs x 32.
+__device__ __forceinline__ void build_lut(const Quant& Q, uint8_t* lut, int tid, int nthreads) {
+  if (Q.bits == 0) return;
+  const double* c = Q.cent64();
+  const int per = Q.bits == 3 ? 2 : 8 / Q.bits, bytes = 2 * per, copies = 128 / bytes, n = Q.bits == 3 ? 64 : 256;
+  for (int e = tid; e < n * per; e += nthreads) {
+    const int v = e / per, i = e - v * per;
+    const __half h = __double2half(c[(v >> (i * Q.bits)) & ((1 << Q.bits) - 1)]);
+    for (int k = 0; k < copies; ++k) *reinterpret_cast<__half*>(lut + v * 128 + k * bytes + 2 * i) = h;
+  }
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+// (w >> 8 i & 255) * 128: byte i as a table offset
+__device__ __forceinline__ uint32_t byte128(uint32_t w, int i) { return ((i ? w >> (8 * i) : w) & 255u) << 7; }
+
+// Chunk c (8 coordinates, 16 bytes of f16) of a row's codes.
+template <int D>
+__device__ __forceinline__ uint4 code_chunk(const Row<D>& r, int bits, int c, uint32_t lut, int lane) {
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (bits == 4) {
+    const uint32_t w = r.code[c], b = lut + 4 * lane;
+    v = make_uint4(lds32(b + byte128(w, 0)), lds32(b + byte128(w, 1)), lds32(b + byte128(w, 2)), lds32(b + byte128(w, 3)));
+  } else if (bits == 2) {
+    const uint32_t w = r.code[c >> 1] >> (16 * (c & 1)), b = lut + 8 * (lane & 15);
+    const uint2 x = lds64(b + byte128(w, 0)), y = lds64(b + byte128(w, 1));
+    v = make_uint4(x.x, x.y, y.x, y.y);
+  } else if (bits == 1) {
+    v = lds128(lut + 16 * (lane & 7) + (((r.code[c >> 2] >> (8 * (c & 3))) & 255u) << 7));
+  } else if (bits == 3) {   // 24 bits from bit 24 c on
+    const int w0 = (24 * c) >> 5, sh = (24 * c) & 31;
+    const uint32_t x = __funnelshift_r(r.code[w0], r.code[min(w0 + 1, D / 8 - 1)], sh), b = lut + 4 * lane;
+    v = make_uint4(lds32(b + ((x & 63u) << 7)), lds32(b + ((x >> 6 & 63u) << 7)), lds32(b + ((x >> 12 & 63u) << 7)),
+                   lds32(b + ((x >> 18 & 63u) << 7)));
+  }
+  return v;
+}
+
+// Places 8 c .. 8 c + 7 of a row's signs: place 32 u + 2 i holds the sign of projection 32 u + i, place 32 u + 2 i + 1 that
+// of 32 u + 16 + i (one shift and one mask give both halves of a word); the rows of S^T in the operand follow that order.
+template <int D>
+__device__ __forceinline__ uint4 sign_chunk(const Row<D>& r, int c, uint32_t ratio2) {
+  const uint32_t w = ~r.sign[c >> 2];
+  const int i = 4 * (c & 3);
+  auto two = [&](int k) { return ((k < 16 ? w << (15 - k) : 0u) & 0x80008000u) ^ ratio2; };
+  return make_uint4(two(i), two(i + 1), two(i + 2), two(i + 3));
+}
+
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+  asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+}
+__device__ __forceinline__ void bulk_store_read_wait() { asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory"); }
+__device__ __forceinline__ void bulk_store_wait() { asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// f16 x f16, fp32 sums, M = 128; bn: B is MN-major (its N runs along the bytes)
+__host__ __device__ constexpr uint32_t flash_idesc(int N, bool bn) {
+  return (1u << 4) | (bn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+// Grid: 2 x CTAs; even CTAs keys, odd CTAs values; CTA j of a kind takes (head, tile) pairs j, j + n, ...
+template <int D>
+__global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a) {
+  using L = ExLayout<D>;
+  extern __shared__ __align__(1024) unsigned char smem_tiles[];
+  unsigned char* const smem = smem_tiles;
+  const uint32_t base = smem_addr(smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int kind = blockIdx.x & 1, j0 = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const Quant& Q = kind ? a.vq : a.kq;
+  const CacheView& C = kind ? a.vc : a.kc;
+  const int tiles = a.p.head[0], work = tiles * a.heads;
+  const int mine = work > j0 ? (work - j0 + step - 1) / step : 0;
+  const uint32_t bars = base + L::kBars;
+  const uint32_t op_full = bars;
+  auto a_full = [&](int s) { return bars + 8u * (1 + s); };
+  auto a_empty = [&](int s) { return bars + 8u * (3 + s); };
+  auto d_full = [&](int s) { return bars + 8u * (5 + s); };
+  auto d_empty = [&](int s) { return bars + 8u * (7 + s); };
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
+  float* maxima = reinterpret_cast<float*>(smem + L::kMisc + 8);   // [4]
+  float* scale_s = reinterpret_cast<float*>(smem + L::kScale);
+  if ((base & 1023u) != 0) {
+    if (tid == 0) report_error(a.err, kErrInternal);
+    return;
+  }
+  if (mine == 0) return;
+  if (tid == 0) {
+    *abort_flag = 0;
+    uint64_t* b = reinterpret_cast<uint64_t*>(smem + L::kBars);
+    bar_init(b, 1);
+    for (int s = 0; s < 2; ++s) bar_init(b + 1 + s, 4), bar_init(b + 3 + s, 1), bar_init(b + 5 + s, 1), bar_init(b + 7 + s, 4);
+  }
+  build_lut(Q, smem + L::kLut, tid, kExThreads);
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(base + L::kMisc), "r"(256u) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    if (*abort_flag || wait_bar(bar, parity)) return;
+    *abort_flag = 1;
+    report_error(a.err, kErrTimeout);
+  };
+  const int katoms = (D + Q.m) / 64;   // 64-wide slices of the contraction
+
+  if (warp < 4) {
+    // ---- operand rows: thread = token of the tile
+    auto place = [&](int i, int& b, int& tile, int& h) -> int64_t {
+      const int w = j0 + i * step;
+      h = w / tiles, tile = w - h * tiles;
+      b = last_at_or_before(a.p.tile_start, a.bt.B, tile);
+      const int n = seq_rows(a, b);
+      int lo, hi;
+      flash_range(a, b, 0, n - 1, n, lo, hi);
+      const int p = (lo / kKT + tile - a.p.tile_start[b]) * kKT + tid;
+      if (p >= hi) return -2;
+      return place_of(a.bt, b, p, a.head0 + h, a.Hkv);
+    };
+    int b, tile, h, nb, ntile, nh;
+    Row<D> cur, nxt;
+    int64_t at = place(0, nb, ntile, nh);
+    load_row<D>(Q, C, at, nxt);
+    for (int i = 0; i < mine; ++i) {
+      const int s = i & 1;
+      cur = nxt, b = nb, tile = ntile, h = nh;
+      const int64_t here = at;
+      if (i + 1 < mine) {
+        at = place(i + 1, nb, ntile, nh);
+        load_row<D>(Q, C, at, nxt);
+      }
+      if (here == -1) report_error(a.err, kErrPaged);
+      const unsigned there = __ballot_sync(0xffffffffu, cur.ok);
+      if (kind == 0 && h == 0 && lane == 0) a.p.seen[4 * tile + warp] = there;
+      // the tile's exponent: 2^E >= every finite norm
+      const float fin = fabsf(cur.norm) < INFINITY ? fabsf(cur.norm) : 0.f;
+      float top = fin;
+      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (lane == 0) maxima[warp] = top;
+      named_sync(1, 128);
+      top = fmaxf(fmaxf(maxima[0], maxima[1]), fmaxf(maxima[2], maxima[3]));
+      int e = -126;
+      if (top > 0.f) frexpf(top, &e);
+      e = max(-126, min(126, e));
+      named_sync(1, 128);
+      if (i >= 2) wait(a_empty(s), ((i >> 1) - 1) & 1);
+      scale_s[s * 128 + tid] = cur.ok ? ldexpf(cur.norm, -e) : 0.f;
+      if (tid == 0) (kind ? a.p.ve : a.p.ke)[(int64_t)h * a.p.max_tiles + tile] = e;
+      const uint32_t row = base + L::kA + s * L::kAStage + tid * 128;
+      if (Q.bits > 0) {
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = code_chunk<D>(cur, Q.bits, c, base + L::kLut, lane);
+          sts128(row + (c >> 3) * kAtomRows + (((c & 7) ^ (tid & 7)) << 4), v.x, v.y, v.z, v.w);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) sts128(row + (c >> 3) * kAtomRows + (((c & 7) ^ (tid & 7)) << 4), 0, 0, 0, 0);
+      }
+      if (Q.m > 0) {
+        const uint32_t r2 = half2_bits(cur.ratio, cur.ratio);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = sign_chunk<D>(cur, c, r2);
+          sts128(row + (D / 64 + (c >> 3)) * kAtomRows + (((c & 7) ^ (tid & 7)) << 4), v.x, v.y, v.z, v.w);
+        }
+      }
+      fence_async();
+      __syncwarp();
+      if (lane == 0) bar_arrive(a_full(s));
+    }
+  } else if (warp < 8) {
+    // ---- results: thread = token; the row goes out through the operand stage that produced it
+    const int r = tid - 128;
+    for (int i = 0; i < mine; ++i) {
+      const int s = i & 1;
+      const int w = j0 + i * step, h = w / tiles, tile = w - h * tiles;
+      wait(d_full(s), (i >> 1) & 1);
+      tc_fence_after();
+      const float f = scale_s[s * 128 + r];
+      const uint32_t row = base + L::kA + s * L::kAStage + r * 128;
+#pragma unroll 1
+      for (int c4 = 0; c4 < D / 32; ++c4) {
+        uint32_t v[32];
+        tmem_ld32(tmem + s * 128 + ((uint32_t)((warp & 3) * 32) << 16), v, 32 * c4);
+        tmem_wait_ld(v);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t o[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            o[x] = half2_bits(__uint_as_float(v[8 * k + 2 * x]) * f, __uint_as_float(v[8 * k + 2 * x + 1]) * f);
+          const int c = 4 * c4 + k;
+          sts128(row + (c >> 3) * kAtomRows + (((c & 7) ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
+        }
+      }
+      tc_fence_before();
+      fence_async();
+      named_sync(2, 128);
+      if (r == 0) {
+        const uint32_t bytes = (D / 64) * kAtomRows;
+        uint8_t* dst = (kind ? a.p.vrows : a.p.krows) + ((int64_t)h * a.p.max_tiles + tile) * bytes;
+        bulk_store(dst, base + L::kA + s * L::kAStage, bytes);
+        bulk_store_read_wait();
+        bar_arrive(a_empty(s));
+      }
+      if (lane == 0) bar_arrive(d_empty(s));
+    }
+    if (r == 0) bulk_store_wait();
+  } else if (lane == 0) {
+    // ---- contraction
+    const uint32_t atom_op = D * 128;
+    expect_tx(op_full, katoms * atom_op);
+    for (int k = 0; k < katoms; ++k) bulk_load(base + k * atom_op, (kind ? a.vops : a.kops) + k * atom_op, atom_op, op_full);
+    wait(op_full, 0);
+    for (int i = 0; i < mine; ++i) {
+      const int s = i & 1;
+      wait(a_full(s), (i >> 1) & 1);
+      if (i >= 2) wait(d_empty(s), ((i >> 1) - 1) & 1);
+      tc_fence_after();
+      for (int k = 0; k < katoms; ++k)
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_f16(tmem + s * 128, sw128_desc(base + L::kA + s * L::kAStage + k * kAtomRows + kk * 32),
+                  sw128_desc(base + k * atom_op + kk * 32), flash_idesc(D, false), (k | kk) > 0 ? 1u : 0u);
+      mma_commit(d_full(s));
+    }
+    // tensor memory is released below: the last contractions must have ended
+    for (int i = max(0, mine - 2); i < mine; ++i) (void)wait_bar(d_full(i & 1), (i >> 1) & 1);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(256u) : "memory");
+}
+
+// ---------------------------------------------------------------- flash
+
+// Warps 0-3 and 4-7: softmax of query tile 0 and 1 (thread = row); 8: copies; 9: MMAs.
+constexpr int kFlThreads = 320;
+constexpr int kFlStages = 4;      // ring of key and value tiles, in the order K0 V0 K1 V1 ...
+
+template <int D>
+struct FlLayout {
+  static constexpr uint32_t kTile = (D / 64) * kAtomRows;   // 32 KB: 128 rows of D f16
+  static constexpr uint32_t kQ = 0;                         // two query tiles
+  static constexpr uint32_t kRing = 2 * kTile;
+  static constexpr uint32_t kBars = kRing + kFlStages * kTile;
+  // full[4], empty[4], q_full[2], s_full[2], p_full[2], pv_done[2], o_free[2]
+  static constexpr int kNumBars = 2 * kFlStages + 10;
+  static constexpr uint32_t kMisc = kBars + 8 * kNumBars;
+  static constexpr uint32_t kBytes = kMisc + 16;
+};
+static_assert(FlLayout<128>::kBytes <= 232448, "flash layout exceeds the shared memory of one CTA");
+
+// MN-major operand (N along the 128-byte rows, one row per K index): blocks of 64 N are kAtomRows apart, groups of 8 K
+// indices 1024 bytes.
+__device__ __forceinline__ uint64_t mn_desc16(uint32_t saddr) {
+  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(kAtomRows >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// A in tensor memory (lane = row, 8 columns of two f16 per 16 K).
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc));
+}
+
+// CTA c of P takes units [c U / P, (c + 1) U / P) of the round's U = heads * units, head by head, item by item.
+struct Span {
+  int64_t u0, u1;
+};
+__device__ __forceinline__ Span span_of(int64_t U, int c, int P) { return {U * c / P, U * (c + 1) / P}; }
+
+// A CTA's share of one item: key tiles [t0, t1) of nt.
+struct Segment {
+  int h, item, b, n, row0, nrows, lo_tile, nt, t0, t1;
+  int64_t next;   // first unit after the item
+  int64_t first;  // first unit of the item
+};
+__device__ __forceinline__ Segment segment_at(const FlashArgs& a, int items, int units, int64_t u, int64_t u1) {
+  Segment s;
+  s.h = (int)(u / units);
+  const int r = (int)(u - (int64_t)s.h * units);
+  s.item = last_at_or_before(a.p.unit, items, r);
+  s.first = (int64_t)s.h * units + a.p.unit[s.item];
+  s.next = (int64_t)s.h * units + a.p.unit[s.item + 1];
+  s.b = last_at_or_before(a.p.item_start, a.bt.B, s.item);
+  s.n = seq_rows(a, s.b);
+  s.row0 = (s.item - a.p.item_start[s.b]) * kItemRows;
+  s.nrows = min(kItemRows, s.n * a.G - s.row0);
+  int lo, hi, lo_all, hi_all;
+  flash_range(a, s.b, s.row0 / a.G, (s.row0 + s.nrows - 1) / a.G, s.n, lo, hi);
+  flash_range(a, s.b, 0, s.n - 1, s.n, lo_all, hi_all);
+  (void)hi_all;
+  s.nt = (int)(s.next - s.first) - kItemCost;
+  s.lo_tile = lo / kKT - lo_all / kKT;   // relative to the sequence's first tile
+  s.t0 = max(0, (int)(u - s.first) - kItemCost);
+  s.t1 = max(0, (int)(min(u1, s.next) - s.first) - kItemCost);
+  return s;
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(taddr), "r"(v[0]),
+      "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]),
+      "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a) {
+  using L = FlLayout<D>;
+  extern __shared__ __align__(1024) unsigned char smem_tiles[];
+  unsigned char* const smem = smem_tiles;
+  const uint32_t base = smem_addr(smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int items = a.p.head[1], units = a.p.head[2];
+  const Span sp = span_of((int64_t)units * a.heads, blockIdx.x, gridDim.x);
+  if ((base & 1023u) != 0) {
+    if (tid == 0) report_error(a.err, kErrInternal);
+    return;
+  }
+  if (sp.u0 >= sp.u1) return;
+  const uint32_t bars = base + L::kBars;
+  auto full = [&](int s) { return bars + 8u * s; };
+  auto empty = [&](int s) { return bars + 8u * (kFlStages + s); };
+  auto q_full = [&](int i) { return bars + 8u * (2 * kFlStages + i); };
+  auto s_full = [&](int i) { return bars + 8u * (2 * kFlStages + 2 + i); };
+  auto p_full = [&](int i) { return bars + 8u * (2 * kFlStages + 4 + i); };
+  auto pv_done = [&](int i) { return bars + 8u * (2 * kFlStages + 6 + i); };
+  auto o_free = [&](int i) { return bars + 8u * (2 * kFlStages + 8 + i); };
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
+  if (tid == 0) {
+    *abort_flag = 0;
+    uint64_t* b = reinterpret_cast<uint64_t*>(smem + L::kBars);
+    for (int s = 0; s < 2 * kFlStages; ++s) bar_init(b + s, 1);
+    for (int i = 0; i < 2; ++i) {
+      bar_init(b + 2 * kFlStages + i, 4);       // q_full: the tile's four warps
+      bar_init(b + 2 * kFlStages + 2 + i, 1);   // s_full: commit
+      bar_init(b + 2 * kFlStages + 4 + i, 4);   // p_full: four warps
+      bar_init(b + 2 * kFlStages + 6 + i, 1);   // pv_done: commit
+      bar_init(b + 2 * kFlStages + 8 + i, 4);   // o_free: four warps
+    }
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(base + L::kMisc), "r"(512u) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t col_s[2] = {tmem, tmem + 128}, col_o[2] = {tmem + 256, tmem + 384};
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    if (*abort_flag || wait_bar(bar, parity)) return;
+    *abort_flag = 1;
+    report_error(a.err, kErrTimeout);
+  };
+
+  if (warp == 8) {
+    if (lane == 0) {
+      int k = 0;   // tiles issued, keys and values counted apart
+      for (int64_t u = sp.u0; u < sp.u1;) {
+        const Segment s = segment_at(a, items, units, u, sp.u1);
+        u = s.next;
+        const int64_t t = (int64_t)s.h * a.p.max_tiles + a.p.tile_start[s.b] + s.lo_tile;
+        for (int j = s.t0; j < s.t1; ++j)
+          for (int kv = 0; kv < 2; ++kv, ++k) {
+            const int st = k % kFlStages;
+            if (k >= kFlStages) wait(empty(st), (k / kFlStages - 1) & 1);
+            if (*abort_flag) break;
+            expect_tx(full(st), L::kTile);
+            bulk_load(base + L::kRing + st * L::kTile, (kv ? a.p.vrows : a.p.krows) + (t + j) * L::kTile, L::kTile, full(st));
+          }
+        if (*abort_flag) break;
+      }
+      // never leave with a copy still landing in this CTA's shared memory
+      for (int i = max(0, k - kFlStages); i < k; ++i) (void)wait_bar(full(i % kFlStages), (i / kFlStages) & 1);
+    }
+  } else if (warp == 9) {
+    if (lane == 0) {
+      int k = 0, seg = 0, tile = 0;   // ring position, segments with tiles, tiles
+      for (int64_t u = sp.u0; u < sp.u1;) {
+        const Segment s = segment_at(a, items, units, u, sp.u1);
+        u = s.next;
+        const int nt = s.t1 - s.t0;
+        if (nt <= 0) continue;
+        auto scores = [&](int i, int kk) {   // S_i = Q_i K^T
+          const int st = kk % kFlStages;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c)
+            mma_f16(col_s[i], sw128_desc(base + L::kQ + i * L::kTile + (c >> 2) * kAtomRows + (c & 3) * 32),
+                    sw128_desc(base + L::kRing + st * L::kTile + (c >> 2) * kAtomRows + (c & 3) * 32), flash_idesc(128, false),
+                    c > 0 ? 1u : 0u);
+          mma_commit(s_full(i));
+        };
+        for (int i = 0; i < 2; ++i) {
+          wait(q_full(i), seg & 1);
+          if (i == 0) wait(full(k % kFlStages), (k / kFlStages) & 1);
+          tc_fence_after();
+          scores(i, k);
+        }
+        mma_commit(empty(k % kFlStages));
+        for (int j = 0; j < nt; ++j, k += 2, ++tile) {
+          const int vs = (k + 1) % kFlStages;
+          for (int i = 0; i < 2; ++i) {
+            if (i == 0) wait(full(vs), ((k + 1) / kFlStages) & 1);
+            if (j == 0 && seg > 0) wait(o_free(i), (seg - 1) & 1);
+            wait(p_full(i), tile & 1);
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < 8; ++c)   // 16 tokens at a time
+              mma_f16_ts(col_o[i], col_s[i] + 8 * c, mn_desc16(base + L::kRing + vs * L::kTile + c * 2048), flash_idesc(D, true),
+                         (j | c) > 0 ? 1u : 0u);
+            mma_commit(pv_done(i));
+            if (i == 1) mma_commit(empty(vs));
+            if (j + 1 < nt) {
+              if (i == 0) {
+                wait(full((k + 2) % kFlStages), ((k + 2) / kFlStages) & 1);
+                tc_fence_after();
+              }
+              scores(i, k + 2);
+              if (i == 1) mma_commit(empty((k + 2) % kFlStages));
+            }
+          }
+        }
+        ++seg;
+      }
+      // tensor memory is released below: the last contractions must have ended
+      if (tile > 0)
+        for (int i = 0; i < 2; ++i) (void)wait_bar(pv_done(i), (tile - 1) & 1);
+    }
+  } else {
+    // ---- softmax: thread = query row
+    const int i = warp >> 2, r = tid & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t cs = col_s[i] + lanes, co = col_o[i] + lanes;
+    int tile = 0;   // tiles of this CTA so far
+    for (int64_t u = sp.u0; u < sp.u1;) {
+      const Segment s = segment_at(a, items, units, u, sp.u1);
+      const bool first_unit = u == s.first;
+      u = s.next;
+      const int nt = s.t1 - s.t0;
+      const int row = s.row0 + 128 * i + r;
+      const bool live = 128 * i + r < s.nrows;
+      const int tok = live ? row / a.G : 0, g = live ? row - tok * a.G : 0;
+      const int64_t t = (int64_t)a.bt.q_start[s.b] + tok;
+      const int hq = (a.head0 + s.h) * a.G + g;
+      const int64_t oat = (t * a.Hq + hq) * D;
+      if (nt <= 0) {
+        if (s.nt == 0 && first_unit && live) {   // no key at all
+          uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + oat);
+          for (int c = 0; c < D / 8; ++c) o[c] = make_uint4(0, 0, 0, 0);
+        }
+        continue;
+      }
+      const int len = max(0, a.bt.len[s.b]), cap = (int)min((int64_t)len, (int64_t)a.bt.max_pages * a.bt.page_size);
+      const int pos = a.bt.len[s.b] - s.n + tok;
+      int lo = 0, hi = live ? cap : 0;   // keys this row sees
+      if (a.causal) {
+        hi = min(hi, pos + 1);
+        if (a.window > 0) lo = max(0, pos - a.window + 1);
+      }
+      // ---- the query: norm, rotation, then times 2^-e below one, to f16
+      float qscale = 0.f;
+      {
+        const uint32_t qrow = base + L::kQ + i * L::kTile + r * 128;
+        bool ok = live;
+        int64_t rp = 0;
+        if (live && a.prep.cos_sin) {
+          rp = a.prep.pos ? (int64_t)a.prep.pos[t] : (int64_t)pos;
+          if (rp < 0 || rp >= a.prep.max_pos) {
+            if (a.prep.pos || rp >= 0) report_error(a.err, kErrPaged);
+            ok = false, hi = 0;
+          }
+        }
+        uint4 raw[D / 8];
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + t * a.q_stride + (int64_t)hq * D);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) raw[c] = ok ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+        const bool f16 = a.q_dtype == TQ_F16;
+        auto get = [&](int x) -> float2 {   // coordinates 2 x, 2 x + 1
+          const uint32_t w = (&raw[x >> 2].x)[x & 3];
+          return f16 ? etc::pair_to_float2<true>(w) : etc::pair_to_float2<false>(w);
+        };
+        float rms = 1.f, ss = 0.f;
+#pragma unroll
+        for (int x = 0; x < D / 2; ++x) {
+          const float2 v = get(x);
+          ss = fmaf(v.x, v.x, fmaf(v.y, v.y, ss));
+        }
+        if (a.prep.weight) {
+          rms = rsqrtf(ss / (float)D + a.prep.eps);
+          ss = 0.f;
+#pragma unroll
+          for (int x = 0; x < D / 2; ++x) {
+            const float2 v = get(x);
+            const float y0 = v.x * rms * load_any(a.prep.weight, a.prep.weight_dtype, 2 * x);
+            const float y1 = v.y * rms * load_any(a.prep.weight, a.prep.weight_dtype, 2 * x + 1);
+            ss = fmaf(y0, y0, fmaf(y1, y1, ss));
+          }
+        }
+        // |q_i| <= |q|: the largest power of two that brings all of them below one
+        int e = 0;
+        const float nq = sqrtf(ss);
+        if (nq > 0.f && nq < INFINITY) frexpf(nq, &e);
+        const float sc = a.scale < 0.f ? -ldexpf(1.f, -e) : ldexpf(1.f, -e);
+        qscale = ldexpf(fabsf(a.scale) * 1.44269504089f, e);
+        const int rot = a.prep.cos_sin ? a.prep.rot_dim : 0, half = rot >> 1;
+        const float* cs_row = a.prep.cos_sin + rp * rot;
+        auto at = [&](int x) -> float2 {
+          float2 v = get(x);
+          if (a.prep.weight) {
+            v.x *= rms * load_any(a.prep.weight, a.prep.weight_dtype, 2 * x);
+            v.y *= rms * load_any(a.prep.weight, a.prep.weight_dtype, 2 * x + 1);
+          }
+          return v;
+        };
+        auto put = [&](int c, const uint32_t (&o)[4]) {   // 16-byte chunk c of the row
+          sts128(qrow + (c >> 3) * kAtomRows + (((c & 7) ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
+        };
+        if (!ok) {
+          const uint32_t z[4] = {0, 0, 0, 0};
+          for (int c = 0; c < D / 8; ++c) put(c, z);
+        } else if (rot == D && !a.prep.interleaved) {
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t o1[4], o2[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const float2 p = at(4 * c + x), w = at(4 * c + x + D / 4);
+              const float2 co2 = *reinterpret_cast<const float2*>(cs_row + 8 * c + 2 * x);
+              const float2 si2 = *reinterpret_cast<const float2*>(cs_row + D / 2 + 8 * c + 2 * x);
+              o1[x] = half2_bits((p.x * co2.x - w.x * si2.x) * sc, (p.y * co2.y - w.y * si2.y) * sc);
+              o2[x] = half2_bits((w.x * co2.x + p.x * si2.x) * sc, (w.y * co2.y + p.y * si2.y) * sc);
+            }
+            put(c, o1);
+            put(c + D / 16, o2);
+          }
+        } else {
+          // any other rotation, pair by pair: the partner of a pair of coordinates is read again from memory
+          const uint16_t* q16 = reinterpret_cast<const uint16_t*>(src);
+          auto one = [&](int x) {
+            float v = load_any(q16, a.q_dtype, x);
+            if (a.prep.weight) v *= rms * load_any(a.prep.weight, a.prep.weight_dtype, x);
+            return v;
+          };
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            uint32_t o[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              float2 v = at(4 * c + x);
+              const int k = 8 * c + 2 * x;
+              if (k < rot) {
+                if (a.prep.interleaved) {
+                  const float co1 = cs_row[k >> 1], si1 = cs_row[half + (k >> 1)];
+                  v = make_float2(v.x * co1 - v.y * si1, v.y * co1 + v.x * si1);
+                } else {
+                  const int kk = k < half ? k : k - half;
+                  const float sg = k < half ? -1.f : 1.f;
+                  const int other = k < half ? k + half : k - half;
+                  v = make_float2(v.x * cs_row[kk] + sg * one(other) * cs_row[half + kk],
+                                  v.y * cs_row[kk + 1] + sg * one(other + 1) * cs_row[half + kk + 1]);
+                }
+              }
+              o[x] = half2_bits(v.x * sc, v.y * sc);
+            }
+            put(c, o);
+          }
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) bar_arrive(q_full(i));
+      }
+      // ---- key tiles
+      const int tile0 = a.p.tile_start[s.b] + s.lo_tile;
+      const int64_t te = (int64_t)s.h * a.p.max_tiles + tile0;
+      int lo_all, hi_all;
+      flash_range(a, s.b, 0, s.n - 1, s.n, lo_all, hi_all);
+      const int key_first = (lo_all / kKT + s.lo_tile) * kKT;
+      float m = -INFINITY, l = 0.f;   // running reference (log2) and sum of weights
+      int vref = 0;                   // the value sums are in units of 2^vref
+      int ke = a.p.ke[te + s.t0], ve = a.p.ve[te + s.t0];
+      uint4 seen = *reinterpret_cast<const uint4*>(a.p.seen + 4 * (tile0 + s.t0));
+      for (int j = s.t0; j < s.t1; ++j, ++tile) {
+        const float c = qscale * exp2f((float)ke);
+        // value tiles come in units of 2^ve: their weights take the difference along. The unit moves up when a tile would
+        // bring weights above 2^(8 + 4); a tile 2^100 below it keeps its place in the sum of weights and adds nothing.
+        const int vnow = j == s.t0 || ve > vref + 4 ? ve : vref;
+        const float fv = exp2f((float)max(j == s.t0 ? 0 : vref - vnow, -126));
+        vref = vnow;
+        const float dv = (float)max(ve - vref, -100);
+        const uint4 there = seen;
+        if (j + 1 < s.t1) {
+          ke = a.p.ke[te + j + 1], ve = a.p.ve[te + j + 1];
+          seen = *reinterpret_cast<const uint4*>(a.p.seen + 4 * (tile0 + j + 1));
+        }
+        const int k0 = key_first + j * kKT;
+        const bool whole = (there.x & there.y & there.z & there.w) == 0xffffffffu && k0 >= lo && k0 + kKT <= hi;
+        const bool masked = __any_sync(0xffffffffu, !whole);
+        wait(s_full(i), tile & 1);
+        tc_fence_after();
+        float mx = -INFINITY;
+        auto mask_of = [&](int q4) -> uint32_t {   // keys 32 q4 .. of the tile this row sees
+          const uint32_t w = q4 == 0 ? there.x : q4 == 1 ? there.y : q4 == 2 ? there.z : there.w;
+          const int f = k0 + 32 * q4, lo1 = min(max(lo - f, 0), 32), hi1 = min(max(hi - f, 0), 32);
+          const uint32_t below = hi1 >= 32 ? 0xffffffffu : (1u << hi1) - 1u;
+          const uint32_t from = lo1 >= 32 ? 0u : 0xffffffffu << lo1;
+          return w & below & from;
+        };
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) {
+          uint32_t v[32];
+          tmem_ld32(cs, v, 32 * q4);
+          tmem_wait_ld(v);
+          if (masked) {
+            const uint32_t ok = mask_of(q4);
+#pragma unroll
+            for (int x = 0; x < 32; ++x) mx = fmaxf(mx, ok >> x & 1 ? __uint_as_float(v[x]) : -INFINITY);
+          } else {
+#pragma unroll
+            for (int x = 0; x < 32; x += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(v[x]), __uint_as_float(v[x + 1])));
+          }
+        }
+        const float top = mx == -INFINITY ? -INFINITY : mx * c;
+        // the reference moves only when a score exceeds it by 2^8: weights stay below 256, and the sums above are rarely scaled
+        const bool move = top > m + 8.f;
+        if (__any_sync(0xffffffffu, move || fv != 1.f)) {
+          float f = !move ? 1.f : m == -INFINITY ? 0.f : exp2f(m - top);
+          if (move) m = top;
+          l *= f;
+          f *= fv;
+          if (j > s.t0) {
+            wait(pv_done(i), (tile - 1) & 1);
+            tc_fence_after();
+#pragma unroll 1
+            for (int q4 = 0; q4 < D / 32; ++q4) {
+              uint32_t v[32];
+              tmem_ld32(co, v, 32 * q4);
+              tmem_wait_ld(v);
+#pragma unroll
+              for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * f);
+              tmem_st16(co + 32 * q4, v);
+              tmem_st16(co + 32 * q4 + 16, v + 16);
+            }
+          }
+        }
+        const float ref = (m == -INFINITY ? 0.f : m) - dv;   // weights come out times 2^(E - reference exponent)
+        float sum = 0.f;
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) {
+          uint32_t v[32], p[16];
+          tmem_ld32(cs, v, 32 * q4);
+          tmem_wait_ld(v);
+          const uint32_t ok = masked ? mask_of(q4) : 0xffffffffu;
+#pragma unroll
+          for (int x = 0; x < 32; x += 2) {
+            float p0 = exp2f(fmaf(__uint_as_float(v[x]), c, -ref)), p1 = exp2f(fmaf(__uint_as_float(v[x + 1]), c, -ref));
+            if (masked) {
+              p0 = ok >> x & 1 ? p0 : 0.f;
+              p1 = ok >> (x + 1) & 1 ? p1 : 0.f;
+            }
+            sum += p0 + p1;
+            p[x >> 1] = half2_bits(p0, p1);
+          }
+          // the weights of 32 keys take 16 of the 32 columns their scores held; nothing read later is overwritten
+          tmem_st16(cs + 16 * q4, p);
+        }
+        etc::tmem_wait_st();
+        l = fmaf(sum, exp2f(-dv), l);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(p_full(i));
+      }
+      // ---- results
+      wait(pv_done(i), (tile - 1) & 1);
+      tc_fence_after();
+      const bool cut = s.t0 > 0 || s.t1 < s.nt;
+      const float up = exp2f((float)vref);
+      if (!cut) {
+        const float f = l > 0.f ? up / l : 0.f;
+        uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + oat);
+#pragma unroll 1
+        for (int q4 = 0; q4 < D / 32; ++q4) {
+          uint32_t v[32];
+          tmem_ld32(co, v, 32 * q4);
+          tmem_wait_ld(v);
+          if (live)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t w[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const float y0 = __uint_as_float(v[8 * k + 2 * x]) * f, y1 = __uint_as_float(v[8 * k + 2 * x + 1]) * f;
+                w[x] = a.q_dtype == TQ_F16 ? half2_bits(y0, y1) : etc::bf16x2_bits(y0, y1);
+              }
+              o[4 * q4 + k] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+      } else {
+        // slot 2 c: the item began before this CTA; 2 c + 1: it goes on behind it
+        float4* part = reinterpret_cast<float4*>(a.p.part) + (int64_t)(2 * blockIdx.x + (s.t0 == 0 ? 1 : 0)) * (D / 4 + 1) * kItemRows;
+#pragma unroll 1
+        for (int q4 = 0; q4 < D / 32; ++q4) {
+          uint32_t v[32];
+          tmem_ld32(co, v, 32 * q4);
+          tmem_wait_ld(v);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            part[(8 * q4 + k) * kItemRows + 128 * i + r] =
+                make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]), __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]));
+        }
+        part[(D / 4) * kItemRows + 128 * i + r] = make_float4(m, l, up, 0.f);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(o_free(i));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512u) : "memory");
+}
+
+// Grid: (CTAs of flash, D / 16): an item that begins in CTA c and goes on behind it; thread = row, 16 coordinates per CTA.
+template <int D>
+__global__ void __launch_bounds__(kItemRows) paged_flash_merge_kernel(FlashArgs a) {
+  const int c = blockIdx.x, P = a.ctas, r = threadIdx.x;
+  const int items = a.p.head[1], units = a.p.head[2];
+  const int64_t U = (int64_t)units * a.heads;
+  const Span sp = span_of(U, c, P);
+  if (sp.u0 >= sp.u1) return;
+  const Segment s = segment_at(a, items, units, sp.u1 - 1, sp.u1);
+  if (s.first < sp.u0 || s.next <= sp.u1) return;   // began earlier, or ends here
+  if (r >= s.nrows) return;
+  const float4* part = reinterpret_cast<const float4*>(a.p.part);
+  constexpr int kSlot = (D / 4 + 1) * kItemRows;
+  float M = -INFINITY;
+  int slots = 0;
+  for (int e = c; e < P; ++e) {
+    const Span q = span_of(U, e, P);
+    if (q.u0 >= s.next) break;
+    const int t0 = max(0, (int)(max(q.u0, s.first) - s.first) - kItemCost), t1 = max(0, (int)(min(q.u1, s.next) - s.first) - kItemCost);
+    if (t1 <= t0) continue;
+    if (t0 == 0 && t1 == s.nt) return;   // one CTA had all of its tiles and wrote the result
+    M = fmaxf(M, part[(int64_t)(2 * e + (t0 == 0 ? 1 : 0)) * kSlot + (D / 4) * kItemRows + r].x);
+    ++slots;
+  }
+  if (slots == 0) return;
+  float acc[16], l = 0.f;
+#pragma unroll
+  for (int x = 0; x < 16; ++x) acc[x] = 0.f;
+  for (int e = c; e < P; ++e) {
+    const Span q = span_of(U, e, P);
+    if (q.u0 >= s.next) break;
+    const int t0 = max(0, (int)(max(q.u0, s.first) - s.first) - kItemCost), t1 = max(0, (int)(min(q.u1, s.next) - s.first) - kItemCost);
+    if (t1 <= t0) continue;
+    const float4* p = part + (int64_t)(2 * e + (t0 == 0 ? 1 : 0)) * kSlot;
+    const float4 st = p[(D / 4) * kItemRows + r];
+    const float w = st.x == -INFINITY ? 0.f : exp2f(st.x - M);
+    l = fmaf(w, st.y, l);
+    const float wv = w * st.z;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 v = p[(4 * blockIdx.y + k) * kItemRows + r];
+      acc[4 * k] = fmaf(wv, v.x, acc[4 * k]), acc[4 * k + 1] = fmaf(wv, v.y, acc[4 * k + 1]);
+      acc[4 * k + 2] = fmaf(wv, v.z, acc[4 * k + 2]), acc[4 * k + 3] = fmaf(wv, v.w, acc[4 * k + 3]);
+    }
+  }
+  const float f = l > 0.f ? 1.f / l : 0.f;
+  const int row = s.row0 + r, tok = row / a.G, hq = (a.head0 + s.h) * a.G + row - tok * a.G;
+  uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (((int64_t)a.bt.q_start[s.b] + tok) * a.Hq + hq) * D + 16 * blockIdx.y);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    uint32_t w[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const float y0 = acc[8 * k + 2 * x] * f, y1 = acc[8 * k + 2 * x + 1] * f;
+      w[x] = a.q_dtype == TQ_F16 ? half2_bits(y0, y1) : etc::bf16x2_bits(y0, y1);
+    }
+    o[k] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+}  // namespace paged
+}  // namespace tqk

@@ -338,6 +338,19 @@ int create_common(int d, int bits_mse, int m, uint64_t seed, int norm_dtype, tq_
   // paged operators: fp64 Pi, S, M, then 16 boundaries (padded with +inf) and 16 centroids
   std::vector<double> t64;
   std::vector<uint8_t> ops16;
+  if ((d == 64 || d == 128) && (m == 0 || m == d)) {
+    // f16 operand of the paged expansion: x_hat_i = sum_k A_k B[i][k], k < d: Pi[k][i]; then sqrt(pi/2)/m S[j][i] with
+    // the projections j of each 32 in the order 0 16 1 17 ... 15 31; slices of 64 k: d rows of 128 swizzled bytes
+    ops16.resize((size_t)(d + m) / 64 * d * 128);
+    for (int i = 0; i < d; ++i)
+      for (int k = 0; k < d + m; ++k) {
+        const int p = k - d, j = p < 0 ? 0 : (p & ~31) + ((p & 31) >> 1) + 16 * (p & 1);
+        const double v = p < 0 ? h->Pi[(size_t)k * d + i] : std::sqrt(M_PI / 2.0) / m * h->S[(size_t)j * d + i];
+        const uint16_t bits = __half_as_ushort(__double2half(v));
+        const size_t off = (size_t)(k >> 6) * d * 128 + (size_t)i * 128 + (size_t)((((k & 63) >> 3) ^ (i & 7)) << 4) + (k & 7) * 2;
+        std::memcpy(&ops16[off], &bits, 2);
+      }
+  }
   if (d <= 256) {
     t64 = h->Pi;
     t64.insert(t64.end(), h->S.begin(), h->S.end());

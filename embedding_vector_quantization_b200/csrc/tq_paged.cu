@@ -16,6 +16,7 @@
 #include "paged_common.cuh"
 #include "paged_append.cuh"
 #include "paged_attn_simt.cuh"
+#include "paged_flash.cuh"
 
 namespace {
 
@@ -237,6 +238,105 @@ int attn_simt(AttnArgs& a, const tq_view& k, const tq_view& v, const SimtPlan& p
   return launched("paged_combine_simt_kernel");
 }
 
+// ---------------------------------------------------------------- attention of chunks, tensor cores
+
+bool simt_forced() {
+  const char* e = std::getenv("TQ_SIMT");
+  return e && std::strcmp(e, "1") == 0;
+}
+
+// 16-bit queries, d = 64 or 128, d signs or none (those handles hold the operands).
+bool flash_formats(const tq_view& k, const tq_view& v) { return k.ops16 && v.ops16 && !simt_forced(); }
+
+struct FlashPlan {
+  int64_t max_seqs, max_tiles, max_items;
+  int heads, ctas;      // KV heads of a round
+  size_t head, tile_start, item_start, unit, ke, ve, seen, part, krows, vrows, total;
+};
+
+constexpr size_t kRowsCap = (size_t)1 << 30;   // f16 rows held at a time, unless one KV head needs more
+
+FlashPlan flash_plan(const tq_view& k, const Batch& b, int Hq, int Hkv, int small_rows, int sms) {
+  FlashPlan p{};
+  const int64_t G = Hq / Hkv;
+  p.max_seqs = std::min<int64_t>(b.B, b.ntok * G / (small_rows + 1));
+  p.max_tiles = std::max<int64_t>(1, p.max_seqs * (((int64_t)b.max_pages * b.page_size + kKT - 1) / kKT));
+  p.max_items = std::max<int64_t>(1, b.ntok * G / kItemRows + p.max_seqs);
+  const size_t tile = (size_t)(k.d / 64) * kAtomRows;
+  p.heads = (int)std::max<size_t>(1, std::min<size_t>(Hkv, kRowsCap / (2 * tile * (size_t)p.max_tiles)));
+  p.ctas = sms;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at = up(at + bytes, 256);
+    return here;
+  };
+  p.head = take(16);
+  p.tile_start = take((size_t)(b.B + 1) * 4);
+  p.item_start = take((size_t)(b.B + 1) * 4);
+  p.unit = take((size_t)(p.max_items + 1) * 4);
+  p.ke = take((size_t)p.heads * p.max_tiles * 4);
+  p.ve = take((size_t)p.heads * p.max_tiles * 4);
+  p.seen = take((size_t)p.max_tiles * 16);
+  p.part = take((size_t)2 * p.ctas * kItemRows * (k.d + 4) * 4);
+  p.krows = take((size_t)p.heads * p.max_tiles * tile);
+  p.vrows = take((size_t)p.heads * p.max_tiles * tile);
+  p.total = at + 256;
+  return p;
+}
+
+template <int D>
+int attn_flash(const AttnArgs& g, const tq_view& k, const tq_view& v, const FlashPlan& p, int small_rows, char* ws, cudaStream_t s) {
+  static std::atomic<uint64_t> s1{0}, s2{0};
+  int st;
+  if ((st = allow_smem(paged_expand_kernel<D>, ExLayout<D>::kBytes, k.device, s1)) ||
+      (st = allow_smem(paged_flash_kernel<D>, FlLayout<D>::kBytes, k.device, s2)))
+    return st;
+  FlashArgs a{};
+  a.q = g.q, a.q_stride = g.q_stride, a.q_dtype = g.q_dtype, a.Hq = g.Hq, a.Hkv = g.Hkv, a.G = g.G;
+  a.bt = g.bt, a.prep = g.prep, a.kq = g.k, a.vq = g.v, a.kc = g.kc, a.vc = g.vc, a.kops = k.ops16, a.vops = v.ops16;
+  a.scale = g.scale, a.causal = g.causal, a.window = g.window, a.small_rows = small_rows, a.ctas = p.ctas;
+  a.out = g.out, a.err = g.err;
+  auto ints = [&](size_t off) { return reinterpret_cast<int*>(ws + off); };
+  a.p.head = ints(p.head), a.p.tile_start = ints(p.tile_start), a.p.item_start = ints(p.item_start), a.p.unit = ints(p.unit);
+  a.p.ke = ints(p.ke), a.p.ve = ints(p.ve), a.p.seen = reinterpret_cast<uint32_t*>(ws + p.seen);
+  a.p.part = reinterpret_cast<float*>(ws + p.part);
+  a.p.krows = reinterpret_cast<uint8_t*>(ws + p.krows), a.p.vrows = reinterpret_cast<uint8_t*>(ws + p.vrows);
+  a.p.max_tiles = (int)p.max_tiles, a.p.max_items = (int)p.max_items;
+  for (a.head0 = 0; a.head0 < a.Hkv; a.head0 += p.heads) {
+    a.heads = std::min(p.heads, a.Hkv - a.head0);
+    {
+      tq_launch_scope scope("paged_plan", s);
+      paged_plan_kernel<<<1, kPlanThreads, 0, s>>>(a);
+    }
+    if ((st = launched("paged_plan_kernel"))) return st;
+    {
+      tq_launch_scope scope("paged_expand", s);
+      paged_expand_kernel<D><<<2 * ((p.ctas + 1) / 2), kExThreads, ExLayout<D>::kBytes, s>>>(a);
+    }
+    if ((st = launched("paged_expand_kernel"))) return st;
+    {
+      tq_launch_scope scope("paged_flash", s);
+      paged_flash_kernel<D><<<p.ctas, kFlThreads, FlLayout<D>::kBytes, s>>>(a);
+    }
+    if ((st = launched("paged_flash_kernel"))) return st;
+    tq_launch_scope scope("paged_merge", s);
+    paged_flash_merge_kernel<D><<<dim3(p.ctas, D / 16), kItemRows, 0, s>>>(a);
+    if ((st = launched("paged_flash_merge_kernel"))) return st;
+  }
+  return st;
+}
+
+constexpr int kSmallRows = 0;   // sequences with at most this many query rows go to the general kernels
+
+// The largest of what the paths of a call may need.
+size_t attn_workspace(const tq_view& k, const tq_view& v, const Batch& b, int Hq, int Hkv) {
+  const int sms = device_sms(k.device);
+  size_t n = simt_plan(k, v, b, Hq, Hkv, sms).total;
+  if (flash_formats(k, v)) n = std::max(n, flash_plan(k, b, Hq, Hkv, kSmallRows, sms).total);
+  return n;
+}
+
 }  // namespace
 
 extern "C" {
@@ -276,7 +376,7 @@ size_t tq_attn_paged_workspace_bytes(const tq_handle* hk, const tq_handle* hv, c
   tq_view kw, vw;
   Batch b{};
   if (check_handles(hk, hv, &kw, &vw) || check_pages(k, "key") || Hkv < 1 || Hq < 1 || Hq % Hkv || check_batch(batch, k, &b)) return 0;
-  return simt_plan(kw, vw, b, Hq, Hkv, device_sms(kw.device)).total;
+  return attn_workspace(kw, vw, b, Hq, Hkv);
 }
 
 int tq_attn_paged(const tq_handle* hk, const tq_handle* hv, const void* q, int q_dtype, int64_t q_stride, int Hq, int Hkv,
@@ -299,8 +399,8 @@ int tq_attn_paged(const tq_handle* hk, const tq_handle* hv, const void* q, int q
   if ((st = check_rows(q, q_dtype, q_stride, Hq, kw.d, "q"))) return st;
   if (!out || !aligned(out, 16)) return fail(TQ_EINVAL, "out is NULL or misaligned (16 bytes)");
   if (!workspace || !aligned(workspace, 16)) return fail(TQ_EINVAL, "workspace is NULL or misaligned (16 bytes)");
-  const SimtPlan plan = simt_plan(kw, vw, a.bt, Hq, Hkv, device_sms(kw.device));
-  if (ws_bytes < plan.total) return fail(TQ_EINVAL, "workspace of %zu bytes, %zu needed", ws_bytes, plan.total);
+  const size_t need = attn_workspace(kw, vw, a.bt, Hq, Hkv);
+  if (ws_bytes < need) return fail(TQ_EINVAL, "workspace of %zu bytes, %zu needed", ws_bytes, need);
   if (tq_internal_fault("launch")) return fail(TQ_ECUDA, "injected launch failure (TQ_FAULT=launch)");
   DeviceGuard dev(kw.device);
   if (dev.err != cudaSuccess) return fail(TQ_ECUDA, "device %d: %s", kw.device, cudaGetErrorString(dev.err));
@@ -310,7 +410,12 @@ int tq_attn_paged(const tq_handle* hk, const tq_handle* hv, const void* q, int q
   a.k = quant_of(kw), a.v = quant_of(vw), a.kc = view_of(kw, k), a.vc = view_of(vw, v);
   a.scale = scale, a.causal = causal, a.window = window, a.out = out, a.err = kw.err;
   char* ws = reinterpret_cast<char*>(up(reinterpret_cast<size_t>(workspace), 256));
-  return attn_simt(a, kw, vw, plan, ws, kw.device, s);
+  const int sms = device_sms(kw.device);
+  if (q_dtype != TQ_F32 && flash_formats(kw, vw)) {
+    const FlashPlan plan = flash_plan(kw, a.bt, Hq, Hkv, kSmallRows, sms);
+    return kw.d == 128 ? attn_flash<128>(a, kw, vw, plan, kSmallRows, ws, s) : attn_flash<64>(a, kw, vw, plan, kSmallRows, ws, s);
+  }
+  return attn_simt(a, kw, vw, simt_plan(kw, vw, a.bt, Hq, Hkv, sms), ws, kw.device, s);
 }
 
 }  // extern "C"
