@@ -56,6 +56,8 @@ struct Plan {
   uint32_t* seen;    // [max_tiles][4] tokens of the tile that exist and lie on a valid page
   uint8_t* krows;    // [heads of a round][max_tiles] f16 key tiles
   uint8_t* vrows;
+  uint8_t* qrows;    // [heads of a round][max_items][2] f16 query tiles
+  float* qfactor;    // [heads of a round][max_items][256] what a row's scores are multiplied by (log2), -1: it sees nothing
   float* part;       // [2 * CTAs][256 rows][d + 2] results of cut items
   int max_tiles, max_items;
 };
@@ -486,10 +488,125 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
   if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(256u) : "memory");
 }
 
+// ---------------------------------------------------------------- queries
+
+// Query rows to f16 tiles, as the attention wants them in shared memory: norm, rotation, then times the power of two that
+// brings every coordinate below one. Four lanes per row; lane q of them holds the 16-byte chunks q, q + 4, ...: the partners
+// of a rotation of the whole head (half a head away) are its own. Bound by latency and bytes: as many rows in flight as fit.
+// Grid: (max_items * 4, heads): 64 rows per CTA.
+template <int D>
+__global__ void __launch_bounds__(256) paged_qtile_kernel(FlashArgs a) {
+  constexpr int C = D / 32;   // chunks per lane
+  const int item = blockIdx.x >> 2, h = blockIdx.y;
+  if (item >= a.p.head[1]) return;
+  const int ql = threadIdx.x & 3, r = (blockIdx.x & 3) * 64 + (threadIdx.x >> 2);
+  const int rot = a.prep.cos_sin ? a.prep.rot_dim : 0, half = rot >> 1;
+  const bool f16 = a.q_dtype == TQ_F16;
+  const int b = last_at_or_before(a.p.item_start, a.bt.B, item), n = seq_rows(a, b);
+  const int64_t t0 = a.bt.q_start[b], slot = (int64_t)h * a.p.max_items + item;
+  const int pos0 = a.bt.len[b] - n, row = (item - a.p.item_start[b]) * kItemRows + r;
+  const bool live = row < n * a.G;
+  const int tok = live ? row / a.G : 0, g = live ? row - tok * a.G : 0, hq = (a.head0 + h) * a.G + g;
+  int64_t rp = pos0 + tok;
+  bool ok = live;
+  if (live && rot) {
+    if (a.prep.pos) rp = a.prep.pos[t0 + tok];
+    if (rp < 0 || rp >= a.prep.max_pos) {
+      if (ql == 0 && (a.prep.pos || rp >= 0)) report_error(a.err, kErrPaged);
+      ok = false;
+    }
+  }
+  const uint16_t* src = static_cast<const uint16_t*>(a.q) + (t0 + tok) * a.q_stride + (int64_t)hq * D;
+  const float* cs_row = a.prep.cos_sin + rp * rot;
+  float z[8 * C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const uint4 w = ok ? __ldg(reinterpret_cast<const uint4*>(src) + ql + 4 * c) : make_uint4(0, 0, 0, 0);
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 v = f16 ? etc::pair_to_float2<true>(x[e]) : etc::pair_to_float2<false>(x[e]);
+      z[8 * c + 2 * e] = v.x, z[8 * c + 2 * e + 1] = v.y;
+    }
+  }
+  float ss = 0.f, rms = 1.f;
+#pragma unroll
+  for (int x = 0; x < 8 * C; ++x) ss = fmaf(z[x], z[x], ss);
+  ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+  ss += __shfl_xor_sync(0xffffffffu, ss, 2);
+  if (a.prep.weight) {
+    rms = rsqrtf(ss / (float)D + a.prep.eps);
+    ss = 0.f;
+#pragma unroll
+    for (int x = 0; x < 8 * C; ++x) {
+      z[x] *= rms * load_any(a.prep.weight, a.prep.weight_dtype, 8 * (ql + 4 * (x >> 3)) + (x & 7));
+      ss = fmaf(z[x], z[x], ss);
+    }
+    ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+    ss += __shfl_xor_sync(0xffffffffu, ss, 2);
+  }
+  if (ok && rot == D && !a.prep.interleaved) {
+#pragma unroll
+    for (int c = 0; c < C / 2; ++c)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int k0 = 8 * (ql + 4 * c) + 4 * e;
+        const float4 co = *reinterpret_cast<const float4*>(cs_row + k0);
+        const float4 si = *reinterpret_cast<const float4*>(cs_row + D / 2 + k0);
+        const float cc[4] = {co.x, co.y, co.z, co.w}, sn[4] = {si.x, si.y, si.z, si.w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          float& lo = z[8 * c + 4 * e + x];
+          float& hi = z[8 * (c + C / 2) + 4 * e + x];
+          const float p = lo, w = hi;
+          lo = p * cc[x] - w * sn[x], hi = w * cc[x] + p * sn[x];
+        }
+      }
+  } else if (ok && rot) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int k0 = 8 * (ql + 4 * c) + 2 * e;
+        float& y0 = z[8 * c + 2 * e];
+        float& y1 = z[8 * c + 2 * e + 1];
+        if (k0 < rot && a.prep.interleaved) {
+          const float co = cs_row[k0 >> 1], si = cs_row[half + (k0 >> 1)], p = y0, w = y1;
+          y0 = p * co - w * si, y1 = w * co + p * si;
+        } else if (k0 < rot) {   // the partner may be any lane's: read again
+          const int kk = k0 < half ? k0 : k0 - half, other = k0 < half ? k0 + half : k0 - half;
+          const float sg = k0 < half ? -rms : rms;
+          float p0 = load_any(src, a.q_dtype, other), p1 = load_any(src, a.q_dtype, other + 1);
+          if (a.prep.weight) {
+            p0 *= load_any(a.prep.weight, a.prep.weight_dtype, other);
+            p1 *= load_any(a.prep.weight, a.prep.weight_dtype, other + 1);
+          }
+          y0 = y0 * cs_row[kk] + sg * p0 * cs_row[half + kk];
+          y1 = y1 * cs_row[kk + 1] + sg * p1 * cs_row[half + kk + 1];
+        }
+      }
+  }
+  // |q_i| <= |q|, which the rotation keeps: the power of two that brings all of them below one
+  int e = 0;
+  const float nq = sqrtf(ss);
+  if (nq > 0.f && nq < INFINITY) frexpf(nq, &e);
+  const float sc = a.scale < 0.f ? -ldexpf(1.f, -e) : ldexpf(1.f, -e);
+  if (ql == 0) a.p.qfactor[slot * kItemRows + r] = ok || !live ? ldexpf(fabsf(a.scale) * 1.44269504089f, e) : -1.f;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int ch = ql + 4 * c;
+    *reinterpret_cast<uint4*>(a.p.qrows + ((2 * slot + (r >> 7)) * (D / 64) + (ch >> 3)) * kAtomRows + (r & 127) * 128 +
+                              (((ch & 7) ^ (r & 7)) << 4)) =
+        make_uint4(half2_bits(z[8 * c] * sc, z[8 * c + 1] * sc), half2_bits(z[8 * c + 2] * sc, z[8 * c + 3] * sc),
+                   half2_bits(z[8 * c + 4] * sc, z[8 * c + 5] * sc), half2_bits(z[8 * c + 6] * sc, z[8 * c + 7] * sc));
+  }
+}
+
 // ---------------------------------------------------------------- flash
 
-// Warps 0-3 and 4-7: softmax of query tile 0 and 1 (thread = row); 8: copies; 9: MMAs.
-constexpr int kFlThreads = 320;
+// Warps 0-3 and 4-7: softmax of query tile 0 and 1 (thread = row); 8: copies; 9: MMAs; 10, 11 fill
+// their warpgroup, which gives registers up: 384 threads x 168 at launch = 128 x (216 + 216 + 72).
+constexpr int kFlThreads = 384;
 constexpr int kFlStages = 4;      // ring of key and value tiles, in the order K0 V0 K1 V1 ...
 
 template <int D>
@@ -498,8 +615,8 @@ struct FlLayout {
   static constexpr uint32_t kQ = 0;                         // two query tiles
   static constexpr uint32_t kRing = 2 * kTile;
   static constexpr uint32_t kBars = kRing + kFlStages * kTile;
-  // full[4], empty[4], q_full[2], s_full[2], p_full[2], pv_done[2], o_free[2]
-  static constexpr int kNumBars = 2 * kFlStages + 10;
+  // full[4], empty[4], q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], o_free[2]
+  static constexpr int kNumBars = 2 * kFlStages + 12;
   static constexpr uint32_t kMisc = kBars + 8 * kNumBars;
   static constexpr uint32_t kBytes = kMisc + 16;
 };
@@ -565,6 +682,50 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
       : "memory");
 }
 
+// ---- pairs of fp32 values in one 64-bit register: one instruction for two sums or products
+__device__ __forceinline__ uint64_t pair2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpair2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+  return r;
+}
+// 2^x for two values on the fused multiply-add pipe (the exponential unit alone would bind the kernel: 16 results a cycle
+// against 4096 fused multiply-adds of the tensor cores). x = n + f, |f| <= 1/2; 2^f by the cubic of least relative error
+// (7.5e-5, a sixth of what the rounding to f16 costs; fitted by linear programming over [-1/2, 1/2]); n is added to the
+// exponent. x <= -126 gives a value near 2^-126, which becomes 0 in f16.
+__device__ __forceinline__ float2 exp2_poly(float x, float y) {
+  const uint64_t v = pair2(fmaxf(x, -126.f), fmaxf(y, -126.f));
+  const uint64_t big = pair2(12582912.f, 12582912.f), none = pair2(-12582912.f, -12582912.f), neg = pair2(-1.f, -1.f);
+  const uint64_t t = add2(v, big);               // 1.5 2^23: the integer part lands in the low bits
+  const uint64_t f = fma2(add2(t, none), neg, v);
+  uint64_t p = fma2(f, pair2(0.055171772837638855f, 0.055171772837638855f), pair2(0.2426113784313202f, 0.2426113784313202f));
+  p = fma2(p, f, pair2(0.6932609677314758f, 0.6932609677314758f));
+  p = fma2(p, f, pair2(0.9999279975891113f, 0.9999279975891113f));
+  const float2 q = unpair2(p), n = unpair2(t);
+  return make_float2(__int_as_float(__float_as_int(q.x) + (__float_as_int(n.x) << 23)),
+                     __int_as_float(__float_as_int(q.y) + (__float_as_int(n.y) << 23)));
+}
+constexpr int kPolyEvery = 4;   // of so many pairs one goes to the polynomial
+
 template <int D>
 __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a) {
   using L = FlLayout<D>;
@@ -583,22 +744,19 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
   auto full = [&](int s) { return bars + 8u * s; };
   auto empty = [&](int s) { return bars + 8u * (kFlStages + s); };
   auto q_full = [&](int i) { return bars + 8u * (2 * kFlStages + i); };
-  auto s_full = [&](int i) { return bars + 8u * (2 * kFlStages + 2 + i); };
-  auto p_full = [&](int i) { return bars + 8u * (2 * kFlStages + 4 + i); };
-  auto pv_done = [&](int i) { return bars + 8u * (2 * kFlStages + 6 + i); };
-  auto o_free = [&](int i) { return bars + 8u * (2 * kFlStages + 8 + i); };
+  auto q_empty = [&](int i) { return bars + 8u * (2 * kFlStages + 2 + i); };
+  auto s_full = [&](int i) { return bars + 8u * (2 * kFlStages + 4 + i); };
+  auto p_full = [&](int i) { return bars + 8u * (2 * kFlStages + 6 + i); };
+  auto pv_done = [&](int i) { return bars + 8u * (2 * kFlStages + 8 + i); };
+  auto o_free = [&](int i) { return bars + 8u * (2 * kFlStages + 10 + i); };
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
   if (tid == 0) {
     *abort_flag = 0;
     uint64_t* b = reinterpret_cast<uint64_t*>(smem + L::kBars);
-    for (int s = 0; s < 2 * kFlStages; ++s) bar_init(b + s, 1);
-    for (int i = 0; i < 2; ++i) {
-      bar_init(b + 2 * kFlStages + i, 4);       // q_full: the tile's four warps
-      bar_init(b + 2 * kFlStages + 2 + i, 1);   // s_full: commit
-      bar_init(b + 2 * kFlStages + 4 + i, 4);   // p_full: four warps
-      bar_init(b + 2 * kFlStages + 6 + i, 1);   // pv_done: commit
-      bar_init(b + 2 * kFlStages + 8 + i, 4);   // o_free: four warps
+    for (int x = 0; x < L::kNumBars; ++x) {   // p_full and o_free: a query tile's four warps; the others: one copy or commit
+      const int y = x - 2 * kFlStages;
+      bar_init(b + x, y == 6 || y == 7 || y == 10 || y == 11 ? 4 : 1);
     }
   }
   if (warp == 9) {
@@ -617,8 +775,9 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
   };
 
   if (warp == 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
     if (lane == 0) {
-      int k = 0;   // tiles issued, keys and values counted apart
+      int k = 0, seg = 0;   // tiles issued (keys and values counted apart), segments with tiles
       for (int64_t u = sp.u0; u < sp.u1;) {
         const Segment s = segment_at(a, items, units, u, sp.u1);
         u = s.next;
@@ -630,13 +789,26 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
             if (*abort_flag) break;
             expect_tx(full(st), L::kTile);
             bulk_load(base + L::kRing + st * L::kTile, (kv ? a.p.vrows : a.p.krows) + (t + j) * L::kTile, L::kTile, full(st));
+            if (j == s.t0 && kv == 0) {   // the queries, behind the first keys
+              const int64_t qt = 2 * ((int64_t)s.h * a.p.max_items + s.item);
+              for (int i = 0; i < 2; ++i) {
+                if (seg > 0) wait(q_empty(i), (seg - 1) & 1);
+                if (*abort_flag) break;
+                expect_tx(q_full(i), L::kTile);
+                bulk_load(base + L::kQ + i * L::kTile, a.p.qrows + (qt + i) * L::kTile, L::kTile, q_full(i));
+              }
+              ++seg;
+            }
           }
         if (*abort_flag) break;
       }
       // never leave with a copy still landing in this CTA's shared memory
       for (int i = max(0, k - kFlStages); i < k; ++i) (void)wait_bar(full(i % kFlStages), (i / kFlStages) & 1);
+      if (seg > 0)
+        for (int i = 0; i < 2; ++i) (void)wait_bar(q_full(i), (seg - 1) & 1);
     }
   } else if (warp == 9) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
     if (lane == 0) {
       int k = 0, seg = 0, tile = 0;   // ring position, segments with tiles, tiles
       for (int64_t u = sp.u0; u < sp.u1;) {
@@ -644,7 +816,7 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
         u = s.next;
         const int nt = s.t1 - s.t0;
         if (nt <= 0) continue;
-        auto scores = [&](int i, int kk) {   // S_i = Q_i K^T
+        auto scores = [&](int i, int kk, bool last) {   // S_i = Q_i K^T
           const int st = kk % kFlStages;
 #pragma unroll
           for (int c = 0; c < D / 16; ++c)
@@ -652,12 +824,13 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
                     sw128_desc(base + L::kRing + st * L::kTile + (c >> 2) * kAtomRows + (c & 3) * 32), flash_idesc(128, false),
                     c > 0 ? 1u : 0u);
           mma_commit(s_full(i));
+          if (last) mma_commit(q_empty(i));
         };
         for (int i = 0; i < 2; ++i) {
           wait(q_full(i), seg & 1);
           if (i == 0) wait(full(k % kFlStages), (k / kFlStages) & 1);
           tc_fence_after();
-          scores(i, k);
+          scores(i, k, nt == 1);
         }
         mma_commit(empty(k % kFlStages));
         for (int j = 0; j < nt; ++j, k += 2, ++tile) {
@@ -678,7 +851,7 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
                 wait(full((k + 2) % kFlStages), ((k + 2) / kFlStages) & 1);
                 tc_fence_after();
               }
-              scores(i, k + 2);
+              scores(i, k + 2, j + 2 == nt);
               if (i == 1) mma_commit(empty((k + 2) % kFlStages));
             }
           }
@@ -689,7 +862,10 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
       if (tile > 0)
         for (int i = 0; i < 2; ++i) (void)wait_bar(pv_done(i), (tile - 1) & 1);
     }
+  } else if (warp >= 10) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;\n");
     // ---- softmax: thread = query row
     const int i = warp >> 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -720,118 +896,9 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
         hi = min(hi, pos + 1);
         if (a.window > 0) lo = max(0, pos - a.window + 1);
       }
-      // ---- the query: norm, rotation, then times 2^-e below one, to f16
-      float qscale = 0.f;
-      {
-        const uint32_t qrow = base + L::kQ + i * L::kTile + r * 128;
-        bool ok = live;
-        int64_t rp = 0;
-        if (live && a.prep.cos_sin) {
-          rp = a.prep.pos ? (int64_t)a.prep.pos[t] : (int64_t)pos;
-          if (rp < 0 || rp >= a.prep.max_pos) {
-            if (a.prep.pos || rp >= 0) report_error(a.err, kErrPaged);
-            ok = false, hi = 0;
-          }
-        }
-        uint4 raw[D / 8];
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + t * a.q_stride + (int64_t)hq * D);
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) raw[c] = ok ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-        const bool f16 = a.q_dtype == TQ_F16;
-        auto get = [&](int x) -> float2 {   // coordinates 2 x, 2 x + 1
-          const uint32_t w = (&raw[x >> 2].x)[x & 3];
-          return f16 ? etc::pair_to_float2<true>(w) : etc::pair_to_float2<false>(w);
-        };
-        float rms = 1.f, ss = 0.f;
-#pragma unroll
-        for (int x = 0; x < D / 2; ++x) {
-          const float2 v = get(x);
-          ss = fmaf(v.x, v.x, fmaf(v.y, v.y, ss));
-        }
-        if (a.prep.weight) {
-          rms = rsqrtf(ss / (float)D + a.prep.eps);
-          ss = 0.f;
-#pragma unroll
-          for (int x = 0; x < D / 2; ++x) {
-            const float2 v = get(x);
-            const float y0 = v.x * rms * load_any(a.prep.weight, a.prep.weight_dtype, 2 * x);
-            const float y1 = v.y * rms * load_any(a.prep.weight, a.prep.weight_dtype, 2 * x + 1);
-            ss = fmaf(y0, y0, fmaf(y1, y1, ss));
-          }
-        }
-        // |q_i| <= |q|: the largest power of two that brings all of them below one
-        int e = 0;
-        const float nq = sqrtf(ss);
-        if (nq > 0.f && nq < INFINITY) frexpf(nq, &e);
-        const float sc = a.scale < 0.f ? -ldexpf(1.f, -e) : ldexpf(1.f, -e);
-        qscale = ldexpf(fabsf(a.scale) * 1.44269504089f, e);
-        const int rot = a.prep.cos_sin ? a.prep.rot_dim : 0, half = rot >> 1;
-        const float* cs_row = a.prep.cos_sin + rp * rot;
-        auto at = [&](int x) -> float2 {
-          float2 v = get(x);
-          if (a.prep.weight) {
-            v.x *= rms * load_any(a.prep.weight, a.prep.weight_dtype, 2 * x);
-            v.y *= rms * load_any(a.prep.weight, a.prep.weight_dtype, 2 * x + 1);
-          }
-          return v;
-        };
-        auto put = [&](int c, const uint32_t (&o)[4]) {   // 16-byte chunk c of the row
-          sts128(qrow + (c >> 3) * kAtomRows + (((c & 7) ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
-        };
-        if (!ok) {
-          const uint32_t z[4] = {0, 0, 0, 0};
-          for (int c = 0; c < D / 8; ++c) put(c, z);
-        } else if (rot == D && !a.prep.interleaved) {
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t o1[4], o2[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float2 p = at(4 * c + x), w = at(4 * c + x + D / 4);
-              const float2 co2 = *reinterpret_cast<const float2*>(cs_row + 8 * c + 2 * x);
-              const float2 si2 = *reinterpret_cast<const float2*>(cs_row + D / 2 + 8 * c + 2 * x);
-              o1[x] = half2_bits((p.x * co2.x - w.x * si2.x) * sc, (p.y * co2.y - w.y * si2.y) * sc);
-              o2[x] = half2_bits((w.x * co2.x + p.x * si2.x) * sc, (w.y * co2.y + p.y * si2.y) * sc);
-            }
-            put(c, o1);
-            put(c + D / 16, o2);
-          }
-        } else {
-          // any other rotation, pair by pair: the partner of a pair of coordinates is read again from memory
-          const uint16_t* q16 = reinterpret_cast<const uint16_t*>(src);
-          auto one = [&](int x) {
-            float v = load_any(q16, a.q_dtype, x);
-            if (a.prep.weight) v *= rms * load_any(a.prep.weight, a.prep.weight_dtype, x);
-            return v;
-          };
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            uint32_t o[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              float2 v = at(4 * c + x);
-              const int k = 8 * c + 2 * x;
-              if (k < rot) {
-                if (a.prep.interleaved) {
-                  const float co1 = cs_row[k >> 1], si1 = cs_row[half + (k >> 1)];
-                  v = make_float2(v.x * co1 - v.y * si1, v.y * co1 + v.x * si1);
-                } else {
-                  const int kk = k < half ? k : k - half;
-                  const float sg = k < half ? -1.f : 1.f;
-                  const int other = k < half ? k + half : k - half;
-                  v = make_float2(v.x * cs_row[kk] + sg * one(other) * cs_row[half + kk],
-                                  v.y * cs_row[kk + 1] + sg * one(other + 1) * cs_row[half + kk + 1]);
-                }
-              }
-              o[x] = half2_bits(v.x * sc, v.y * sc);
-            }
-            put(c, o);
-          }
-        }
-        fence_async();
-        __syncwarp();
-        if (lane == 0) bar_arrive(q_full(i));
-      }
+      const float factor = a.p.qfactor[((int64_t)s.h * a.p.max_items + s.item) * kItemRows + 128 * i + r];
+      const float qscale = fabsf(factor);
+      if (factor < 0.f) hi = 0;   // no rotation for its position: the row sees nothing
       // ---- key tiles
       const int tile0 = a.p.tile_start[s.b] + s.lo_tile;
       const int64_t te = (int64_t)s.h * a.p.max_tiles + tile0;
@@ -843,7 +910,7 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
       int ke = a.p.ke[te + s.t0], ve = a.p.ve[te + s.t0];
       uint4 seen = *reinterpret_cast<const uint4*>(a.p.seen + 4 * (tile0 + s.t0));
       for (int j = s.t0; j < s.t1; ++j, ++tile) {
-        const float c = qscale * exp2f((float)ke);
+        const float c = fmaxf(qscale * exp2f((float)ke), 1e-37f);   // above 0: c times the mask's -infinity stays -infinity
         // value tiles come in units of 2^ve: their weights take the difference along. The unit moves up when a tile would
         // bring weights above 2^(8 + 4); a tile 2^100 below it keeps its place in the sum of weights and adds nothing.
         const int vnow = j == s.t0 || ve > vref + 4 ? ve : vref;
@@ -860,29 +927,31 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
         const bool masked = __any_sync(0xffffffffu, !whole);
         wait(s_full(i), tile & 1);
         tc_fence_after();
-        float mx = -INFINITY;
-        auto mask_of = [&](int q4) -> uint32_t {   // keys 32 q4 .. of the tile this row sees
-          const uint32_t w = q4 == 0 ? there.x : q4 == 1 ? there.y : q4 == 2 ? there.z : there.w;
-          const int f = k0 + 32 * q4, lo1 = min(max(lo - f, 0), 32), hi1 = min(max(hi - f, 0), 32);
-          const uint32_t below = hi1 >= 32 ? 0xffffffffu : (1u << hi1) - 1u;
-          const uint32_t from = lo1 >= 32 ? 0u : 0xffffffffu << lo1;
-          return w & below & from;
-        };
+        uint32_t v[4][32];
 #pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) {
-          uint32_t v[32];
-          tmem_ld32(cs, v, 32 * q4);
-          tmem_wait_ld(v);
-          if (masked) {
-            const uint32_t ok = mask_of(q4);
+        for (int q4 = 0; q4 < 4; ++q4) tmem_ld32(cs, v[q4], 32 * q4);
 #pragma unroll
-            for (int x = 0; x < 32; ++x) mx = fmaxf(mx, ok >> x & 1 ? __uint_as_float(v[x]) : -INFINITY);
-          } else {
+        for (int q4 = 0; q4 < 4; ++q4) tmem_wait_ld(v[q4]);
+        if (masked) {
 #pragma unroll
-            for (int x = 0; x < 32; x += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(v[x]), __uint_as_float(v[x + 1])));
+          for (int q4 = 0; q4 < 4; ++q4) {
+            const uint32_t w = q4 == 0 ? there.x : q4 == 1 ? there.y : q4 == 2 ? there.z : there.w;
+            const int f = k0 + 32 * q4, lo1 = min(max(lo - f, 0), 32), hi1 = min(max(hi - f, 0), 32);
+            const uint32_t ok = w & (hi1 >= 32 ? 0xffffffffu : (1u << hi1) - 1u) & (lo1 >= 32 ? 0u : 0xffffffffu << lo1);
+#pragma unroll
+            for (int x = 0; x < 32; ++x) v[q4][x] = ok >> x & 1 ? v[q4][x] : 0xff800000u;
           }
         }
-        const float top = mx == -INFINITY ? -INFINITY : mx * c;
+        float mx4[4];
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) {
+          mx4[q4] = __uint_as_float(v[q4][0]);
+#pragma unroll
+          for (int x = 1; x < 31; x += 2) mx4[q4] = fmaxf(mx4[q4], fmaxf(__uint_as_float(v[q4][x]), __uint_as_float(v[q4][x + 1])));
+          mx4[q4] = fmaxf(mx4[q4], __uint_as_float(v[q4][31]));
+        }
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+        const float top = mx * c;
         // the reference moves only when a score exceeds it by 2^8: weights stay below 256, and the sums above are rarely scaled
         const bool move = top > m + 8.f;
         if (__any_sync(0xffffffffu, move || fv != 1.f)) {
@@ -906,26 +975,23 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
           }
         }
         const float ref = (m == -INFINITY ? 0.f : m) - dv;   // weights come out times 2^(E - reference exponent)
-        float sum = 0.f;
+        const uint64_t c2 = pair2(c, c), r2 = pair2(-ref, -ref);
+        uint64_t sums[2] = {0, 0};
 #pragma unroll
         for (int q4 = 0; q4 < 4; ++q4) {
-          uint32_t v[32], p[16];
-          tmem_ld32(cs, v, 32 * q4);
-          tmem_wait_ld(v);
-          const uint32_t ok = masked ? mask_of(q4) : 0xffffffffu;
+          uint32_t p[16];
 #pragma unroll
-          for (int x = 0; x < 32; x += 2) {
-            float p0 = exp2f(fmaf(__uint_as_float(v[x]), c, -ref)), p1 = exp2f(fmaf(__uint_as_float(v[x + 1]), c, -ref));
-            if (masked) {
-              p0 = ok >> x & 1 ? p0 : 0.f;
-              p1 = ok >> (x + 1) & 1 ? p1 : 0.f;
-            }
-            sum += p0 + p1;
-            p[x >> 1] = half2_bits(p0, p1);
+          for (int x = 0; x < 16; ++x) {
+            const float2 e = unpair2(fma2(pair2(__uint_as_float(v[q4][2 * x]), __uint_as_float(v[q4][2 * x + 1])), c2, r2));
+            const float2 w = x % kPolyEvery == kPolyEvery - 1 ? exp2_poly(e.x, e.y) : make_float2(ex2(e.x), ex2(e.y));
+            sums[x & 1] = add2(sums[x & 1], pair2(w.x, w.y));
+            p[x] = half2_bits(w.x, w.y);
           }
-          // the weights of 32 keys take 16 of the 32 columns their scores held; nothing read later is overwritten
+          // the weights of 32 keys take 16 of the columns the scores held
           tmem_st16(cs + 16 * q4, p);
         }
+        const float2 sum2 = unpair2(add2(sums[0], sums[1]));
+        const float sum = sum2.x + sum2.y;
         etc::tmem_wait_st();
         l = fmaf(sum, exp2f(-dv), l);
         tc_fence_before();

@@ -251,7 +251,7 @@ bool flash_formats(const tq_view& k, const tq_view& v) { return k.ops16 && v.ops
 struct FlashPlan {
   int64_t max_seqs, max_tiles, max_items;
   int heads, ctas;      // KV heads of a round
-  size_t head, tile_start, item_start, unit, ke, ve, seen, part, krows, vrows, total;
+  size_t head, tile_start, item_start, unit, ke, ve, seen, part, krows, vrows, qrows, qfactor, total;
 };
 
 constexpr size_t kRowsCap = (size_t)1 << 30;   // f16 rows held at a time, unless one KV head needs more
@@ -281,6 +281,8 @@ FlashPlan flash_plan(const tq_view& k, const Batch& b, int Hq, int Hkv, int smal
   p.part = take((size_t)2 * p.ctas * kItemRows * (k.d + 4) * 4);
   p.krows = take((size_t)p.heads * p.max_tiles * tile);
   p.vrows = take((size_t)p.heads * p.max_tiles * tile);
+  p.qrows = take((size_t)p.heads * p.max_items * 2 * tile);
+  p.qfactor = take((size_t)p.heads * p.max_items * kItemRows * 4);
   p.total = at + 256;
   return p;
 }
@@ -302,6 +304,7 @@ int attn_flash(const AttnArgs& g, const tq_view& k, const tq_view& v, const Flas
   a.p.ke = ints(p.ke), a.p.ve = ints(p.ve), a.p.seen = reinterpret_cast<uint32_t*>(ws + p.seen);
   a.p.part = reinterpret_cast<float*>(ws + p.part);
   a.p.krows = reinterpret_cast<uint8_t*>(ws + p.krows), a.p.vrows = reinterpret_cast<uint8_t*>(ws + p.vrows);
+  a.p.qrows = reinterpret_cast<uint8_t*>(ws + p.qrows), a.p.qfactor = reinterpret_cast<float*>(ws + p.qfactor);
   a.p.max_tiles = (int)p.max_tiles, a.p.max_items = (int)p.max_items;
   for (a.head0 = 0; a.head0 < a.Hkv; a.head0 += p.heads) {
     a.heads = std::min(p.heads, a.Hkv - a.head0);
@@ -310,6 +313,11 @@ int attn_flash(const AttnArgs& g, const tq_view& k, const tq_view& v, const Flas
       paged_plan_kernel<<<1, kPlanThreads, 0, s>>>(a);
     }
     if ((st = launched("paged_plan_kernel"))) return st;
+    {
+      tq_launch_scope scope("paged_qtile", s);
+      paged_qtile_kernel<D><<<dim3(4 * (unsigned)p.max_items, a.heads), 256, 0, s>>>(a);
+    }
+    if ((st = launched("paged_qtile_kernel"))) return st;
     {
       tq_launch_scope scope("paged_expand", s);
       paged_expand_kernel<D><<<2 * ((p.ctas + 1) / 2), kExThreads, ExLayout<D>::kBytes, s>>>(a);
