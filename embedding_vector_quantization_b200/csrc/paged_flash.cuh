@@ -604,9 +604,11 @@ __global__ void __launch_bounds__(256) paged_qtile_kernel(FlashArgs a) {
 
 // ---------------------------------------------------------------- flash
 
-// Warps 0-3 and 4-7: softmax of query tile 0 and 1 (thread = row); 8: copies; 9: MMAs; 10, 11 fill
-// their warpgroup, which gives registers up: 384 threads x 168 at launch = 128 x (216 + 216 + 72).
-constexpr int kFlThreads = 384;
+// Warps 0-15: softmax, two threads per query row (warps 0-3 and 4-7: keys 0-63 and 64-127 of the rows of query tile 0, 8-15
+// of tile 1): with one thread per row its chain of loads, maximum and exponentials took twice the time that the tensor cores
+// need for the other tile. 16: copies; 17: MMAs; 18, 19 fill their warpgroup, which gives registers up:
+// 640 threads x 96 at launch = 128 x (4 x 104 + 64).
+constexpr int kFlThreads = 640;
 constexpr int kFlStages = 4;      // ring of key and value tiles, in the order K0 V0 K1 V1 ...
 
 template <int D>
@@ -617,7 +619,8 @@ struct FlLayout {
   static constexpr uint32_t kBars = kRing + kFlStages * kTile;
   // full[4], empty[4], q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], o_free[2]
   static constexpr int kNumBars = 2 * kFlStages + 12;
-  static constexpr uint32_t kMisc = kBars + 8 * kNumBars;
+  static constexpr uint32_t kRow = kBars + 8 * kNumBars;     // float [2][256]: what the two threads of a row tell each other
+  static constexpr uint32_t kMisc = kRow + 2048;
   static constexpr uint32_t kBytes = kMisc + 16;
 };
 static_assert(FlLayout<128>::kBytes <= 232448, "flash layout exceeds the shared memory of one CTA");
@@ -633,11 +636,33 @@ __device__ __forceinline__ uint64_t mn_desc16(uint32_t saddr) {
   return d;
 }
 
-// A in tensor memory (lane = row, 8 columns of two f16 per 16 K).
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+// ---- issue by one lane of a whole warp: the warp stays together, so that addresses and descriptors live in uniform
+// registers (a lone thread spends longer on moving them there than the tensor cores on the instruction)
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r;
+}
+template <bool ACC>
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc));
+      "{\n .reg .pred p, q;\n setp.ne.u32 q, %0, 0;\n setp.ne.u32 p, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%1], %2, %3, %4, p;\n}\n" ::"r"(leader),
+      "r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "n"(ACC ? 1 : 0));
+}
+// A in tensor memory (lane = row, 8 columns of two f16 per 16 K).
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 q, %0, 0;\n setp.ne.u32 p, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], %3, %4, p;\n}\n" ::"r"(leader),
+      "r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void commit_one(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.u32 q, %0, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n}\n" ::"r"(leader),
+      "r"(bar)
+      : "memory");
 }
 
 // CTA c of P takes units [c U / P, (c + 1) U / P) of the round's U = heads * units, head by head, item by item.
@@ -724,6 +749,16 @@ __device__ __forceinline__ float2 exp2_poly(float x, float y) {
   return make_float2(__int_as_float(__float_as_int(q.x) + (__float_as_int(n.x) << 23)),
                      __int_as_float(__float_as_int(q.y) + (__float_as_int(n.y) << 23)));
 }
+// Barrier of n threads that tells whether any of them said so.
+__device__ __forceinline__ bool bar_any(int id, int n, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)pred), "r"(id), "r"(n)
+      : "memory");
+  return r != 0;
+}
 constexpr int kPolyEvery = 4;   // of so many pairs one goes to the polynomial
 
 template <int D>
@@ -754,12 +789,12 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
   if (tid == 0) {
     *abort_flag = 0;
     uint64_t* b = reinterpret_cast<uint64_t*>(smem + L::kBars);
-    for (int x = 0; x < L::kNumBars; ++x) {   // p_full and o_free: a query tile's four warps; the others: one copy or commit
+    for (int x = 0; x < L::kNumBars; ++x) {   // p_full and o_free: a query tile's eight warps; the others: one copy or commit
       const int y = x - 2 * kFlStages;
-      bar_init(b + x, y == 6 || y == 7 || y == 10 || y == 11 ? 4 : 1);
+      bar_init(b + x, y == 6 || y == 7 || y == 10 || y == 11 ? 8 : 1);
     }
   }
-  if (warp == 9) {
+  if (warp == 17) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(base + L::kMisc), "r"(512u) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
   }
@@ -774,8 +809,8 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
     report_error(a.err, kErrTimeout);
   };
 
-  if (warp == 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
+  if (warp == 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
     if (lane == 0) {
       int k = 0, seg = 0;   // tiles issued (keys and values counted apart), segments with tiles
       for (int64_t u = sp.u0; u < sp.u1;) {
@@ -807,69 +842,75 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
       if (seg > 0)
         for (int i = 0; i < 2; ++i) (void)wait_bar(q_full(i), (seg - 1) & 1);
     }
-  } else if (warp == 9) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
-    if (lane == 0) {
-      int k = 0, seg = 0, tile = 0;   // ring position, segments with tiles, tiles
-      for (int64_t u = sp.u0; u < sp.u1;) {
-        const Segment s = segment_at(a, items, units, u, sp.u1);
-        u = s.next;
-        const int nt = s.t1 - s.t0;
-        if (nt <= 0) continue;
-        auto scores = [&](int i, int kk, bool last) {   // S_i = Q_i K^T
-          const int st = kk % kFlStages;
+  } else if (warp == 17) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+    const uint32_t lead = elect_one();
+    const uint64_t q_desc = sw128_desc(base + L::kQ), k_desc = sw128_desc(base + L::kRing), v_desc = mn_desc16(base + L::kRing);
+    constexpr uint32_t kT16 = L::kTile >> 4;   // a tile in the descriptors' unit of 16 bytes
+    int k = 0, seg = 0, tile = 0;   // ring position, segments with tiles, tiles
+    for (int64_t u = sp.u0; u < sp.u1;) {
+      const Segment s = segment_at(a, items, units, u, sp.u1);
+      u = s.next;
+      const int nt = s.t1 - s.t0;
+      if (nt <= 0) continue;
+      auto scores = [&](int i, int kk, bool last) {   // S_i = Q_i K^T
+        const uint64_t qd = q_desc + i * kT16, kd = k_desc + (kk % kFlStages) * kT16;
+        mma_ss<false>(lead, col_s[i], qd, kd, flash_idesc(128, false));
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c)
-            mma_f16(col_s[i], sw128_desc(base + L::kQ + i * L::kTile + (c >> 2) * kAtomRows + (c & 3) * 32),
-                    sw128_desc(base + L::kRing + st * L::kTile + (c >> 2) * kAtomRows + (c & 3) * 32), flash_idesc(128, false),
-                    c > 0 ? 1u : 0u);
-          mma_commit(s_full(i));
-          if (last) mma_commit(q_empty(i));
-        };
-        for (int i = 0; i < 2; ++i) {
-          wait(q_full(i), seg & 1);
-          if (i == 0) wait(full(k % kFlStages), (k / kFlStages) & 1);
-          tc_fence_after();
-          scores(i, k, nt == 1);
+        for (int c = 1; c < D / 16; ++c) {
+          const uint32_t off = ((c >> 2) * kAtomRows + (c & 3) * 32) >> 4;
+          mma_ss<true>(lead, col_s[i], qd + off, kd + off, flash_idesc(128, false));
         }
-        mma_commit(empty(k % kFlStages));
-        for (int j = 0; j < nt; ++j, k += 2, ++tile) {
-          const int vs = (k + 1) % kFlStages;
-          for (int i = 0; i < 2; ++i) {
-            if (i == 0) wait(full(vs), ((k + 1) / kFlStages) & 1);
-            if (j == 0 && seg > 0) wait(o_free(i), (seg - 1) & 1);
-            wait(p_full(i), tile & 1);
-            tc_fence_after();
+        commit_one(lead, s_full(i));
+        if (last) commit_one(lead, q_empty(i));
+      };
 #pragma unroll
-            for (int c = 0; c < 8; ++c)   // 16 tokens at a time
-              mma_f16_ts(col_o[i], col_s[i] + 8 * c, mn_desc16(base + L::kRing + vs * L::kTile + c * 2048), flash_idesc(D, true),
-                         (j | c) > 0 ? 1u : 0u);
-            mma_commit(pv_done(i));
-            if (i == 1) mma_commit(empty(vs));
-            if (j + 1 < nt) {
-              if (i == 0) {
-                wait(full((k + 2) % kFlStages), ((k + 2) / kFlStages) & 1);
-                tc_fence_after();
-              }
-              scores(i, k + 2, j + 2 == nt);
-              if (i == 1) mma_commit(empty((k + 2) % kFlStages));
+      for (int i = 0; i < 2; ++i) {
+        wait(q_full(i), seg & 1);
+        if (i == 0) wait(full(k % kFlStages), (k / kFlStages) & 1);
+        tc_fence_after();
+        scores(i, k, nt == 1);
+      }
+      commit_one(lead, empty(k % kFlStages));
+      for (int j = 0; j < nt; ++j, k += 2, ++tile) {
+        const int vs = (k + 1) % kFlStages;
+        const uint64_t vd = v_desc + vs * kT16;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (i == 0) wait(full(vs), ((k + 1) / kFlStages) & 1);
+          if (j == 0 && seg > 0) wait(o_free(i), (seg - 1) & 1);
+          wait(p_full(i), tile & 1);
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < 8; ++c)   // 16 tokens at a time
+            mma_ts(lead, col_o[i], col_s[i] + 8 * c, vd + ((c * 2048) >> 4), flash_idesc(D, true), c > 0 ? 1u : (j > 0 ? 1u : 0u));
+          commit_one(lead, pv_done(i));
+          if (i == 1) commit_one(lead, empty(vs));
+          if (j + 1 < nt) {
+            if (i == 0) {
+              wait(full((k + 2) % kFlStages), ((k + 2) / kFlStages) & 1);
+              tc_fence_after();
             }
+            scores(i, k + 2, j + 2 == nt);
+            if (i == 1) commit_one(lead, empty((k + 2) % kFlStages));
           }
         }
-        ++seg;
       }
-      // tensor memory is released below: the last contractions must have ended
-      if (tile > 0)
-        for (int i = 0; i < 2; ++i) (void)wait_bar(pv_done(i), (tile - 1) & 1);
+      ++seg;
     }
-  } else if (warp >= 10) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
+    // tensor memory is released below: the last contractions must have ended
+    if (tile > 0)
+      for (int i = 0; i < 2; ++i) (void)wait_bar(pv_done(i), (tile - 1) & 1);
+  } else if (warp >= 18) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;\n");
-    // ---- softmax: thread = query row
-    const int i = warp >> 2, r = tid & 127;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n");
+    // ---- softmax: thread = half a query row
+    const int i = warp >> 3, half = (warp >> 2) & 1, r = tid & 127;
+    float* const mine = reinterpret_cast<float*>(smem + L::kRow) + 256 * i + 128 * half + r;
+    const float* const theirs = reinterpret_cast<float*>(smem + L::kRow) + 256 * i + 128 * (half ^ 1) + r;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t cs = col_s[i] + lanes, co = col_o[i] + lanes;
+    const uint32_t cs = col_s[i] + lanes, co = col_o[i] + lanes + half * (D / 2);   // scores; this thread's value sums
     int tile = 0;   // tiles of this CTA so far
     for (int64_t u = sp.u0; u < sp.u1;) {
       const Segment s = segment_at(a, items, units, u, sp.u1);
@@ -884,8 +925,8 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
       const int64_t oat = (t * a.Hq + hq) * D;
       if (nt <= 0) {
         if (s.nt == 0 && first_unit && live) {   // no key at all
-          uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + oat);
-          for (int c = 0; c < D / 8; ++c) o[c] = make_uint4(0, 0, 0, 0);
+          uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + oat + half * (D / 2));
+          for (int c = 0; c < D / 16; ++c) o[c] = make_uint4(0, 0, 0, 0);
         }
         continue;
       }
@@ -917,68 +958,74 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
         const float fv = exp2f((float)max(j == s.t0 ? 0 : vref - vnow, -126));
         vref = vnow;
         const float dv = (float)max(ve - vref, -100);
-        const uint4 there = seen;
+        const uint4 seen_now = seen;
         if (j + 1 < s.t1) {
           ke = a.p.ke[te + j + 1], ve = a.p.ve[te + j + 1];
           seen = *reinterpret_cast<const uint4*>(a.p.seen + 4 * (tile0 + j + 1));
         }
-        const int k0 = key_first + j * kKT;
-        const bool whole = (there.x & there.y & there.z & there.w) == 0xffffffffu && k0 >= lo && k0 + kKT <= hi;
+        const int k0 = key_first + j * kKT + 64 * half;
+        const uint32_t there[2] = {half ? seen_now.z : seen_now.x, half ? seen_now.w : seen_now.y};
+        const bool whole = (there[0] & there[1]) == 0xffffffffu && k0 >= lo && k0 + 64 <= hi;
         const bool masked = __any_sync(0xffffffffu, !whole);
         wait(s_full(i), tile & 1);
         tc_fence_after();
-        uint32_t v[4][32];
+        uint32_t v[2][32];
 #pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) tmem_ld32(cs, v[q4], 32 * q4);
+        for (int q4 = 0; q4 < 2; ++q4) tmem_ld32(cs + 64 * half, v[q4], 32 * q4);
 #pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) tmem_wait_ld(v[q4]);
+        for (int q4 = 0; q4 < 2; ++q4) tmem_wait_ld(v[q4]);
         if (masked) {
 #pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4) {
-            const uint32_t w = q4 == 0 ? there.x : q4 == 1 ? there.y : q4 == 2 ? there.z : there.w;
+          for (int q4 = 0; q4 < 2; ++q4) {
             const int f = k0 + 32 * q4, lo1 = min(max(lo - f, 0), 32), hi1 = min(max(hi - f, 0), 32);
-            const uint32_t ok = w & (hi1 >= 32 ? 0xffffffffu : (1u << hi1) - 1u) & (lo1 >= 32 ? 0u : 0xffffffffu << lo1);
+            const uint32_t ok = there[q4] & (hi1 >= 32 ? 0xffffffffu : (1u << hi1) - 1u) & (lo1 >= 32 ? 0u : 0xffffffffu << lo1);
 #pragma unroll
             for (int x = 0; x < 32; ++x) v[q4][x] = ok >> x & 1 ? v[q4][x] : 0xff800000u;
           }
         }
         float mx4[4];
 #pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) {
-          mx4[q4] = __uint_as_float(v[q4][0]);
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t(&w)[32] = v[q >> 1];
+          const int x0 = 16 * (q & 1);
+          mx4[q] = __uint_as_float(w[x0]);
 #pragma unroll
-          for (int x = 1; x < 31; x += 2) mx4[q4] = fmaxf(mx4[q4], fmaxf(__uint_as_float(v[q4][x]), __uint_as_float(v[q4][x + 1])));
-          mx4[q4] = fmaxf(mx4[q4], __uint_as_float(v[q4][31]));
+          for (int x = 1; x < 15; x += 2) mx4[q] = fmaxf(mx4[q], fmaxf(__uint_as_float(w[x0 + x]), __uint_as_float(w[x0 + x + 1])));
+          mx4[q] = fmaxf(mx4[q], __uint_as_float(w[x0 + 15]));
         }
-        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-        const float top = mx * c;
-        // the reference moves only when a score exceeds it by 2^8: weights stay below 256, and the sums above are rarely scaled
-        const bool move = top > m + 8.f;
-        if (__any_sync(0xffffffffu, move || fv != 1.f)) {
-          float f = !move ? 1.f : m == -INFINITY ? 0.f : exp2f(m - top);
+        float top = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;
+        // The reference moves only when a score exceeds it by 2^8: weights stay below 256, and the sums are rarely scaled.
+        // All threads of the tile learn here whether any row moves; from here on no score is needed in tensor memory.
+        if (bar_any(1 + i, 256, top > m + 8.f || fv != 1.f)) {
+          *mine = top;
+          named_sync(1 + i, 256);
+          top = fmaxf(top, *theirs);
+          const bool move = top > m + 8.f;
+          float f = !move ? 1.f : m == -INFINITY ? 0.f : ex2(m - top);
           if (move) m = top;
           l *= f;
           f *= fv;
-          if (j > s.t0) {
+          if (j > s.t0 && __any_sync(0xffffffffu, f != 1.f)) {
             wait(pv_done(i), (tile - 1) & 1);
             tc_fence_after();
 #pragma unroll 1
-            for (int q4 = 0; q4 < D / 32; ++q4) {
-              uint32_t v[32];
-              tmem_ld32(co, v, 32 * q4);
-              tmem_wait_ld(v);
+            for (int q4 = 0; q4 < D / 64; ++q4) {
+              uint32_t y[32];
+              tmem_ld32(co, y, 32 * q4);
+              tmem_wait_ld(y);
 #pragma unroll
-              for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * f);
-              tmem_st16(co + 32 * q4, v);
-              tmem_st16(co + 32 * q4 + 16, v + 16);
+              for (int x = 0; x < 32; ++x) y[x] = __float_as_uint(__uint_as_float(y[x]) * f);
+              tmem_st16(co + 32 * q4, y);
+              tmem_st16(co + 32 * q4 + 16, y + 16);
             }
           }
+          named_sync(1 + i, 256);   // the exchanged maxima have been read
         }
         const float ref = (m == -INFINITY ? 0.f : m) - dv;   // weights come out times 2^(E - reference exponent)
         const uint64_t c2 = pair2(c, c), r2 = pair2(-ref, -ref);
         uint64_t sums[2] = {0, 0};
 #pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) {
+        for (int q4 = 0; q4 < 2; ++q4) {
           uint32_t p[16];
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
@@ -987,8 +1034,8 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
             sums[x & 1] = add2(sums[x & 1], pair2(w.x, w.y));
             p[x] = half2_bits(w.x, w.y);
           }
-          // the weights of 32 keys take 16 of the columns the scores held
-          tmem_st16(cs + 16 * q4, p);
+          // the weights of 128 keys take the first 64 columns of the scores
+          tmem_st16(cs + 32 * half + 16 * q4, p);
         }
         const float2 sum2 = unpair2(add2(sums[0], sums[1]));
         const float sum = sum2.x + sum2.y;
@@ -1002,12 +1049,16 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
       wait(pv_done(i), (tile - 1) & 1);
       tc_fence_after();
       const bool cut = s.t0 > 0 || s.t1 < s.nt;
+      *mine = l;
+      named_sync(1 + i, 256);
+      l += *theirs;
+      named_sync(1 + i, 256);
       const float up = exp2f((float)vref);
       if (!cut) {
         const float f = l > 0.f ? up / l : 0.f;
-        uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + oat);
+        uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + oat + half * (D / 2));
 #pragma unroll 1
-        for (int q4 = 0; q4 < D / 32; ++q4) {
+        for (int q4 = 0; q4 < D / 64; ++q4) {
           uint32_t v[32];
           tmem_ld32(co, v, 32 * q4);
           tmem_wait_ld(v);
@@ -1027,16 +1078,16 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
         // slot 2 c: the item began before this CTA; 2 c + 1: it goes on behind it
         float4* part = reinterpret_cast<float4*>(a.p.part) + (int64_t)(2 * blockIdx.x + (s.t0 == 0 ? 1 : 0)) * (D / 4 + 1) * kItemRows;
 #pragma unroll 1
-        for (int q4 = 0; q4 < D / 32; ++q4) {
+        for (int q4 = 0; q4 < D / 64; ++q4) {
           uint32_t v[32];
           tmem_ld32(co, v, 32 * q4);
           tmem_wait_ld(v);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            part[(8 * q4 + k) * kItemRows + 128 * i + r] =
+            part[(D / 8 * half + 8 * q4 + k) * kItemRows + 128 * i + r] =
                 make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]), __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]));
         }
-        part[(D / 4) * kItemRows + 128 * i + r] = make_float4(m, l, up, 0.f);
+        if (half == 0) part[(D / 4) * kItemRows + 128 * i + r] = make_float4(m, l, up, 0.f);
       }
       tc_fence_before();
       __syncwarp();
@@ -1046,7 +1097,7 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512u) : "memory");
+  if (warp == 17) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512u) : "memory");
 }
 
 // Grid: (CTAs of flash, D / 16): an item that begins in CTA c and goes on behind it; thread = row, 16 coordinates per CTA.
