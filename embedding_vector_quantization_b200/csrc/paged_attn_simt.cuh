@@ -26,6 +26,7 @@ struct AttnArgs {
   CacheView kc, vc;
   float scale;
   int causal, window, nsplit, tile_rows;
+  int small_rows;  // > 0: only sequences with at most this many query rows are prepared (paged_decode.cuh)
   float* qr;       // [ntok * Hq][dk] rotated queries (general kernels)
   float* part;     // partial results
   void* out;
@@ -93,10 +94,16 @@ __global__ void __launch_bounds__(kAppThreads) paged_qprep_kernel(AttnArgs a) {
   float* part_s = ys + (size_t)R * w;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row0 = (int64_t)blockIdx.x * R, rows = a.bt.ntok * a.Hq;
+  __shared__ int wanted;
+  grid_dep_launch();
+  if (tid == 0) wanted = 0;
+  __syncthreads();
   for (int r = warp; r < R; r += kAppThreads / 32) {
     const int64_t row = row0 + r, t = row / a.Hq;
     const int h = (int)(row - t * a.Hq);
-    const int b = row < rows ? warp_find_seq(a.bt, t) : -1;
+    int b = row < rows ? warp_find_seq(a.bt, t) : -1;
+    if (b >= 0 && a.small_rows > 0 && seq_tokens(a.bt, b) * a.G > a.small_rows) b = -1;
+    if (b >= 0 && lane == 0) wanted = 1;
     float z[8];
 #pragma unroll
     for (int c = 0; c < 8; ++c) z[c] = 0.f;
@@ -114,6 +121,7 @@ __global__ void __launch_bounds__(kAppThreads) paged_qprep_kernel(AttnArgs a) {
       if (lane + 32 * c < d) zf[r * d + lane + 32 * c] = z[c];
   }
   __syncthreads();
+  if (!wanted) return;
   const float s1 = a.scale * 1.44269504089f, s2 = m > 0 ? s1 * kQjlScale / (float)m : 0.f;
   rows_matvec<R>(zf, d, a.k.PiT, d, part_s, ys);
   for (int e = tid; e < R * d; e += kAppThreads) {

@@ -1,0 +1,601 @@
+// Attention of a few query rows per sequence (single tokens, G <= 8 query heads per KV head) over paged caches: d = 64 or
+// 128, 2- or 4-bit codes, with or without d signs.
+//
+// Bound by the bytes of the packed rows, so the rows go from the page to the tensor cores' registers with as few
+// instructions as possible. A chunk is 16 tokens of one page (pages are multiples of 16): its codes, signs and norms are
+// contiguous, and a warp streams its chunks through a ring of its own with 16-byte asynchronous copies. Scores are
+// m16n8k16 products with the 16 tokens as rows and the query rows as columns: a lane's operand registers are pairs of
+// coordinates of one token, which a table turns out of one packed byte (a copy of the table for each bank, so that no two
+// lanes meet). Coordinates are numbered so that a lane's share of a token's row is contiguous. The value product has
+// coordinates as rows and tokens as its inner dimension: two tokens' table entries, interleaved; its weights are the scores'
+// registers, transposed across the warp (movmatrix). Weights carry the value norms (times a power of two that keeps them
+// below 2^12), the sums stay in the codes' domain and the merge rotates them back.
+//
+// Work is cut evenly: CTA c of P takes units [c U / P, (c + 1) U / P) of the batch's U chunks (sequence by sequence, head by
+// head), whatever the sequences' lengths; a CTA's part of one (sequence, head) is one partial result.
+#pragma once
+
+#include "paged_flash.cuh"
+
+namespace tqk {
+namespace paged {
+
+constexpr int kDcWarps = 8, kDcThreads = 32 * kDcWarps;
+constexpr int kDcMaxB = 2048;    // sequences whose running sums fit shared memory
+constexpr int kChunk = 16;
+
+template <int D, int BK, int BV, bool SG>
+struct DcLayout {
+  static constexpr int kRowK = D * BK / 8, kRowV = D * BV / 8, kRowS = SG ? D / 8 : 0;
+  // one chunk: codes, signs, norms, residual norms of the keys, then of the values
+  static constexpr int kSignK = kChunk * kRowK, kNormK = kSignK + kChunk * kRowS, kEndK = kNormK + (SG ? 64 : 32) * 2;
+  static constexpr int kSignV = kEndK + kChunk * kRowV, kNormV = kSignV + kChunk * kRowS, kStage = kNormV + (SG ? 64 : 32) * 2;
+  static constexpr int kDV = D + (SG ? D : 0);
+  static constexpr int kStages = BK == BV ? 4 : 3;   // two tables leave room for one stage less (two CTAs per SM)
+  static constexpr uint32_t kLutK = 0, kLutV = BK == BV ? 0 : 32768;
+  static constexpr uint32_t kRing = kLutV + 32768;
+  static constexpr uint32_t kRingBytes = kDcWarps * kStages * kStage;
+  static constexpr uint32_t kMerge = kDcWarps * 8 * kDV * 4;                  // the warps' sums, over the ring
+  static constexpr uint32_t kStat = kRing + (kRingBytes > kMerge ? kRingBytes : kMerge);   // float [8 warps][8 rows][2]
+  static constexpr uint32_t kPre = kStat + kDcWarps * 64;                     // int64 [B + 1]
+};
+
+struct DecodeArgs {
+  AttnArgs a;
+  int ctas;
+};
+
+__device__ __forceinline__ int small_tokens(const AttnArgs& a, int b) {
+  const int n = seq_tokens(a.bt, b);
+  return n > 0 && n * a.G <= a.small_rows ? n : 0;
+}
+// Chunks of one head of sequence b, and its first.
+__device__ __forceinline__ int small_chunks(const AttnArgs& a, int b, int n, int& first) {
+  first = 0;
+  if (n == 0) return 0;
+  int lo, hi;
+  key_range(a.bt, b, 0, n - 1, n, a.causal, a.window, lo, hi);
+  first = lo / kChunk;
+  return hi > lo ? (hi + kChunk - 1) / kChunk - first : 0;
+}
+
+// Running sums over the sequences of chunks * Hkv into pre[0 .. B], by the whole CTA of NT threads.
+template <int NT>
+__device__ __forceinline__ void chunk_sums(const AttnArgs& a, int64_t* pre, int64_t* warp_s) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int64_t done = 0;
+  for (int b0 = 0; b0 < a.bt.B; b0 += NT) {
+    const int b = b0 + tid;
+    int64_t v = 0;
+    if (b < a.bt.B) {
+      int first;
+      v = (int64_t)small_chunks(a, b, small_tokens(a, b), first) * a.Hkv;
+    }
+    int64_t incl = v;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    if (lane == 31) warp_s[warp] = incl;
+    __syncthreads();
+    int64_t before = done;
+    for (int w = 0; w < warp; ++w) before += warp_s[w];
+    if (b < a.bt.B) pre[b] = before + incl - v;
+    for (int w = 0; w < NT / 32; ++w) done += warp_s[w];
+    __syncthreads();
+  }
+  if (tid == 0) pre[a.bt.B] = done;
+  __syncthreads();
+}
+
+__device__ __forceinline__ int last_at_or_before64(const int64_t* start, int n, int64_t x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (start[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
+// Byte offset of (token row r, byte o) among a chunk's rows of RB bytes: rows and 32-byte halves trade places so that the
+// lanes of one access (tokens r, r + 4 together, or t + 4 j for t = 0 .. 3) fall into different banks.
+template <int RB>
+__device__ __forceinline__ int spot(int r, int o) {
+  if (RB == 64) return ((r >> 1) << 7) + (((r & 1) ^ ((r >> 2) & 1)) << 6) + (o ^ (((r >> 1) & 1) << 5));
+  if (RB == 32) return ((r >> 2) << 7) + (((r & 3) ^ (((r >> 2) & 1) << 1)) << 5) + o;
+  return r * RB + o;
+}
+// N bytes (2, 4, 8 or 16) from shared memory as words.
+template <int N>
+__device__ __forceinline__ void lds_bytes(uint32_t a, uint32_t* w) {
+  if (N == 16) {
+    const uint4 v = lds128(a);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else if (N == 8) {
+    const uint2 v = lds64(a);
+    w[0] = v.x, w[1] = v.y;
+  } else if (N == 4) {
+    w[0] = lds32(a);
+  } else {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(v) : "r"(a));
+    w[0] = v;
+  }
+}
+__device__ __forceinline__ float lds_half(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(v) : "r"(a));
+  return __half2float(__ushort_as_half(v));
+}
+// The pairs of coordinates in byte i of w: 4 bits one pair, 2 bits two (x: coordinates 0, 1; y: 2, 3).
+template <int B>
+__device__ __forceinline__ uint2 lut_byte(uint32_t w, int i, uint32_t lut4, uint32_t lut8) {
+  if (B == 4) return make_uint2(lds32(lut4 + byte128(w, i)), 0);
+  return lds64(lut8 + byte128(w, i));
+}
+
+template <int D, int BK, int BV, bool SG, bool NF16>
+__global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs da) {
+  using L = DcLayout<D, BK, BV, SG>;
+  extern __shared__ __align__(128) unsigned char smem_dc[];
+  const AttnArgs& a = da.a;
+  const uint32_t base = smem_addr(smem_dc);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  int64_t* pre = reinterpret_cast<int64_t*>(smem_dc + L::kPre);
+  float* stat = reinterpret_cast<float*>(smem_dc + L::kStat);   // [warp][row] maximum, then [warp][row] sum
+  __shared__ int64_t warp_s[kDcWarps];
+  grid_dep_launch();
+  chunk_sums<kDcThreads>(a, pre, warp_s);
+  const int64_t U = pre[a.bt.B];
+  const Span sp = span_of(U, blockIdx.x, gridDim.x);
+  if (sp.u0 >= sp.u1) return;
+  build_lut(a.k, smem_dc + L::kLutK, tid, kDcThreads);
+  if (BK != BV) build_lut(a.v, smem_dc + L::kLutV, tid, kDcThreads);
+  __syncthreads();
+  const uint32_t lutk = base + L::kLutK, lutv = base + L::kLutV;
+  const uint32_t k4 = lutk + 4 * lane, k8 = lutk + 8 * (lane & 15), v4 = lutv + 4 * lane, v8 = lutv + 8 * (lane & 15);
+  const uint32_t ring = base + L::kRing + warp * L::kStages * L::kStage;
+  constexpr int KB = L::kRowK / 4, VB = L::kRowV / 8;      // bytes of a row that a lane reads
+  constexpr int KW = (KB + 3) / 4, VW = (VB + 3) / 4;
+  constexpr int KS = D / 16;                               // inner steps of the score product, and row tiles of the value one
+  const int tk = (g >> 1) + 4 * (g & 1);                   // the token of score row g (row g + 8: 8 later)
+  grid_dep_wait();
+
+  for (int64_t u = sp.u0; u < sp.u1;) {
+    const int b = last_at_or_before64(pre, a.bt.B, u);
+    const int n = small_tokens(a, b);
+    int first;
+    const int nch = small_chunks(a, b, n, first);
+    const int h = (int)((u - pre[b]) / nch);
+    const int64_t item_u = pre[b] + (int64_t)h * nch;
+    const int c0 = (int)(u - item_u), c1 = (int)(min(sp.u1, item_u + nch) - item_u);
+    u = item_u + nch;
+    const int tok0 = a.bt.q_start[b], rows = n * a.G, len = a.bt.len[b];
+    int lo_all, hi_all;
+    key_range(a.bt, b, 0, n - 1, n, a.causal, a.window, lo_all, hi_all);
+    // rows 2 t, 2 t + 1 are this lane's columns: the keys they see
+    int lo[2], hi[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int r = 2 * t + j, pos = len - n + r / a.G;
+      lo[j] = 0, hi[j] = r < rows ? hi_all : 0;
+      if (a.causal) {
+        hi[j] = min(hi[j], pos + 1);
+        if (a.window > 0) lo[j] = max(0, pos - a.window + 1);
+      }
+    }
+    // ---- queries: row g, this lane's coordinates, as f16 times a power of two
+    uint32_t qc[2 * KS], qs[SG ? 2 * KS : 1];
+    float fc[2], fs[2];
+    {
+      constexpr int DK = D + (SG ? D : 0);
+      const float* src = a.qr + ((int64_t)(tok0 + g / a.G) * a.Hq + h * a.G + g % a.G) * DK;
+      float z[D / 4];
+      float top = 0.f;
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x) {
+        const float4 v = g < rows ? *reinterpret_cast<const float4*>(src + t * (D / 4) + 4 * x) : make_float4(0, 0, 0, 0);
+        z[4 * x] = v.x, z[4 * x + 1] = v.y, z[4 * x + 2] = v.z, z[4 * x + 3] = v.w;
+      }
+#pragma unroll
+      for (int x = 0; x < D / 4; ++x) top = fmaxf(top, fabsf(z[x]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      int e = 0;
+      if (top > 0.f && top < INFINITY) frexpf(top, &e);
+      float dn = ldexpf(1.f, -e), upf = ldexpf(1.f, e);
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+        qc[2 * s] = half2_bits(z[4 * s] * dn, z[4 * s + 1] * dn), qc[2 * s + 1] = half2_bits(z[4 * s + 2] * dn, z[4 * s + 3] * dn);
+      fc[0] = __shfl_sync(0xffffffffu, upf, 8 * t), fc[1] = __shfl_sync(0xffffffffu, upf, 8 * t + 4);
+      if (SG) {
+        // this lane's signs are those of projections t D/4 .. : step s takes pairs (i, i + D/8), i = 2 s, 2 s + 1
+        top = 0.f;
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          const float4 v = g < rows ? *reinterpret_cast<const float4*>(src + D + t * (D / 4) + 4 * x) : make_float4(0, 0, 0, 0);
+          z[4 * x] = v.x, z[4 * x + 1] = v.y, z[4 * x + 2] = v.z, z[4 * x + 3] = v.w;
+        }
+#pragma unroll
+        for (int x = 0; x < D / 4; ++x) top = fmaxf(top, fabsf(z[x]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        e = 0;
+        if (top > 0.f && top < INFINITY) frexpf(top, &e);
+        dn = ldexpf(1.f, -e), upf = ldexpf(1.f, e);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          qs[2 * s] = half2_bits(z[2 * s] * dn, z[2 * s + D / 8] * dn);
+          qs[2 * s + 1] = half2_bits(z[2 * s + 1] * dn, z[2 * s + 1 + D / 8] * dn);
+        }
+        fs[0] = __shfl_sync(0xffffffffu, upf, 8 * t), fs[1] = __shfl_sync(0xffffffffu, upf, 8 * t + 4);
+      }
+    }
+    float oc[KS][4], os[SG ? KS : 1][4];
+#pragma unroll
+    for (int x = 0; x < KS; ++x)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) oc[x][j] = 0.f;
+#pragma unroll
+    for (int x = 0; x < (SG ? KS : 1); ++x)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) os[x][j] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    int ve = 0;           // value norms are taken times 2^-ve
+    float vdn = 0.f;      // 2^-ve; 0: no value yet
+
+    // ---- the warp's chunks: c0 + warp, + 8, ...; the ring holds those under way
+    const int mine = c1 - c0 > warp ? (c1 - c0 - warp + kDcWarps - 1) / kDcWarps : 0;
+    unsigned there = 0;   // bit (i mod 32): chunk i lies on a valid page
+    const int64_t hrow = (int64_t)h * a.bt.page_size;
+    auto fetch = [&](int i) {
+      bool ok = false;
+      if (i < mine) {
+        const int p = (first + c0 + warp + i * kDcWarps) * kChunk;
+        const int pi = p / a.bt.page_size, slot = p - pi * a.bt.page_size;
+        const int64_t page = a.bt.table[(int64_t)b * a.bt.max_pages + pi];
+        ok = page >= 0 && page < a.bt.num_pages;
+        if (ok) {
+          const int64_t at = page * a.Hkv * a.bt.page_size + hrow + slot;   // row of the chunk's first token
+          const uint32_t st = ring + (i % L::kStages) * L::kStage;
+          const uint8_t* ck = a.kc.codes + at * L::kRowK;
+          const uint8_t* cv = a.vc.codes + at * L::kRowV;
+#pragma unroll
+          for (int x = lane; x < kChunk * L::kRowK / 16; x += 32) {
+            const int r = x / (L::kRowK / 16), o = (x % (L::kRowK / 16)) * 16;
+            cp16(st + spot<L::kRowK>(r, o), ck + 16 * x);
+          }
+#pragma unroll
+          for (int x = lane; x < kChunk * L::kRowV / 16; x += 32) {
+            const int r = x / (L::kRowV / 16), o = (x % (L::kRowV / 16)) * 16;
+            cp16(st + L::kEndK + spot<L::kRowV>(r, o), cv + 16 * x);
+          }
+          if (SG) {
+            constexpr int NS = kChunk * L::kRowS / 16;
+            if (lane < NS) cp16(st + L::kSignK + 16 * lane, a.kc.signs + at * L::kRowS + 16 * lane);
+            else if (lane < 2 * NS) cp16(st + L::kSignV + 16 * (lane - NS), a.vc.signs + at * L::kRowS + 16 * (lane - NS));
+          }
+          constexpr int NB = NF16 ? 2 : 4;   // bytes of a norm
+          const char* nk = static_cast<const char*>(a.kc.norms) + at * NB;
+          const char* nv = static_cast<const char*>(a.vc.norms) + at * NB;
+          if (lane < NB) cp16(st + L::kNormK + 16 * lane, nk + 16 * lane);
+          else if (lane < 2 * NB) cp16(st + L::kNormV + 16 * (lane - NB), nv + 16 * (lane - NB));
+          else if (SG && lane < 2 * NB + 2) cp16(st + L::kNormK + 64 + 16 * (lane - 2 * NB), a.kc.rnorms + at + 8 * (lane - 2 * NB));
+          else if (SG && lane < 2 * NB + 4) cp16(st + L::kNormV + 64 + 16 * (lane - 2 * NB - 2), a.vc.rnorms + at + 8 * (lane - 2 * NB - 2));
+        } else if (lane == 0) {
+          report_error(a.err, kErrPaged);
+        }
+      }
+      there = ok ? there | 1u << (i & 31) : there & ~(1u << (i & 31));
+      asm volatile("cp.async.commit_group;\n" ::: "memory");
+    };
+    for (int i = 0; i < L::kStages - 1; ++i) fetch(i);
+    for (int i = 0; i < mine; ++i) {
+      __syncwarp();   // the stage that is filled next has been read by every lane
+      fetch(i + L::kStages - 1);
+      asm volatile("cp.async.wait_group %0;\n" ::"n"(L::kStages - 1) : "memory");
+      __syncwarp();
+      if (!(there >> (i & 31) & 1)) continue;
+      const uint32_t st = ring + (i % L::kStages) * L::kStage;
+      const int key0 = (first + c0 + warp + i * kDcWarps) * kChunk;
+      auto norm_at = [&](uint32_t off, int r) -> float {
+        if (NF16) return lds_half(st + off + 2 * r);
+        return __uint_as_float(lds32(st + off + 4 * r));
+      };
+      // ---- scores of tokens tk, tk + 8 (rows g, g + 8) for query rows 2 t, 2 t + 1
+      float s1[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
+      {
+        uint32_t w0[KW], w1[KW];
+        lds_bytes<KB>(st + spot<L::kRowK>(tk, KB * t), w0);
+        lds_bytes<KB>(st + spot<L::kRowK>(tk + 8, KB * t), w1);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          uint32_t a0, a1, a2, a3;
+          if (BK == 4) {
+            a0 = lut_byte<4>(w0[s >> 1], 2 * (s & 1), k4, k8).x, a2 = lut_byte<4>(w0[s >> 1], 2 * (s & 1) + 1, k4, k8).x;
+            a1 = lut_byte<4>(w1[s >> 1], 2 * (s & 1), k4, k8).x, a3 = lut_byte<4>(w1[s >> 1], 2 * (s & 1) + 1, k4, k8).x;
+          } else {
+            const uint2 x = lut_byte<2>(w0[s >> 2], s & 3, k4, k8), y = lut_byte<2>(w1[s >> 2], s & 3, k4, k8);
+            a0 = x.x, a2 = x.y, a1 = y.x, a3 = y.y;
+          }
+          mma16816(s1, a0, a1, a2, a3, qc[2 * s], qc[2 * s + 1]);
+        }
+        if (SG) {
+          uint32_t x, y;
+          if (D == 128) {
+            lds_bytes<4>(st + L::kSignK + tk * L::kRowS + 4 * t, &x);
+            lds_bytes<4>(st + L::kSignK + (tk + 8) * L::kRowS + 4 * t, &y);
+          } else {   // 16 signs: the upper eight to bits 16 .. 23
+            lds_bytes<2>(st + L::kSignK + tk * L::kRowS + 2 * t, &x);
+            lds_bytes<2>(st + L::kSignK + (tk + 8) * L::kRowS + 2 * t, &y);
+            x = __byte_perm(x, 0, 0x4140), y = __byte_perm(y, 0, 0x4140);
+          }
+          x = ~x, y = ~y;
+#pragma unroll
+          for (int s = 0; s < KS; ++s) {
+            auto two = [](uint32_t w, int k) { return ((w << (15 - k)) & 0x80008000u) ^ 0x3C003C00u; };
+            mma16816(s2, two(x, 2 * s), two(y, 2 * s), two(x, 2 * s + 1), two(y, 2 * s + 1), qs[2 * s], qs[2 * s + 1]);
+          }
+        }
+      }
+      const int kA = key0 + tk, kB = kA + 8;
+      const float nA = norm_at(L::kNormK, tk), nB = norm_at(L::kNormK, tk + 8);
+      float rA = 0.f, rB = 0.f;
+      if (SG) rA = lds_half(st + L::kNormK + 64 + 2 * tk), rB = lds_half(st + L::kNormK + 64 + 2 * (tk + 8));
+      float x[4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        x[j] = s1[j] * (nA * fc[j]);
+        x[2 + j] = s1[2 + j] * (nB * fc[j]);
+        if (SG) x[j] = fmaf(s2[j], rA * fs[j], x[j]), x[2 + j] = fmaf(s2[2 + j], rB * fs[j], x[2 + j]);
+        if (!(kA >= lo[j] && kA < hi[j])) x[j] = -INFINITY;
+        if (!(kB >= lo[j] && kB < hi[j])) x[2 + j] = -INFINITY;
+      }
+      // value norms; a token behind the sequence's end counts for nothing, whatever its slot holds
+      float vA = kA < hi_all ? norm_at(L::kNormV, tk) : 0.f, vB = kB < hi_all ? norm_at(L::kNormV, tk + 8) : 0.f;
+      float wA = 0.f, wB = 0.f;
+      if (SG) {
+        wA = kA < hi_all ? lds_half(st + L::kNormV + 64 + 2 * tk) : 0.f;
+        wB = kB < hi_all ? lds_half(st + L::kNormV + 64 + 2 * (tk + 8)) : 0.f;
+      }
+      const float vt = fmaxf(vA, vB);
+      const bool up0 = fmaxf(x[0], x[2]) > m[0] + 8.f || fmaxf(x[1], x[3]) > m[1] + 8.f || vt * vdn > 16.f || vdn == 0.f;
+      if (__any_sync(0xffffffffu, up0)) {   // rarely: a reference moves
+        float f[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float top = fmaxf(x[j], x[2 + j]);
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          f[j] = 1.f;
+          if (top > m[j]) f[j] = m[j] == -INFINITY ? 0.f : ex2(m[j] - top), m[j] = top;
+          l[j] *= f[j];
+        }
+        float vm = vt < INFINITY ? vt : 0.f;
+        for (int o = 16; o; o >>= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+        if (vdn == 0.f || vm * vdn > 16.f) {
+          int e = -126;
+          if (vm > 0.f) frexpf(vm, &e);
+          e = max(-126, min(126, e));
+          if (vdn != 0.f) {
+            const float fv = ex2((float)max(ve - e, -126));
+            f[0] *= fv, f[1] *= fv;
+          }
+          ve = e, vdn = ldexpf(1.f, -e);
+        }
+#pragma unroll
+        for (int y = 0; y < KS; ++y) {
+          oc[y][0] *= f[0], oc[y][1] *= f[1], oc[y][2] *= f[0], oc[y][3] *= f[1];
+          if (SG) os[y][0] *= f[0], os[y][1] *= f[1], os[y][2] *= f[0], os[y][3] *= f[1];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float ref = m[j] == -INFINITY ? 0.f : m[j];
+        x[j] = ex2(x[j] - ref), x[2 + j] = ex2(x[2 + j] - ref);
+        l[j] += x[j] + x[2 + j];
+      }
+      vA *= vdn, vB *= vdn;
+      const uint32_t b0 = movmatrix(half2_bits(x[0] * vA, x[1] * vA)), b1 = movmatrix(half2_bits(x[2] * vB, x[3] * vB));
+      // ---- values: lane (g, t) holds coordinates g D/8 .. of tokens t, t + 4, t + 8, t + 12
+      {
+        uint32_t w[4][VW];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) lds_bytes<VB>(st + L::kEndK + spot<L::kRowV>(t + 4 * j, VB * g), w[j]);
+        if (BV == 4) {
+#pragma unroll
+          for (int y = 0; y < KS; ++y) {   // byte y: coordinates 2 y, 2 y + 1 -> rows g, g + 8 of tile y
+            uint32_t v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = lut_byte<4>(w[j][y >> 2], y & 3, v4, v8).x;
+            mma16816(oc[y], __byte_perm(v[0], v[1], 0x5410), __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x5410),
+                     __byte_perm(v[2], v[3], 0x7632), b0, b1);
+          }
+        } else {
+#pragma unroll
+          for (int y = 0; y < KS / 2; ++y) {   // byte y: coordinates 4 y .. 4 y + 3 -> tiles 2 y, 2 y + 1
+            uint2 v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = lut_byte<2>(w[j][y >> 2], y & 3, v4, v8);
+            mma16816(oc[2 * y], __byte_perm(v[0].x, v[1].x, 0x5410), __byte_perm(v[0].x, v[1].x, 0x7632),
+                     __byte_perm(v[2].x, v[3].x, 0x5410), __byte_perm(v[2].x, v[3].x, 0x7632), b0, b1);
+            mma16816(oc[2 * y + 1], __byte_perm(v[0].y, v[1].y, 0x5410), __byte_perm(v[0].y, v[1].y, 0x7632),
+                     __byte_perm(v[2].y, v[3].y, 0x5410), __byte_perm(v[2].y, v[3].y, 0x7632), b0, b1);
+          }
+        }
+        if (SG) {   // lane (g, t): signs of projections g D/8 .. of its four tokens; two tokens in one word
+          wA *= vdn, wB *= vdn;
+          const uint32_t r0 = movmatrix(half2_bits(x[0] * wA, x[1] * wA)), r1 = movmatrix(half2_bits(x[2] * wB, x[3] * wB));
+          uint32_t sg[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (D == 128) {
+              lds_bytes<2>(st + L::kSignV + (t + 4 * j) * L::kRowS + 2 * g, &sg[j]);
+            } else {
+              uint32_t v;
+              asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(v) : "r"(st + L::kSignV + (t + 4 * j) * L::kRowS + g));
+              sg[j] = v;
+            }
+          }
+          const uint32_t p = ~__byte_perm(sg[0], sg[1], 0x5410), q = ~__byte_perm(sg[2], sg[3], 0x5410);
+#pragma unroll
+          for (int y = 0; y < KS; ++y) {
+            auto two = [](uint32_t w2, int k) { return ((w2 << (15 - k)) & 0x80008000u) ^ 0x3C003C00u; };
+            mma16816(os[y], two(p, 2 * y), two(p, 2 * y + 1), two(q, 2 * y), two(q, 2 * y + 1), r0, r1);
+          }
+        }
+      }
+    }
+    asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+    // ---- the warps' results, merged in their order
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      l[j] += __shfl_xor_sync(0xffffffffu, l[j], 4);
+      l[j] += __shfl_xor_sync(0xffffffffu, l[j], 8);
+      l[j] += __shfl_xor_sync(0xffffffffu, l[j], 16);
+    }
+    if (g == 0) {
+      stat[warp * 8 + 2 * t] = m[0], stat[warp * 8 + 2 * t + 1] = m[1];
+      stat[64 + warp * 8 + 2 * t] = l[0], stat[64 + warp * 8 + 2 * t + 1] = l[1];
+    }
+    __syncthreads();   // every warp is done with the ring
+    float top[2];
+    {
+      const float upv = vdn == 0.f ? 0.f : ex2((float)ve);
+      float f[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        top[j] = -INFINITY;
+        for (int w = 0; w < kDcWarps; ++w) top[j] = fmaxf(top[j], stat[w * 8 + 2 * t + j]);
+        f[j] = m[j] == -INFINITY ? 0.f : ex2(m[j] - top[j]) * upv;
+      }
+      // sums [warp][coordinate][row]
+      float* o = reinterpret_cast<float*>(smem_dc + L::kRing) + warp * 8 * L::kDV;
+#pragma unroll
+      for (int y = 0; y < KS; ++y) {
+        const int c = g * (D / 8) + 2 * y;
+        *reinterpret_cast<float2*>(o + c * 8 + 2 * t) = make_float2(oc[y][0] * f[0], oc[y][1] * f[1]);
+        *reinterpret_cast<float2*>(o + (c + 1) * 8 + 2 * t) = make_float2(oc[y][2] * f[0], oc[y][3] * f[1]);
+        if (SG) {
+          *reinterpret_cast<float2*>(o + (D + c) * 8 + 2 * t) = make_float2(os[y][0] * f[0], os[y][1] * f[1]);
+          *reinterpret_cast<float2*>(o + (D + c + 1) * 8 + 2 * t) = make_float2(os[y][2] * f[0], os[y][3] * f[1]);
+        }
+      }
+    }
+    __syncthreads();
+    float* part = a.part + ((int64_t)blockIdx.x + (int64_t)b * a.Hkv + h) * 8 * (L::kDV + 2);
+    const float* o = reinterpret_cast<const float*>(smem_dc + L::kRing);
+    for (int e = tid; e < 8 * L::kDV; e += kDcThreads) {   // [coordinate][row]
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < kDcWarps; ++w) s += o[w * 8 * L::kDV + e];
+      part[e] = s;
+    }
+    if (tid < 8) {
+      float mt = -INFINITY, lt = 0.f;
+      for (int w = 0; w < kDcWarps; ++w) mt = fmaxf(mt, stat[w * 8 + tid]);
+      for (int w = 0; w < kDcWarps; ++w) lt += stat[w * 8 + tid] == -INFINITY ? 0.f : stat[64 + w * 8 + tid] * ex2(stat[w * 8 + tid] - mt);
+      part[8 * L::kDV + tid] = mt, part[8 * L::kDV + 8 + tid] = lt;
+    }
+    __syncthreads();   // before the ring and the statistics are written again
+  }
+}
+
+// Grid: (B, Hkv): the rows of one (sequence, head): its CTAs' parts merged in order, then o = (Pi_V^T acc + c S_V^T acc_s) / sum.
+__global__ void __launch_bounds__(kAppThreads) paged_decode_merge_kernel(DecodeArgs da) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  const AttnArgs& a = da.a;
+  constexpr int R = 8;
+  const int d = a.v.d, m = a.v.m, dv = d + m, b = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
+  float* acc = reinterpret_cast<float*>(smem);        // [8][d], then [8][m]
+  float* acc2 = acc + R * d;
+  float* o1 = acc2 + R * m;                           // [8][d]
+  float* o2 = o1 + R * d;
+  float* part_s = o2 + R * d;
+  __shared__ float f[R];
+  __shared__ int64_t sums[kAppThreads / 32 + 2];
+  const int n = small_tokens(a, b);
+  if (n == 0) return;
+  int first;
+  const int nch = small_chunks(a, b, n, first);
+  // the units before this sequence, and all of them
+  int64_t before = 0, all = 0;
+  for (int x = tid; x < a.bt.B; x += kAppThreads) {
+    int f0;
+    const int64_t v = (int64_t)small_chunks(a, x, small_tokens(a, x), f0) * a.Hkv;
+    all += v;
+    if (x < b) before += v;
+  }
+  for (int o = 16; o; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o), all += __shfl_xor_sync(0xffffffffu, all, o);
+  __shared__ int64_t sums2[kAppThreads / 32];
+  if ((tid & 31) == 0) sums[tid >> 5] = before, sums2[tid >> 5] = all;
+  __syncthreads();
+  before = all = 0;
+  for (int w = 0; w < kAppThreads / 32; ++w) before += sums[w], all += sums2[w];
+  const int P = da.ctas;
+  const int64_t u0 = before + (int64_t)h * nch, u1 = u0 + nch;
+  // CTA c has unit u when all c / P <= u < all (c + 1) / P (floors)
+  int ca = 0, cb = -1;
+  if (nch > 0) {
+    ca = (int)(u0 * P / all);
+    while (span_of(all, ca, P).u1 <= u0) ++ca;
+    while (ca > 0 && span_of(all, ca, P).u0 > u0) --ca;
+    cb = (int)((u1 - 1) * P / all);
+    while (span_of(all, cb, P).u1 <= u1 - 1) ++cb;
+    while (cb > 0 && span_of(all, cb, P).u0 > u1 - 1) --cb;
+  }
+  grid_dep_wait();
+  const int64_t size = 8 * (int64_t)(dv + 2);
+  const float* part = a.part + ((int64_t)b * a.Hkv + h) * size;
+  for (int e = tid; e < R * dv; e += kAppThreads) {
+    const int r = e & 7, j = e >> 3;
+    float top = -INFINITY, v = 0.f, sum = 0.f;
+    for (int c = ca; c <= cb; ++c) {
+      const Span q = span_of(all, c, P);
+      if (q.u0 >= q.u1) continue;
+      top = fmaxf(top, part[c * size + 8 * dv + r]);
+    }
+    if (top != -INFINITY)
+      for (int c = ca; c <= cb; ++c) {
+        const Span q = span_of(all, c, P);
+        if (q.u0 >= q.u1) continue;
+        const float* p = part + c * size;
+        const float mc = p[8 * dv + r];
+        const float w = mc == -INFINITY ? 0.f : ex2(mc - top);
+        v = fmaf(w, p[e], v);
+        sum = fmaf(w, p[8 * dv + 8 + r], sum);
+      }
+    if (j < d) acc[r * d + j] = v;
+    else acc2[r * m + j - d] = v;
+    if (j == 0) f[r] = sum > 0.f ? 1.f / sum : 0.f;
+  }
+  __syncthreads();
+  rows_matvec<R>(acc, d, a.v.Pi, d, part_s, o1);
+  if (m > 0) rows_matvec<R>(acc2, m, a.v.S, d, part_s, o2);
+  const int64_t tok0 = a.bt.q_start[b];
+  for (int e = tid; e < R * d; e += kAppThreads) {
+    const int r = e / d, i = e - r * d;
+    if (r >= n * a.G) continue;
+    float v = o1[e];
+    if (m > 0) v = fmaf(kQjlScale / (float)m, o2[e], v);
+    store_any(a.out, a.q_dtype, ((tok0 + r / a.G) * a.Hq + h * a.G + r % a.G) * d + i, v * f[r]);
+  }
+}
+
+}  // namespace paged
+}  // namespace tqk

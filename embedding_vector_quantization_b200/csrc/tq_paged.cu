@@ -17,6 +17,7 @@
 #include "paged_append.cuh"
 #include "paged_attn_simt.cuh"
 #include "paged_flash.cuh"
+#include "paged_decode.cuh"
 
 namespace {
 
@@ -335,13 +336,97 @@ int attn_flash(const AttnArgs& g, const tq_view& k, const tq_view& v, const Flas
   return st;
 }
 
-constexpr int kSmallRows = 0;   // sequences with at most this many query rows go to the general kernels
+// ---------------------------------------------------------------- attention of single tokens
 
-// The largest of what the paths of a call may need.
+constexpr int kSmallRows = 8;   // query rows of a sequence and KV head that the single-token kernel takes: its product's columns
+
+// Whether the single-token kernel has these formats: 4- or 2-bit codes, signs on both sides or on neither.
+bool decode_formats(const tq_view& k, const tq_view& v, const Batch& b) {
+  if (!flash_formats(k, v) || k.norm_dtype != v.norm_dtype || b.B > kDcMaxB) return false;
+  if (k.m > 0 || v.m > 0) return k.m == k.d && v.m == v.d && k.bits == 2 && v.bits == 2;
+  return (k.bits == 4 && (v.bits == 4 || v.bits == 2)) || (k.bits == 2 && v.bits == 2);
+}
+
+struct DecodePlan {
+  int ctas;
+  size_t qr, part, total;
+};
+
+DecodePlan decode_plan(const tq_view& k, const tq_view& v, const Batch& b, int Hq, int Hkv, int sms) {
+  DecodePlan p{};
+  p.ctas = 2 * sms;
+  p.qr = 0;
+  p.part = up((size_t)b.ntok * Hq * (k.d + k.m) * 4, 256);
+  p.total = p.part + up(((size_t)p.ctas + (size_t)b.B * Hkv) * 8 * (v.d + v.m + 2) * 4, 256) + 256;
+  return p;
+}
+
+// A launch that may start while the kernel before it drains (that kernel's results are read after griddepcontrol.wait).
+template <typename K, typename A>
+int launch_after(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, const A& args, const char* what) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid, cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at, cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args);
+  if (e != cudaSuccess) return fail(TQ_ECUDA, "%s: %s", what, cudaGetErrorString(e));
+  return launched(what);
+}
+
+template <int D, int BK, int BV, bool SG, bool NF16>
+int decode_launch(const DecodeArgs& a, int device, cudaStream_t s) {
+  static std::atomic<uint64_t> seen{0};
+  using L = DcLayout<D, BK, BV, SG>;
+  if (int st = allow_smem(paged_decode_kernel<D, BK, BV, SG, NF16>, L::kPre + (kDcMaxB + 1) * 8, device, seen)) return st;
+  tq_launch_scope scope("paged_decode", s);
+  return launch_after(paged_decode_kernel<D, BK, BV, SG, NF16>, dim3(a.ctas), kDcThreads, L::kPre + (size_t)(a.a.bt.B + 1) * 8, s, a,
+                      "paged_decode_kernel");
+}
+
+template <int D, bool NF16>
+int decode_formats_launch(const DecodeArgs& a, int device, cudaStream_t s) {
+  if (a.a.k.m > 0) return decode_launch<D, 2, 2, true, NF16>(a, device, s);
+  if (a.a.k.bits == 2) return decode_launch<D, 2, 2, false, NF16>(a, device, s);
+  return a.a.v.bits == 4 ? decode_launch<D, 4, 4, false, NF16>(a, device, s) : decode_launch<D, 4, 2, false, NF16>(a, device, s);
+}
+
+int attn_decode_paged(AttnArgs a, const tq_view& k, const tq_view& v, const DecodePlan& p, char* ws, cudaStream_t s) {
+  static std::atomic<uint64_t> s1{0}, s2{0};
+  constexpr int R = 8;
+  const size_t merge = (size_t)R * (256 + 256 + 2 * 256) * 4 + (size_t)kAppThreads * R * 4;
+  int st;
+  if ((st = allow_smem(paged_qprep_kernel<R>, qprep_smem_bytes(256, 256, R), k.device, s1)) ||
+      (st = allow_smem(paged_decode_merge_kernel, merge, k.device, s2)))
+    return st;
+  a.qr = reinterpret_cast<float*>(ws + p.qr);
+  a.part = reinterpret_cast<float*>(ws + p.part);
+  a.small_rows = kSmallRows;
+  {
+    tq_launch_scope scope("paged_qprep", s);
+    paged_qprep_kernel<R><<<(unsigned)((a.bt.ntok * a.Hq + R - 1) / R), kAppThreads, qprep_smem_bytes(k.d, k.m, R), s>>>(a);
+  }
+  if ((st = launched("paged_qprep_kernel"))) return st;
+  DecodeArgs da{};
+  da.a = a, da.ctas = p.ctas;
+  const bool h = k.norm_dtype == TQ_F16;
+  if (k.d == 128) st = h ? decode_formats_launch<128, true>(da, k.device, s) : decode_formats_launch<128, false>(da, k.device, s);
+  else st = h ? decode_formats_launch<64, true>(da, k.device, s) : decode_formats_launch<64, false>(da, k.device, s);
+  if (st) return st;
+  tq_launch_scope scope("paged_dmerge", s);
+  return launch_after(paged_decode_merge_kernel, dim3((unsigned)a.bt.B, (unsigned)a.Hkv), kAppThreads, merge, s, da, "paged_decode_merge_kernel");
+}
+
+// The largest of what the paths of a call may need; they run one after the other in the same space.
 size_t attn_workspace(const tq_view& k, const tq_view& v, const Batch& b, int Hq, int Hkv) {
   const int sms = device_sms(k.device);
   size_t n = simt_plan(k, v, b, Hq, Hkv, sms).total;
-  if (flash_formats(k, v)) n = std::max(n, flash_plan(k, b, Hq, Hkv, kSmallRows, sms).total);
+  if (flash_formats(k, v)) {
+    const int small = decode_formats(k, v, b) ? kSmallRows : 0;
+    if (small) n = std::max(n, decode_plan(k, v, b, Hq, Hkv, sms).total);
+    if ((int64_t)b.max_q * (Hq / Hkv) > small) n = std::max(n, flash_plan(k, b, Hq, Hkv, small, sms).total);
+  }
   return n;
 }
 
@@ -420,8 +505,12 @@ int tq_attn_paged(const tq_handle* hk, const tq_handle* hv, const void* q, int q
   char* ws = reinterpret_cast<char*>(up(reinterpret_cast<size_t>(workspace), 256));
   const int sms = device_sms(kw.device);
   if (q_dtype != TQ_F32 && flash_formats(kw, vw)) {
-    const FlashPlan plan = flash_plan(kw, a.bt, Hq, Hkv, kSmallRows, sms);
-    return kw.d == 128 ? attn_flash<128>(a, kw, vw, plan, kSmallRows, ws, s) : attn_flash<64>(a, kw, vw, plan, kSmallRows, ws, s);
+    const int G = Hq / Hkv, small = decode_formats(kw, vw, a.bt) ? kSmallRows : 0;
+    st = TQ_OK;
+    if (G <= small) st = attn_decode_paged(a, kw, vw, decode_plan(kw, vw, a.bt, Hq, Hkv, sms), ws, s);
+    if (st || (int64_t)a.bt.max_q * G <= small) return st;
+    const FlashPlan plan = flash_plan(kw, a.bt, Hq, Hkv, small, sms);
+    return kw.d == 128 ? attn_flash<128>(a, kw, vw, plan, small, ws, s) : attn_flash<64>(a, kw, vw, plan, small, ws, s);
   }
   return attn_simt(a, kw, vw, simt_plan(kw, vw, a.bt, Hq, Hkv, sms), ws, kw.device, s);
 }
