@@ -26,7 +26,7 @@ struct AttnArgs {
   CacheView kc, vc;
   float scale;
   int causal, window, nsplit, tile_rows;
-  int small_rows;  // > 0: only sequences with at most this many query rows are prepared (paged_decode.cuh)
+  int small_rows;  // the single-token kernels: sequences with at most this many query rows
   float* qr;       // [ntok * Hq][dk] rotated queries (general kernels)
   float* part;     // partial results
   void* out;
@@ -79,12 +79,18 @@ __device__ __forceinline__ void key_range(const Batch& bt, int b, int i0, int i1
   hi = max(hi, lo);
 }
 
+// What the rotated query of a row holds that sees nothing, because its rotation position is out of range: one bit pattern
+// of NaN (a NaN of a computed query is another).
+#define TQ_BLIND_BITS 0x7fb1b1b1
+#define kBlind __int_as_float(TQ_BLIND_BITS)
+__device__ __forceinline__ bool is_blind(float x) { return __float_as_int(x) == TQ_BLIND_BITS; }
+
 __host__ __device__ inline size_t qprep_smem_bytes(int d, int m, int R) {
   const int w = d > m ? d : m;
   return (size_t)R * d * 4 + (size_t)R * w * 4 + (size_t)kAppThreads * R * 4;
 }
 
-// Grid: ceil(ntok * Hq / R). Rows that are padding or whose rotation position is out of range get q' = 0.
+// Grid: ceil(ntok * Hq / R). Rows of padding get q' = 0, rows whose rotation position is out of range kBlind.
 template <int R>
 __global__ void __launch_bounds__(kAppThreads) paged_qprep_kernel(AttnArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
@@ -93,17 +99,14 @@ __global__ void __launch_bounds__(kAppThreads) paged_qprep_kernel(AttnArgs a) {
   float* ys = zf + (size_t)R * d;
   float* part_s = ys + (size_t)R * w;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ int blind[R];
   const int64_t row0 = (int64_t)blockIdx.x * R, rows = a.bt.ntok * a.Hq;
-  __shared__ int wanted;
-  grid_dep_launch();
-  if (tid == 0) wanted = 0;
+  if (tid < R) blind[tid] = 0;
   __syncthreads();
   for (int r = warp; r < R; r += kAppThreads / 32) {
     const int64_t row = row0 + r, t = row / a.Hq;
     const int h = (int)(row - t * a.Hq);
-    int b = row < rows ? warp_find_seq(a.bt, t) : -1;
-    if (b >= 0 && a.small_rows > 0 && seq_tokens(a.bt, b) * a.G > a.small_rows) b = -1;
-    if (b >= 0 && lane == 0) wanted = 1;
+    const int b = row < rows ? warp_find_seq(a.bt, t) : -1;
     float z[8];
 #pragma unroll
     for (int c = 0; c < 8; ++c) z[c] = 0.f;
@@ -112,6 +115,7 @@ __global__ void __launch_bounds__(kAppThreads) paged_qprep_kernel(AttnArgs a) {
       if (a.prep.cos_sin && (p < 0 || p >= a.prep.max_pos)) {
         // (a negative position of its own needs no report: the row sees nothing)
         if (lane == 0 && (a.prep.pos || p >= 0)) report_error(a.err, kErrPaged);
+        if (lane == 0) blind[r] = 1;
       } else {
         prep_head<float, 8>(a.q, a.q_dtype, t * a.q_stride + (int64_t)h * d, d, a.prep, p, z);
       }
@@ -121,12 +125,11 @@ __global__ void __launch_bounds__(kAppThreads) paged_qprep_kernel(AttnArgs a) {
       if (lane + 32 * c < d) zf[r * d + lane + 32 * c] = z[c];
   }
   __syncthreads();
-  if (!wanted) return;
   const float s1 = a.scale * 1.44269504089f, s2 = m > 0 ? s1 * kQjlScale / (float)m : 0.f;
   rows_matvec<R>(zf, d, a.k.PiT, d, part_s, ys);
   for (int e = tid; e < R * d; e += kAppThreads) {
     const int r = e / d;
-    if (row0 + r < rows) a.qr[(row0 + r) * dk + (e - r * d)] = ys[e] * s1;
+    if (row0 + r < rows) a.qr[(row0 + r) * dk + (e - r * d)] = blind[r] ? kBlind : ys[e] * s1;
   }
   if (m == 0) return;
   __syncthreads();
@@ -219,7 +222,7 @@ __global__ void __launch_bounds__(kAttThreads) paged_attn_simt_kernel(AttnArgs a
       float s = 0.f;
       for (int i = 0; i < dk; ++i) s = fmaf(qs[r * dk + i], kv[t * ld + i], s);
       const int row = tl.row0 + r, p = pos_first + row / a.G, key = t0 + t;
-      bool seen = r < tl.nrows && at_k[t] >= 0;
+      bool seen = r < tl.nrows && at_k[t] >= 0 && !is_blind(qs[r * dk]);
       if (a.causal) seen = seen && key <= p && (a.window <= 0 || key > p - a.window);
       sc[e] = seen ? s : -INFINITY;
     }

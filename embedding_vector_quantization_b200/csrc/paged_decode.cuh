@@ -31,13 +31,19 @@ struct DcLayout {
   static constexpr int kSignK = kChunk * kRowK, kNormK = kSignK + kChunk * kRowS, kEndK = kNormK + (SG ? 64 : 32) * 2;
   static constexpr int kSignV = kEndK + kChunk * kRowV, kNormV = kSignV + kChunk * kRowS, kStage = kNormV + (SG ? 64 : 32) * 2;
   static constexpr int kDV = D + (SG ? D : 0);
-  static constexpr int kStages = BK == BV ? 4 : 3;   // two tables leave room for one stage less (two CTAs per SM)
-  static constexpr uint32_t kLutK = 0, kLutV = BK == BV ? 0 : 32768;
-  static constexpr uint32_t kRing = kLutV + 32768;
-  static constexpr uint32_t kRingBytes = kDcWarps * kStages * kStage;
-  static constexpr uint32_t kMerge = kDcWarps * 8 * kDV * 4;                  // the warps' sums, over the ring
-  static constexpr uint32_t kStat = kRing + (kRingBytes > kMerge ? kRingBytes : kMerge);   // float [8 warps][8 rows][2]
-  static constexpr uint32_t kPre = kStat + kDcWarps * 64;                     // int64 [B + 1]
+  // Two CTAs per SM: two tables leave room for one stage less; a warp's ring also holds its sums at an item's end.
+  static constexpr int kStages = BK != BV ? 3 : SG && D == 128 ? 5 : 4;
+  static constexpr int kWarpRing = kStages * kStage;
+  static_assert(kWarpRing >= 8 * kDV * 4, "a warp's sums must fit its ring");
+  // The tables lie at a multiple of 32 KB of the shared window, so that a packed byte's offset and the lane's are or-ed
+  // into the address; as many warps' rings as fit lie before them, the others, then the statistics behind.
+  static constexpr int kTables = BK == BV ? 1 : 2;
+  static constexpr int kFrontWarps = (32768 - 2048) / kWarpRing < kDcWarps ? (32768 - 2048) / kWarpRing : kDcWarps;
+  static constexpr uint32_t kBack = kTables * 32768;                                    // from the tables on
+  static constexpr uint32_t kStat = kBack + (kDcWarps - kFrontWarps) * kWarpRing;       // float [2][8 warps][8 rows]
+  static constexpr uint32_t kPre = kStat + kDcWarps * 64;                               // int64 [B + 1]
+  // dynamic shared memory for B sequences: the window begins at most 2 KB (static and reserved memory) in
+  static constexpr size_t bytes(int B) { return 32768 + kPre + (size_t)(B + 1) * 8; }
 };
 
 struct DecodeArgs {
@@ -142,10 +148,11 @@ __device__ __forceinline__ float lds_half(uint32_t a) {
   return __half2float(__ushort_as_half(v));
 }
 // The pairs of coordinates in byte i of w: 4 bits one pair, 2 bits two (x: coordinates 0, 1; y: 2, 3).
+// at4, at8: the lane's copy in the table's first row, at a multiple of 32 KB.
 template <int B>
-__device__ __forceinline__ uint2 lut_byte(uint32_t w, int i, uint32_t lut4, uint32_t lut8) {
-  if (B == 4) return make_uint2(lds32(lut4 + byte128(w, i)), 0);
-  return lds64(lut8 + byte128(w, i));
+__device__ __forceinline__ uint2 lut_byte(uint32_t w, int i, uint32_t at4, uint32_t at8) {
+  if (B == 4) return make_uint2(lds32(byte128(w, i) | at4), 0);
+  return lds64(byte128(w, i) | at8);
 }
 
 template <int D, int BK, int BV, bool SG, bool NF16>
@@ -153,22 +160,28 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
   using L = DcLayout<D, BK, BV, SG>;
   extern __shared__ __align__(128) unsigned char smem_dc[];
   const AttnArgs& a = da.a;
-  const uint32_t base = smem_addr(smem_dc);
+  const uint32_t base = smem_addr(smem_dc), lut = (base + 32767u) & ~32767u;
+  unsigned char* const tables = smem_dc + (lut - base);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  int64_t* pre = reinterpret_cast<int64_t*>(smem_dc + L::kPre);
-  float* stat = reinterpret_cast<float*>(smem_dc + L::kStat);   // [warp][row] maximum, then [warp][row] sum
+  int64_t* pre = reinterpret_cast<int64_t*>(tables + L::kPre);
+  float* stat = reinterpret_cast<float*>(tables + L::kStat);   // [warp][row] maximum, then [warp][row] sum
   __shared__ int64_t warp_s[kDcWarps];
+  if (lut - base < L::kFrontWarps * L::kWarpRing) {   // more static memory than expected
+    if (tid == 0) report_error(a.err, kErrInternal);
+    return;
+  }
   grid_dep_launch();
   chunk_sums<kDcThreads>(a, pre, warp_s);
   const int64_t U = pre[a.bt.B];
   const Span sp = span_of(U, blockIdx.x, gridDim.x);
   if (sp.u0 >= sp.u1) return;
-  build_lut(a.k, smem_dc + L::kLutK, tid, kDcThreads);
-  if (BK != BV) build_lut(a.v, smem_dc + L::kLutV, tid, kDcThreads);
+  build_lut(a.k, tables, tid, kDcThreads);
+  if (BK != BV) build_lut(a.v, tables + 32768, tid, kDcThreads);
   __syncthreads();
-  const uint32_t lutk = base + L::kLutK, lutv = base + L::kLutV;
-  const uint32_t k4 = lutk + 4 * lane, k8 = lutk + 8 * (lane & 15), v4 = lutv + 4 * lane, v8 = lutv + 8 * (lane & 15);
-  const uint32_t ring = base + L::kRing + warp * L::kStages * L::kStage;
+  const uint32_t k4 = lut | 4 * lane, k8 = lut | 8 * (lane & 15);
+  const uint32_t v4 = k4 + (L::kTables - 1) * 32768, v8 = k8 + (L::kTables - 1) * 32768;
+  const uint32_t ring_off = warp < L::kFrontWarps ? warp * L::kWarpRing : lut - base + L::kBack + (warp - L::kFrontWarps) * L::kWarpRing;
+  const uint32_t ring = base + ring_off;
   constexpr int KB = L::kRowK / 4, VB = L::kRowV / 8;      // bytes of a row that a lane reads
   constexpr int KW = (KB + 3) / 4, VW = (VB + 3) / 4;
   constexpr int KS = D / 16;                               // inner steps of the score product, and row tiles of the value one
@@ -206,11 +219,18 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
       const float* src = a.qr + ((int64_t)(tok0 + g / a.G) * a.Hq + h * a.G + g % a.G) * DK;
       float z[D / 4];
       float top = 0.f;
+      bool blind = false;
 #pragma unroll
       for (int x = 0; x < D / 16; ++x) {
         const float4 v = g < rows ? *reinterpret_cast<const float4*>(src + t * (D / 4) + 4 * x) : make_float4(0, 0, 0, 0);
         z[4 * x] = v.x, z[4 * x + 1] = v.y, z[4 * x + 2] = v.z, z[4 * x + 3] = v.w;
       }
+      blind = is_blind(z[0]);
+#pragma unroll
+      for (int x = 0; x < D / 4; ++x) z[x] = blind ? 0.f : z[x];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (__shfl_sync(0xffffffffu, (int)blind, 8 * t + 4 * j)) hi[j] = 0;
 #pragma unroll
       for (int x = 0; x < D / 4; ++x) top = fmaxf(top, fabsf(z[x]));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -227,7 +247,7 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
         top = 0.f;
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
-          const float4 v = g < rows ? *reinterpret_cast<const float4*>(src + D + t * (D / 4) + 4 * x) : make_float4(0, 0, 0, 0);
+          const float4 v = g < rows && !blind ? *reinterpret_cast<const float4*>(src + D + t * (D / 4) + 4 * x) : make_float4(0, 0, 0, 0);
           z[4 * x] = v.x, z[4 * x + 1] = v.y, z[4 * x + 2] = v.z, z[4 * x + 3] = v.w;
         }
 #pragma unroll
@@ -245,6 +265,9 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
         fs[0] = __shfl_sync(0xffffffffu, upf, 8 * t), fs[1] = __shfl_sync(0xffffffffu, upf, 8 * t + 4);
       }
     }
+    int lo_w = max(lo[0], lo[1]), hi_w = min(2 * t < rows ? hi[0] : INT_MAX, 2 * t + 1 < rows ? hi[1] : INT_MAX);
+    lo_w = max(lo_w, __shfl_xor_sync(0xffffffffu, lo_w, 1)), lo_w = max(lo_w, __shfl_xor_sync(0xffffffffu, lo_w, 2));
+    hi_w = min(hi_w, __shfl_xor_sync(0xffffffffu, hi_w, 1)), hi_w = min(hi_w, __shfl_xor_sync(0xffffffffu, hi_w, 2));
     float oc[KS][4], os[SG ? KS : 1][4];
 #pragma unroll
     for (int x = 0; x < KS; ++x)
@@ -261,16 +284,17 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
     // ---- the warp's chunks: c0 + warp, + 8, ...; the ring holds those under way
     const int mine = c1 - c0 > warp ? (c1 - c0 - warp + kDcWarps - 1) / kDcWarps : 0;
     unsigned there = 0;   // bit (i mod 32): chunk i lies on a valid page
-    const int64_t hrow = (int64_t)h * a.bt.page_size;
+    const int cpp = a.bt.page_size / kChunk;   // chunks of a page
+    const uint32_t inv = cpp > 1 ? (uint32_t)(0xffffffffu / (uint32_t)cpp) + 1u : 0u;   // exact below 2^26 chunks
+    const int32_t* tab = a.bt.table + (int64_t)b * a.bt.max_pages;
     auto fetch = [&](int i) {
       bool ok = false;
       if (i < mine) {
-        const int p = (first + c0 + warp + i * kDcWarps) * kChunk;
-        const int pi = p / a.bt.page_size, slot = p - pi * a.bt.page_size;
-        const int64_t page = a.bt.table[(int64_t)b * a.bt.max_pages + pi];
+        const uint32_t ch = first + c0 + warp + i * kDcWarps, pi = cpp > 1 ? __umulhi(ch, inv) : ch;
+        const int page = tab[pi];
         ok = page >= 0 && page < a.bt.num_pages;
         if (ok) {
-          const int64_t at = page * a.Hkv * a.bt.page_size + hrow + slot;   // row of the chunk's first token
+          const int64_t at = ((int64_t)(page * (uint64_t)a.Hkv + h) * cpp + (ch - pi * cpp)) * kChunk;   // row of its first token
           const uint32_t st = ring + (i % L::kStages) * L::kStage;
           const uint8_t* ck = a.kc.codes + at * L::kRowK;
           const uint8_t* cv = a.vc.codes + at * L::kRowV;
@@ -352,7 +376,6 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
           }
         }
       }
-      const int kA = key0 + tk, kB = kA + 8;
       const float nA = norm_at(L::kNormK, tk), nB = norm_at(L::kNormK, tk + 8);
       float rA = 0.f, rB = 0.f;
       if (SG) rA = lds_half(st + L::kNormK + 64 + 2 * tk), rB = lds_half(st + L::kNormK + 64 + 2 * (tk + 8));
@@ -362,15 +385,19 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
         x[j] = s1[j] * (nA * fc[j]);
         x[2 + j] = s1[2 + j] * (nB * fc[j]);
         if (SG) x[j] = fmaf(s2[j], rA * fs[j], x[j]), x[2 + j] = fmaf(s2[2 + j], rB * fs[j], x[2 + j]);
-        if (!(kA >= lo[j] && kA < hi[j])) x[j] = -INFINITY;
-        if (!(kB >= lo[j] && kB < hi[j])) x[2 + j] = -INFINITY;
       }
-      // value norms; a token behind the sequence's end counts for nothing, whatever its slot holds
-      float vA = kA < hi_all ? norm_at(L::kNormV, tk) : 0.f, vB = kB < hi_all ? norm_at(L::kNormV, tk + 8) : 0.f;
-      float wA = 0.f, wB = 0.f;
-      if (SG) {
-        wA = kA < hi_all ? lds_half(st + L::kNormV + 64 + 2 * tk) : 0.f;
-        wB = kB < hi_all ? lds_half(st + L::kNormV + 64 + 2 * (tk + 8)) : 0.f;
+      float vA = norm_at(L::kNormV, tk), vB = norm_at(L::kNormV, tk + 8), wA = 0.f, wB = 0.f;
+      if (SG) wA = lds_half(st + L::kNormV + 64 + 2 * tk), wB = lds_half(st + L::kNormV + 64 + 2 * (tk + 8));
+      if (key0 < lo_w || key0 + kChunk > hi_w) {   // some row does not see all of the chunk
+        const int kA = key0 + tk, kB = kA + 8;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (!(kA >= lo[j] && kA < hi[j])) x[j] = -INFINITY;
+          if (!(kB >= lo[j] && kB < hi[j])) x[2 + j] = -INFINITY;
+        }
+        // a token behind the sequence's end counts for nothing, whatever its slot holds
+        if (kA >= hi_all) vA = wA = 0.f;
+        if (kB >= hi_all) vB = wB = 0.f;
       }
       const float vt = fmaxf(vA, vB);
       const bool up0 = fmaxf(x[0], x[2]) > m[0] + 8.f || fmaxf(x[1], x[3]) > m[1] + 8.f || vt * vdn > 16.f || vdn == 0.f;
@@ -485,7 +512,7 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
         f[j] = m[j] == -INFINITY ? 0.f : ex2(m[j] - top[j]) * upv;
       }
       // sums [warp][coordinate][row]
-      float* o = reinterpret_cast<float*>(smem_dc + L::kRing) + warp * 8 * L::kDV;
+      float* o = reinterpret_cast<float*>(smem_dc + ring_off);
 #pragma unroll
       for (int y = 0; y < KS; ++y) {
         const int c = g * (D / 8) + 2 * y;
@@ -499,11 +526,12 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
     }
     __syncthreads();
     float* part = a.part + ((int64_t)blockIdx.x + (int64_t)b * a.Hkv + h) * 8 * (L::kDV + 2);
-    const float* o = reinterpret_cast<const float*>(smem_dc + L::kRing);
     for (int e = tid; e < 8 * L::kDV; e += kDcThreads) {   // [coordinate][row]
       float s = 0.f;
 #pragma unroll
-      for (int w = 0; w < kDcWarps; ++w) s += o[w * 8 * L::kDV + e];
+      for (int w = 0; w < kDcWarps; ++w)
+        s += reinterpret_cast<const float*>(w < L::kFrontWarps ? smem_dc + w * L::kWarpRing
+                                                               : tables + L::kBack + (w - L::kFrontWarps) * L::kWarpRing)[e];
       part[e] = s;
     }
     if (tid < 8) {
@@ -516,85 +544,162 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
   }
 }
 
-// Grid: (B, Hkv): the rows of one (sequence, head): its CTAs' parts merged in order, then o = (Pi_V^T acc + c S_V^T acc_s) / sum.
-__global__ void __launch_bounds__(kAppThreads) paged_decode_merge_kernel(DecodeArgs da) {
+// ---- the small products around it: 8 rows times 32 columns of a constant matrix per CTA
+
+// out[r][0 .. 31] = sum_i in[r][i] T[i][col .. col + 31] (row length ld) for 8 rows: warp w sums its eighth of i; the eight
+// parts meet in part_s ([8 warps][8 rows][32]) in a fixed order.
+__device__ __forceinline__ void rows_slice(const float* in, int ni, const float* T, int ld, int col, float* part_s, float* out) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, share = ni / 8;   // ni: a multiple of 32
+  float acc[8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r) acc[r] = 0.f;
+  const float* t = T + (size_t)(warp * share) * ld + col + lane;
+#pragma unroll 16
+  for (int i = 0; i < share; ++i) {
+    const float p = __ldg(t + (size_t)i * ld);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) acc[r] = fmaf(in[r * ni + warp * share + i], p, acc[r]);
+  }
+#pragma unroll
+  for (int r = 0; r < 8; ++r) part_s[(warp * 8 + r) * 32 + lane] = acc[r];
+  __syncthreads();
+  float s = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) s += part_s[w * 256 + tid];
+  out[tid] = s;   // [8][32]
+  __syncthreads();
+}
+
+// Queries of the small sequences. Grid: (8-row groups of (token, head), (d + m) / 32 column slices); 256 threads.
+__global__ void __launch_bounds__(256) paged_qslice_kernel(DecodeArgs da) {
+  __shared__ float zf[8 * 128], part_s[8 * 256], ys[256];
+  __shared__ int wanted;
+  const AttnArgs& a = da.a;
+  const int d = a.k.d, m = a.k.m, dk = d + m, tid = threadIdx.x, lane = tid & 31, r = tid >> 5;
+  const int64_t row0 = (int64_t)blockIdx.x * 8, rows = a.bt.ntok * a.Hq, row = row0 + r;
+  grid_dep_launch();
+  if (tid == 0) wanted = 0;
+  __syncthreads();
+  const int64_t t = row / a.Hq;
+  const int h = (int)(row - t * a.Hq);
+  int b = row < rows ? warp_find_seq(a.bt, t) : -1;
+  if (b >= 0 && small_tokens(a, b) == 0) b = -1;
+  float z[4] = {0.f, 0.f, 0.f, 0.f};
+  bool blind = false;
+  if (b >= 0) {
+    const int64_t p = a.prep.pos ? (int64_t)a.prep.pos[t] : (int64_t)a.bt.len[b] - a.bt.q_start[b + 1] + t;
+    if (lane == 0) wanted = 1;
+    if (a.prep.cos_sin && (p < 0 || p >= a.prep.max_pos)) {
+      if (lane == 0 && (a.prep.pos || p >= 0)) report_error(a.err, kErrPaged);
+      blind = true;   // it sees nothing
+    } else {
+      prep_head<float, 4>(a.q, a.q_dtype, t * a.q_stride + (int64_t)h * d, d, a.prep, p, z);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    if (lane + 32 * c < d) zf[r * d + lane + 32 * c] = z[c];
+  __syncthreads();
+  if (!wanted) return;
+  const int col = 32 * blockIdx.y;
+  const bool code = col < d;
+  rows_slice(zf, d, code ? a.k.PiT : a.k.ST, code ? d : m, code ? col : col - d, part_s, ys);
+  const float f = a.scale * 1.44269504089f * (code ? 1.f : kQjlScale / (float)m);
+  if (row < rows) a.qr[row * dk + col + lane] = blind ? kBlind : ys[tid] * f;
+}
+
+// Grid: (B, Hkv, d / 32): 32 coordinates of the rows of one (sequence, head): its CTAs' parts merged in order, then
+// o = (Pi_V^T acc + c S_V^T acc_s) / sum.
+__global__ void __launch_bounds__(256) paged_decode_merge_kernel(DecodeArgs da) {
   extern __shared__ __align__(16) unsigned char smem[];
   const AttnArgs& a = da.a;
-  constexpr int R = 8;
-  const int d = a.v.d, m = a.v.m, dv = d + m, b = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
+  const int d = a.v.d, m = a.v.m, dv = d + m, b = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int P = da.ctas;
   float* acc = reinterpret_cast<float*>(smem);        // [8][d], then [8][m]
-  float* acc2 = acc + R * d;
-  float* o1 = acc2 + R * m;                           // [8][d]
-  float* o2 = o1 + R * d;
-  float* part_s = o2 + R * d;
-  __shared__ float f[R];
-  __shared__ int64_t sums[kAppThreads / 32 + 2];
+  float* part_s = acc + 8 * dv;                       // [8][256]
+  float* o1 = part_s + 8 * 256;                       // [256]
+  float* o2 = o1 + 256;
+  float* wgt = o2 + 256;                              // [P][8] weights of the parts
+  int* cta = reinterpret_cast<int*>(wgt + 8 * P);     // [P] the CTAs that hold one
+  __shared__ int64_t sums[8], sums2[8];
+  __shared__ float f[8];
+  __shared__ int parts;
   const int n = small_tokens(a, b);
   if (n == 0) return;
   int first;
   const int nch = small_chunks(a, b, n, first);
   // the units before this sequence, and all of them
   int64_t before = 0, all = 0;
-  for (int x = tid; x < a.bt.B; x += kAppThreads) {
+  for (int x = tid; x < a.bt.B; x += 256) {
     int f0;
     const int64_t v = (int64_t)small_chunks(a, x, small_tokens(a, x), f0) * a.Hkv;
     all += v;
     if (x < b) before += v;
   }
   for (int o = 16; o; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o), all += __shfl_xor_sync(0xffffffffu, all, o);
-  __shared__ int64_t sums2[kAppThreads / 32];
-  if ((tid & 31) == 0) sums[tid >> 5] = before, sums2[tid >> 5] = all;
+  if (lane == 0) sums[warp] = before, sums2[warp] = all;
+  if (tid == 0) parts = 0;
   __syncthreads();
   before = all = 0;
-  for (int w = 0; w < kAppThreads / 32; ++w) before += sums[w], all += sums2[w];
-  const int P = da.ctas;
+  for (int w = 0; w < 8; ++w) before += sums[w], all += sums2[w];
   const int64_t u0 = before + (int64_t)h * nch, u1 = u0 + nch;
-  // CTA c has unit u when all c / P <= u < all (c + 1) / P (floors)
-  int ca = 0, cb = -1;
-  if (nch > 0) {
-    ca = (int)(u0 * P / all);
-    while (span_of(all, ca, P).u1 <= u0) ++ca;
-    while (ca > 0 && span_of(all, ca, P).u0 > u0) --ca;
-    cb = (int)((u1 - 1) * P / all);
-    while (span_of(all, cb, P).u1 <= u1 - 1) ++cb;
-    while (cb > 0 && span_of(all, cb, P).u0 > u1 - 1) --cb;
+  if (warp == 0) {   // the CTAs whose units meet [u0, u1), in order
+    int np = 0;
+    for (int c0 = 0; c0 < P; c0 += 32) {
+      const Span q = span_of(all, c0 + lane, P);
+      const bool in = c0 + lane < P && q.u0 < q.u1 && q.u0 < u1 && q.u1 > u0;
+      const unsigned who = __ballot_sync(0xffffffffu, in);
+      if (in) cta[np + __popc(who & ((1u << lane) - 1))] = c0 + lane;
+      np += __popc(who);
+    }
+    if (lane == 0) parts = np;
   }
   grid_dep_wait();
+  __syncthreads();
+  const int np = parts;
   const int64_t size = 8 * (int64_t)(dv + 2);
   const float* part = a.part + ((int64_t)b * a.Hkv + h) * size;
-  for (int e = tid; e < R * dv; e += kAppThreads) {
-    const int r = e & 7, j = e >> 3;
-    float top = -INFINITY, v = 0.f, sum = 0.f;
-    for (int c = ca; c <= cb; ++c) {
-      const Span q = span_of(all, c, P);
-      if (q.u0 >= q.u1) continue;
-      top = fmaxf(top, part[c * size + 8 * dv + r]);
+  {   // warp r: the weights of row r
+    float top = -INFINITY, sum = 0.f;
+    for (int c = lane; c < np; c += 32) top = fmaxf(top, part[cta[c] * size + 8 * dv + warp]);
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int c = lane; c < np; c += 32) {
+      const float* p = part + cta[c] * size + 8 * dv;
+      const float w = p[warp] == -INFINITY ? 0.f : ex2(p[warp] - top);
+      wgt[c * 8 + warp] = w;
+      sum = fmaf(w, p[8 + warp], sum);
     }
-    if (top != -INFINITY)
-      for (int c = ca; c <= cb; ++c) {
-        const Span q = span_of(all, c, P);
-        if (q.u0 >= q.u1) continue;
-        const float* p = part + c * size;
-        const float mc = p[8 * dv + r];
-        const float w = mc == -INFINITY ? 0.f : ex2(mc - top);
-        v = fmaf(w, p[e], v);
-        sum = fmaf(w, p[8 * dv + 8 + r], sum);
-      }
-    if (j < d) acc[r * d + j] = v;
-    else acc2[r * m + j - d] = v;
-    if (j == 0) f[r] = sum > 0.f ? 1.f / sum : 0.f;
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) f[warp] = sum > 0.f ? 1.f / sum : 0.f;
   }
   __syncthreads();
-  rows_matvec<R>(acc, d, a.v.Pi, d, part_s, o1);
-  if (m > 0) rows_matvec<R>(acc2, m, a.v.S, d, part_s, o2);
-  const int64_t tok0 = a.bt.q_start[b];
-  for (int e = tid; e < R * d; e += kAppThreads) {
-    const int r = e / d, i = e - r * d;
-    if (r >= n * a.G) continue;
-    float v = o1[e];
-    if (m > 0) v = fmaf(kQjlScale / (float)m, o2[e], v);
-    store_any(a.out, a.q_dtype, ((tok0 + r / a.G) * a.Hq + h * a.G + r % a.G) * d + i, v * f[r]);
+  {   // thread: elements tid, tid + 256, ... of the sums, all of row tid mod 8
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = 0.f;
+    const int nk = dv / 32;
+#pragma unroll 4
+    for (int c = 0; c < np; ++c) {
+      const float w = wgt[c * 8 + (tid & 7)];
+      const float* p = part + cta[c] * size + tid;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < nk) v[k] = fmaf(w, p[256 * k], v[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int e = tid + 256 * k, r = e & 7, j = e >> 3;
+      if (k < nk) acc[j < d ? r * d + j : 8 * d + r * m + j - d] = v[k];
+    }
   }
+  __syncthreads();
+  const int col = 32 * blockIdx.z;
+  rows_slice(acc, d, a.v.Pi, d, col, part_s, o1);
+  if (m > 0) rows_slice(acc + 8 * d, m, a.v.S, d, col, part_s, o2);
+  if (warp >= n * a.G) return;
+  float v = o1[tid];
+  if (m > 0) v = fmaf(kQjlScale / (float)m, o2[tid], v);
+  store_any(a.out, a.q_dtype, ((a.bt.q_start[b] + warp / a.G) * (int64_t)a.Hq + h * a.G + warp % a.G) * d + col + lane, v * f[warp]);
 }
 
 }  // namespace paged

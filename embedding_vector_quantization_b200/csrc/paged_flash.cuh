@@ -236,12 +236,13 @@ __device__ __forceinline__ void load_row(const Quant& Q, const CacheView& c, int
 // of a phase meet: 4 bits 4 B x 32 copies, 2 bits 8 B x 16, 1 bit 16 B x 8, 3 bits 64 pairs x 32.
 __device__ __forceinline__ void build_lut(const Quant& Q, uint8_t* lut, int tid, int nthreads) {
   if (Q.bits == 0) return;
-  const double* c = Q.cent64();
-  const int per = Q.bits == 3 ? 2 : 8 / Q.bits, bytes = 2 * per, copies = 128 / bytes, n = Q.bits == 3 ? 64 : 256;
-  for (int e = tid; e < n * per; e += nthreads) {
-    const int v = e / per, i = e - v * per;
-    const __half h = __double2half(c[(v >> (i * Q.bits)) & ((1 << Q.bits) - 1)]);
-    for (int k = 0; k < copies; ++k) *reinterpret_cast<__half*>(lut + v * 128 + k * bytes + 2 * i) = h;
+  // a warp per entry, a lane per word: lane l writes the pair l mod (words of an entry)
+  const int per = Q.bits == 3 ? 2 : 8 / Q.bits, n = Q.bits == 3 ? 64 : 256, mask = (1 << Q.bits) - 1;
+  const int lane = tid & 31, p = (lane & (per / 2 - 1)) * 2 * Q.bits;
+  const uint32_t own = __half_as_ushort(__float2half_rn(lane <= mask ? Q.cent[lane] : 0.f));   // lane i: centroid i
+  for (int v = tid >> 5; v < n; v += nthreads >> 5) {
+    const uint32_t x = __shfl_sync(0xffffffffu, own, v >> p & mask), y = __shfl_sync(0xffffffffu, own, v >> (p + Q.bits) & mask);
+    *reinterpret_cast<uint32_t*>(lut + v * 128 + 4 * lane) = x | y << 16;
   }
 }
 
@@ -255,19 +256,20 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
 }
-// (w >> 8 i & 255) * 128: byte i as a table offset
-__device__ __forceinline__ uint32_t byte128(uint32_t w, int i) { return ((i ? w >> (8 * i) : w) & 255u) << 7; }
+// (w >> 8 i & 255) * 128: byte i as a table offset, one shift and one mask
+__device__ __forceinline__ uint32_t byte128(uint32_t w, int i) { return (i == 0 ? w << 7 : w >> (8 * i - 7)) & 0x7f80u; }
 
 // Chunk c (8 coordinates, 16 bytes of f16) of a row's codes.
 template <int D>
 __device__ __forceinline__ uint4 code_chunk(const Row<D>& r, int bits, int c, uint32_t lut, int lane) {
   uint4 v = make_uint4(0, 0, 0, 0);
   if (bits == 4) {
-    const uint32_t w = r.code[c], b = lut + 4 * lane;
-    v = make_uint4(lds32(b + byte128(w, 0)), lds32(b + byte128(w, 1)), lds32(b + byte128(w, 2)), lds32(b + byte128(w, 3)));
+    const uint32_t w = r.code[c], b = 4 * lane;
+    v = make_uint4(lds32(lut + (byte128(w, 0) | b)), lds32(lut + (byte128(w, 1) | b)), lds32(lut + (byte128(w, 2) | b)),
+                   lds32(lut + (byte128(w, 3) | b)));
   } else if (bits == 2) {
-    const uint32_t w = r.code[c >> 1] >> (16 * (c & 1)), b = lut + 8 * (lane & 15);
-    const uint2 x = lds64(b + byte128(w, 0)), y = lds64(b + byte128(w, 1));
+    const uint32_t w = r.code[c >> 1], b = 8 * (lane & 15);
+    const uint2 x = lds64(lut + (byte128(w, 2 * (c & 1)) | b)), y = lds64(lut + (byte128(w, 2 * (c & 1) + 1) | b));
     v = make_uint4(x.x, x.y, y.x, y.y);
   } else if (bits == 1) {
     v = lds128(lut + 16 * (lane & 7) + (((r.code[c >> 2] >> (8 * (c & 3))) & 255u) << 7));

@@ -379,9 +379,9 @@ template <int D, int BK, int BV, bool SG, bool NF16>
 int decode_launch(const DecodeArgs& a, int device, cudaStream_t s) {
   static std::atomic<uint64_t> seen{0};
   using L = DcLayout<D, BK, BV, SG>;
-  if (int st = allow_smem(paged_decode_kernel<D, BK, BV, SG, NF16>, L::kPre + (kDcMaxB + 1) * 8, device, seen)) return st;
+  if (int st = allow_smem(paged_decode_kernel<D, BK, BV, SG, NF16>, L::bytes(kDcMaxB), device, seen)) return st;
   tq_launch_scope scope("paged_decode", s);
-  return launch_after(paged_decode_kernel<D, BK, BV, SG, NF16>, dim3(a.ctas), kDcThreads, L::kPre + (size_t)(a.a.bt.B + 1) * 8, s, a,
+  return launch_after(paged_decode_kernel<D, BK, BV, SG, NF16>, dim3(a.ctas), kDcThreads, L::bytes(a.a.bt.B), s, a,
                       "paged_decode_kernel");
 }
 
@@ -393,29 +393,27 @@ int decode_formats_launch(const DecodeArgs& a, int device, cudaStream_t s) {
 }
 
 int attn_decode_paged(AttnArgs a, const tq_view& k, const tq_view& v, const DecodePlan& p, char* ws, cudaStream_t s) {
-  static std::atomic<uint64_t> s1{0}, s2{0};
-  constexpr int R = 8;
-  const size_t merge = (size_t)R * (256 + 256 + 2 * 256) * 4 + (size_t)kAppThreads * R * 4;
+  static std::atomic<uint64_t> s1{0};
+  const size_t merge = (size_t)(8 * 256 + 8 * 256 + 512 + 9 * p.ctas) * 4;
   int st;
-  if ((st = allow_smem(paged_qprep_kernel<R>, qprep_smem_bytes(256, 256, R), k.device, s1)) ||
-      (st = allow_smem(paged_decode_merge_kernel, merge, k.device, s2)))
-    return st;
+  if ((st = allow_smem(paged_decode_merge_kernel, merge, k.device, s1))) return st;
   a.qr = reinterpret_cast<float*>(ws + p.qr);
   a.part = reinterpret_cast<float*>(ws + p.part);
   a.small_rows = kSmallRows;
-  {
-    tq_launch_scope scope("paged_qprep", s);
-    paged_qprep_kernel<R><<<(unsigned)((a.bt.ntok * a.Hq + R - 1) / R), kAppThreads, qprep_smem_bytes(k.d, k.m, R), s>>>(a);
-  }
-  if ((st = launched("paged_qprep_kernel"))) return st;
   DecodeArgs da{};
   da.a = a, da.ctas = p.ctas;
+  {
+    tq_launch_scope scope("paged_qprep", s);
+    paged_qslice_kernel<<<dim3((unsigned)((a.bt.ntok * a.Hq + 7) / 8), (k.d + k.m) / 32), 256, 0, s>>>(da);
+  }
+  if ((st = launched("paged_qslice_kernel"))) return st;
   const bool h = k.norm_dtype == TQ_F16;
   if (k.d == 128) st = h ? decode_formats_launch<128, true>(da, k.device, s) : decode_formats_launch<128, false>(da, k.device, s);
   else st = h ? decode_formats_launch<64, true>(da, k.device, s) : decode_formats_launch<64, false>(da, k.device, s);
   if (st) return st;
   tq_launch_scope scope("paged_dmerge", s);
-  return launch_after(paged_decode_merge_kernel, dim3((unsigned)a.bt.B, (unsigned)a.Hkv), kAppThreads, merge, s, da, "paged_decode_merge_kernel");
+  return launch_after(paged_decode_merge_kernel, dim3((unsigned)a.bt.B, (unsigned)a.Hkv, k.d / 32), 256, merge, s, da,
+                      "paged_decode_merge_kernel");
 }
 
 // The largest of what the paths of a call may need; they run one after the other in the same space.

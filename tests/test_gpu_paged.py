@@ -352,6 +352,24 @@ def test_attention_bad_pages(tq, dtype):
     fk.handle.status()
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("news", [[1, 2], [60, 1]])
+def test_attention_rotation_out_of_range(tq, news, dtype):
+    """A query whose rotation position is not in the table gets zeros (recorded); the others are untouched."""
+    c = attention_case(tq, 128, "mse4", "mse4", 1, 4, news, [100, 90], 16, dtype, "half")
+    fk, fv, bt, kc, vc, kr, vr, q, pr = c
+    pos = torch.randint(0, 4096, (bt.ntok,), generator=torch.Generator().manual_seed(3), dtype=torch.int32).cuda()
+    good = tq.HeadPrep(cos_sin=pr.cos_sin, pos=pos)
+    want = check_case(tq, (fk, fv, bt, kc, vc, kr, vr, q, good), 0.09, False, 0, H_FP32 if dtype == "fp32" else H_F16)
+    for wrong in (-1, 4096, 2 ** 31 - 1, -2 ** 31):
+        p2 = pos.clone()
+        p2[1] = wrong
+        got = tq.attn_paged(fk.handle, fv.handle, q, kc, vc, bt, 0.09, causal=False, prep=tq.HeadPrep(cos_sin=pr.cos_sin, pos=p2))
+        assert fk.handle.status() == tq.TQ_EINVAL and fk.handle.status() == tq.TQ_OK
+        keep = torch.arange(bt.ntok) != 1
+        assert (got[1] == 0).all() and torch.equal(got[keep.cuda()], want[keep.cuda()])
+
+
 def test_append_then_attend_as_a_server_does(tq):
     """Prompts in chunks, then decode steps, some sequences joining late: append and attend each step, both on a side
     stream, against attention over the package's own rows in 64 bits."""
