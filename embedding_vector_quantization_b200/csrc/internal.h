@@ -20,6 +20,7 @@ struct tq_view {
   const float *PiT, *Pi, *MT, *ST, *S, *cent, *bnd;   // fp32: [d][d], [d][d], [d][m], [d][m], [m][d], centroids, boundaries
   const double* t64;       // d <= 256: Pi [d][d], S [m][d], M [m][d], 16 boundaries (+inf padded), 16 centroids
   const uint8_t* ops16;    // d = 64 or 128 (m = 0 or d): f16 operands, of the paged expansion (tq_api.cu); NULL otherwise
+  const uint8_t* ops_app;  // d = 64 or 128 (m = 0 or d), with codes: f16 pairs of Pi and M (tq_api.cu); NULL otherwise
   float m_abs, m_norm;     // largest row of M in the 1-norm and the 2-norm
   int* err;                // device error word
   const double *cent_h, *bnd_h;   // host copies

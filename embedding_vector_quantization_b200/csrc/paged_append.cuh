@@ -102,8 +102,10 @@ __global__ void __launch_bounds__(kAppThreads) paged_append_kernel(AppendArgs a)
   }
   const int64_t row0 = (int64_t)blockIdx.x * R, rows = a.bt.ntok * a.Hkv;
   for (int r = warp; r < R; r += kAppThreads / 32) {
-    const int64_t row = row0 + r, t = row / a.Hkv;
-    const int h = (int)(row - t * a.Hkv);
+    const int64_t row = row0 + r;
+    int64_t t;
+    int h;
+    split_row(row, a.Hkv, t, h);
     const int b = row < rows ? warp_find_seq(a.bt, t) : -1;
     int64_t at = -1, rp = 0;
     bool bad = false;

@@ -63,10 +63,20 @@ __device__ __forceinline__ int seq_tokens(const Batch& bt, int b) {
   return lo >= 0 && hi > lo && hi <= bt.ntok ? hi - lo : 0;
 }
 
+// Token and head of row `row` = token * H + head (a 64-bit quotient only where 32 bits do not do).
+__device__ __forceinline__ void split_row(int64_t row, int H, int64_t& t, int& h) {
+  if (row <= 0xffffffffll) {
+    const uint32_t q = (uint32_t)row / (uint32_t)H;
+    t = q, h = (int)((uint32_t)row - q * H);
+  } else {
+    t = row / H, h = (int)(row - t * H);
+  }
+}
+
 // Row index of (position p, head h) of sequence b in a cache [page][Hkv][slot], -1 if its page is out of range.
 __device__ __forceinline__ int64_t place_of(const Batch& bt, int b, int64_t p, int h, int Hkv) {
   if (p < 0 || p >= (int64_t)bt.max_pages * bt.page_size) return -1;
-  const int pi = (int)(p / bt.page_size), slot = (int)(p - (int64_t)pi * bt.page_size);
+  const uint32_t pi = (uint32_t)p / (uint32_t)bt.page_size, slot = (uint32_t)p - pi * bt.page_size;   // p < 2^30
   const int64_t page = bt.table[(int64_t)b * bt.max_pages + pi];
   if (page < 0 || page >= bt.num_pages) return -1;
   return (page * Hkv + h) * bt.page_size + slot;

@@ -580,8 +580,9 @@ __global__ void __launch_bounds__(256) paged_qslice_kernel(DecodeArgs da) {
   grid_dep_launch();
   if (tid == 0) wanted = 0;
   __syncthreads();
-  const int64_t t = row / a.Hq;
-  const int h = (int)(row - t * a.Hq);
+  int64_t t;
+  int h;
+  split_row(row, a.Hq, t, h);
   int b = row < rows ? warp_find_seq(a.bt, t) : -1;
   if (b >= 0 && small_tokens(a, b) == 0) b = -1;
   float z[4] = {0.f, 0.f, 0.f, 0.f};

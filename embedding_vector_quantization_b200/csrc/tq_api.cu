@@ -62,6 +62,7 @@ struct tq_handle {
   int* derr = nullptr;    // device error word
   uint8_t* dOps = nullptr; // d = 128: pre-swizzled 16-bit hi/lo operands of the tensor-core encode
   double* d64 = nullptr;    // d <= 256: fp64 tables of the paged operators (layout: tq_view in internal.h)
+  uint8_t* dOpsApp = nullptr; // d = 64 or 128: f16 pairs of the paged append (layout: tq_view in internal.h)
   uint8_t* dOps16 = nullptr; // d = 64 or 128: f16 operands of the paged operators (layout: tq_view in internal.h)
   float m_abs = 0.f, m_norm = 0.f;  // largest row of M = S Pi^T in the 1-norm and the 2-norm
   uint16_t* dPiB = nullptr; // MSE, d % 256 = 0, 256 <= d <= 4096: Pi as a bf16 pair, [2][d][d] (hi rows, lo rows)
@@ -198,6 +199,8 @@ void free_device(tq_handle* h) {
   h->dPiB = nullptr;
   cudaFree(h->d64);
   cudaFree(h->dOps16);
+  cudaFree(h->dOpsApp);
+  h->dOpsApp = nullptr;
   h->d64 = nullptr;
   h->dOps16 = nullptr;
   cudaFree(h->dTab);
@@ -351,6 +354,22 @@ int create_common(int d, int bits_mse, int m, uint64_t seed, int norm_dtype, tq_
         std::memcpy(&ops16[off], &bits, 2);
       }
   }
+  // f16 pairs of the paged append, K-major in slices of 64 k as above: Pi 2^8 (high, low), M 2^5 (high, low)
+  std::vector<uint8_t> ops_app;
+  if ((d == 64 || d == 128) && (m == 0 || m == d) && bits_mse > 0) {
+    const size_t mat = (size_t)d * d * 2;
+    ops_app.resize(mat * (m ? 4 : 2));
+    for (int x = 0; x < (m ? 2 : 1); ++x)
+      for (int j = 0; j < d; ++j)
+        for (int k = 0; k < d; ++k) {
+          const double v = x ? 32.0 * M[(size_t)j * d + k] : 256.0 * h->Pi[(size_t)j * d + k];
+          const __half hi = __double2half(v), lo = __double2half(v - (double)__half2float(hi));
+          const uint16_t hb = __half_as_ushort(hi), lb = __half_as_ushort(lo);
+          const size_t off = (size_t)(k >> 6) * d * 128 + (size_t)j * 128 + (size_t)((((k & 63) >> 3) ^ (j & 7)) << 4) + (k & 7) * 2;
+          std::memcpy(&ops_app[(2 * x) * mat + off], &hb, 2);
+          std::memcpy(&ops_app[(2 * x + 1) * mat + off], &lb, 2);
+        }
+  }
   if (d <= 256) {
     t64 = h->Pi;
     t64.insert(t64.end(), h->S.begin(), h->S.end());
@@ -366,6 +385,7 @@ int create_common(int d, int bits_mse, int m, uint64_t seed, int norm_dtype, tq_
   }
   int st = TQ_OK;
   if ((st = upload(&h->d64, t64, "fp64 tables")) || (st = upload(&h->dOps16, ops16, "f16 operands")) ||
+      (st = upload(&h->dOpsApp, ops_app, "f16 pairs")) ||
       (st = upload(&h->dPi, Pi, "Pi")) || (st = upload(&h->dPiT, PiT, "PiT")) ||
       (st = upload(&h->dS, S, "S")) || (st = upload(&h->dST, ST, "ST")) || (st = upload(&h->dMT, MT, "MT")) ||
       (st = upload(&h->dcent, cent, "centroids")) || (st = upload(&h->dbnd, bnd, "bounds")) ||
@@ -1071,7 +1091,7 @@ void tq_internal_view(const tq_handle* h, tq_view* v) {
   v->d = h->d, v->bits = h->bits, v->m = h->m, v->norm_dtype = h->norm_dtype;
   v->codes_B = h->codes_B, v->signs_B = h->signs_B, v->device = h->device, v->polar = h->polar;
   v->PiT = h->dPiT, v->Pi = h->dPi, v->MT = h->dMT, v->ST = h->dST, v->S = h->dS, v->cent = h->dcent, v->bnd = h->dbnd;
-  v->t64 = h->d64, v->ops16 = h->dOps16, v->m_abs = h->m_abs, v->m_norm = h->m_norm, v->err = h->derr;
+  v->t64 = h->d64, v->ops16 = h->dOps16, v->ops_app = h->dOpsApp, v->m_abs = h->m_abs, v->m_norm = h->m_norm, v->err = h->derr;
   v->cent_h = h->cent.data(), v->bnd_h = h->bnd.data();
 }
 int tq_internal_ok() { return ok(); }

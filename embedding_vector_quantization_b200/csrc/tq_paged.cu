@@ -18,6 +18,7 @@
 #include "paged_attn_simt.cuh"
 #include "paged_flash.cuh"
 #include "paged_decode.cuh"
+#include "paged_append_tc.cuh"
 
 namespace {
 
@@ -188,6 +189,68 @@ int append_simt(const AppendArgs& a, int device, cudaStream_t s) {
   return launched("paged_append_kernel");
 }
 
+bool simt_forced() {
+  const char* e = std::getenv("TQ_SIMT");
+  return e && std::strcmp(e, "1") == 0;
+}
+
+// A launch that may start while the kernel before it drains (that kernel's results are read after griddepcontrol.wait).
+template <typename K, typename A>
+int launch_after(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, const A& args, const char* what) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid, cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at, cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args);
+  if (e != cudaSuccess) return fail(TQ_ECUDA, "%s: %s", what, cudaGetErrorString(e));
+  return launched(what);
+}
+
+template <int D, int BITS, bool PROD>
+int append_tc_launch(const AppendTcArgs& a, int device, bool beside, cudaStream_t s) {
+  static std::atomic<uint64_t> seen{0};
+  using L = TaLayout<D, PROD>;
+  if (int st = allow_smem(paged_append_tc_kernel<D, BITS, PROD>, L::kBytes, device, seen)) return st;
+  const int64_t tiles = (a.bt.ntok * a.Hkv + 127) / 128;
+  const dim3 grid((unsigned)std::min<int64_t>(tiles, std::max(1, device_sms(device) / 2)));   // keys and values run side by side
+  tq_launch_scope scope("append_paged", s);
+  if (beside) return launch_after(paged_append_tc_kernel<D, BITS, PROD>, grid, kTaThreads, L::kBytes, s, a, "paged_append_tc_kernel");
+  paged_append_tc_kernel<D, BITS, PROD><<<grid, kTaThreads, L::kBytes, s>>>(a);
+  return launched("paged_append_tc_kernel");
+}
+
+template <int D, bool PROD>
+int append_tc_bits(const AppendTcArgs& a, int device, bool beside, cudaStream_t s) {
+  switch (a.q.bits) {
+    case 1: return append_tc_launch<D, 1, PROD>(a, device, beside, s);
+    case 2: return append_tc_launch<D, 2, PROD>(a, device, beside, s);
+    case 3: return append_tc_launch<D, 3, PROD>(a, device, beside, s);
+    default: return append_tc_launch<D, 4, PROD>(a, device, beside, s);
+  }
+}
+
+constexpr int64_t kAppendTcRows = 1024;   // vectors of a kind from which the tensor cores take over
+
+// Keys on one half of the SMs, values on the other: the second kernel starts beside the first and waits for it before it ends.
+int append_tc(const AppendArgs& g, const tq_view& k, const tq_view& v, cudaStream_t s) {
+  for (int kind = 0; kind < 2; ++kind) {
+    const tq_view& w = kind ? v : k;
+    AppendTcArgs a{};
+    a.x = g.x[kind], a.stride = g.stride[kind], a.x_dtype = g.x_dtype, a.Hkv = g.Hkv, a.bt = g.bt;
+    a.check_prep = g.prep;
+    if (kind == 0) a.prep = g.prep;
+    a.exact_hi = g.x_dtype != TQ_F32 && !a.prep.cos_sin && !a.prep.weight;
+    a.q = g.q[kind], a.c = g.c[kind], a.ops = w.ops_app, a.err = g.err;
+    int st;
+    if (w.d == 128) st = w.m ? append_tc_bits<128, true>(a, w.device, kind == 1, s) : append_tc_bits<128, false>(a, w.device, kind == 1, s);
+    else st = w.m ? append_tc_bits<64, true>(a, w.device, kind == 1, s) : append_tc_bits<64, false>(a, w.device, kind == 1, s);
+    if (st) return st;
+  }
+  return TQ_OK;
+}
+
 // ---------------------------------------------------------------- attention, general kernels
 
 struct SimtPlan {
@@ -240,11 +303,6 @@ int attn_simt(AttnArgs& a, const tq_view& k, const tq_view& v, const SimtPlan& p
 }
 
 // ---------------------------------------------------------------- attention of chunks, tensor cores
-
-bool simt_forced() {
-  const char* e = std::getenv("TQ_SIMT");
-  return e && std::strcmp(e, "1") == 0;
-}
 
 // 16-bit queries, d = 64 or 128, d signs or none (those handles hold the operands).
 bool flash_formats(const tq_view& k, const tq_view& v) { return k.ops16 && v.ops16 && !simt_forced(); }
@@ -361,20 +419,6 @@ DecodePlan decode_plan(const tq_view& k, const tq_view& v, const Batch& b, int H
   return p;
 }
 
-// A launch that may start while the kernel before it drains (that kernel's results are read after griddepcontrol.wait).
-template <typename K, typename A>
-int launch_after(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, const A& args, const char* what) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid, cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at, cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args);
-  if (e != cudaSuccess) return fail(TQ_ECUDA, "%s: %s", what, cudaGetErrorString(e));
-  return launched(what);
-}
-
 template <int D, int BK, int BV, bool SG, bool NF16>
 int decode_launch(const DecodeArgs& a, int device, cudaStream_t s) {
   static std::atomic<uint64_t> seen{0};
@@ -458,6 +502,7 @@ int tq_append_paged(const tq_handle* hk, const tq_handle* hv, const void* k_new,
   a.c[0] = view_of(kw, k), a.c[1] = view_of(vw, v);
   a.err = kw.err;
   const int64_t rows = batch->ntok * Hkv;
+  if (rows >= kAppendTcRows && kw.ops_app && vw.ops_app && !simt_forced()) return append_tc(a, kw, vw, s);
   if (rows <= device_sms(kw.device)) return append_simt<1>(a, kw.device, s);
   return append_simt<8>(a, kw.device, s);
 }

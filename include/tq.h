@@ -337,8 +337,8 @@ typedef struct tq_head_prep {
  *                projection's output
  *  hk, hv        MSE, prod or QJL-only handles of one d <= 256 (m <= 256), on one device
  * The indices and signs are those of exact arithmetic: a coordinate that lies within the rounding of the fast
- * path of a border is computed again in 64 bits, so a token's bytes depend neither on the batch it came in
- * nor on the kernel that wrote it.
+ * path of a border is computed again in 64 bits, so a token's codes and signs depend neither on the batch it
+ * came in nor on the kernel that wrote it (norms, sums in fp32 or fp64, may differ by one step).
  * A token whose page (outside 0 .. num_pages - 1, position outside 0 .. max_pages * page_size - 1) or rotation
  * position (outside 0 .. max_pos - 1) is out of range is skipped and recorded in hk's error word (TQ_EINVAL
  * from tq_last_status). Two tokens with the same place race; which one stays is undefined. */
