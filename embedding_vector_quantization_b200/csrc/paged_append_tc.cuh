@@ -28,8 +28,10 @@ namespace paged {
 constexpr float kU = 5.9604645e-8f;
 constexpr float kTcBandY = 24.f * kU;
 constexpr float kTcBandS = 12.f * kU;    // times m_norm
-constexpr int kTaPrepWarps = 8, kTaEpiWarps = 8;
-constexpr int kTaThreads = 32 * (kTaPrepWarps + kTaEpiWarps + 1);
+// Warps 0-7 prepare, 8-23 finish (two groups of eight, two threads per row: the chain of one thread per row took twice as
+// long), 24 issues, 25-27 fill its warpgroup. Registers: 896 threads x 72 at launch = 128 x (2 x 104 + 4 x 64 + 40).
+constexpr int kTaPrepWarps = 8, kTaEpiWarps = 16;
+constexpr int kTaThreads = 32 * (kTaPrepWarps + kTaEpiWarps + 4);
 
 // f16 pairs, K-major: Pi_h, Pi_l (times 2^8), M_h, M_l (times 2^5); each D/64 slices of D rows.
 template <int D, bool PROD>
@@ -39,8 +41,9 @@ struct TaLayout {
   static constexpr uint32_t kTile = (D / 64) * kAtomRows;         // 128 rows
   static constexpr int kStages = PROD && D == 128 ? 1 : 2;        // z tiles (pairs)
   static constexpr uint32_t kA = kOps;
-  static constexpr uint32_t kRow = kA + kStages * 2 * kTile;      // per stage of four: int64 place[128], float2 (N_s, N)[128]
-  static constexpr uint32_t kBars = kRow + 4 * 2048;
+  static constexpr uint32_t kRow = kA + kStages * 2 * kTile;      // per tile of four: int64 place[128], float2 (N_s, N)[128], int64 rp[128]
+  static constexpr uint32_t kSq = kRow + 4 * 3072;                // float [2 groups][2][128]: halves of |e|^2
+  static constexpr uint32_t kBars = kSq + 2048;
   // op_full, a_full[2], a_empty[2], d1_full[2], e_full[2], d2_full[2], d_free[2]
   static constexpr int kNumBars = 13;
   static constexpr uint32_t kMisc = kBars + 8 * kNumBars;
@@ -108,10 +111,15 @@ __device__ __forceinline__ void exact_row(const AppendTcArgs& a, int64_t t, int 
   n = sqrt(ss);
 }
 template <int D>
-__device__ __forceinline__ double exact_dot(const double* row, const double (&z)[D / 32]) {
+__device__ __forceinline__ void load_row64(const double* row, double (&p)[D / 32]) {
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) p[c] = __ldg(row + (threadIdx.x & 31) + 32 * c);
+}
+template <int D>
+__device__ __forceinline__ double exact_dot(const double (&p)[D / 32], const double (&z)[D / 32]) {
   double s = 0.0;
 #pragma unroll
-  for (int c = 0; c < D / 32; ++c) s += row[(threadIdx.x & 31) + 32 * c] * z[c];
+  for (int c = 0; c < D / 32; ++c) s += p[c] * z[c];
   for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return s;
 }
@@ -160,7 +168,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) paged_append_tc_kernel(AppendTc
     *abort_flag = 0;
     uint64_t* b = reinterpret_cast<uint64_t*>(smem + L::kBars);
     for (int i = 0; i < L::kNumBars; ++i) {
-      const int n = i == 1 || i == 2 ? kTaPrepWarps : i == 7 || i == 8 || i == 11 || i == 12 ? 4 : 1;
+      const int n = i == 1 || i == 2 ? kTaPrepWarps : i == 7 || i == 8 || i == 11 || i == 12 ? kTaEpiWarps / 2 : 1;
       bar_init(b + i, n);
     }
   }
@@ -180,14 +188,16 @@ __global__ void __launch_bounds__(kTaThreads, 1) paged_append_tc_kernel(AppendTc
   };
 
   if (warp < kTaPrepWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n");
     // ---- rows -> z pairs; lane q of a row's four holds the 16-byte chunks (8 coordinates) q, q + 4, ...
     constexpr int C = D / 32;
     const int ql = lane & 3, rot = a.prep.cos_sin ? a.prep.rot_dim : 0, half = rot >> 1;
     const int64_t start0 = a.bt.q_start[0], end = a.bt.q_start[a.bt.B];
     for (int i = 0; i < mine; ++i) {
       const int s = i % L::kStages, ri = i & 3;
-      int64_t* place_s = reinterpret_cast<int64_t*>(smem + L::kRow + ri * 2048);
-      float2* norm_s = reinterpret_cast<float2*>(smem + L::kRow + ri * 2048 + 1024);
+      int64_t* place_s = reinterpret_cast<int64_t*>(smem + L::kRow + ri * 3072);
+      float2* norm_s = reinterpret_cast<float2*>(smem + L::kRow + ri * 3072 + 1024);
+      int64_t* rp_s = reinterpret_cast<int64_t*>(smem + L::kRow + ri * 3072 + 2048);   // for the rows that are computed twice
       // places and (16-bit) values of both halves first: one latency for them all
       int64_t at2[2], rp2[2], from2[2];
       uint4 raw[2][C];
@@ -343,13 +353,16 @@ __global__ void __launch_bounds__(kTaThreads, 1) paged_append_tc_kernel(AppendTc
           sts128(zr + off, hi[0], hi[1], hi[2], hi[3]);
           if (!a.exact_hi) sts128(zr + L::kTile + off, lo[0], lo[1], lo[2], lo[3]);
         }
-        if (ql == 0) place_s[r] = at, norm_s[r] = make_float2(n * sc1 * sc2, n);
+        if (ql == 0) place_s[r] = at, rp_s[r] = rp, norm_s[r] = make_float2(n * sc1 * sc2, n);
       }
       fence_async();
       __syncwarp();
       if (lane == 0) bar_arrive(a_full(s));
     }
+  } else if (warp > kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
   } else if (warp == kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
     const uint32_t lead = elect_one();
     if (lead) {
       expect_tx(op_full, L::kOps);
@@ -401,8 +414,10 @@ __global__ void __launch_bounds__(kTaThreads, 1) paged_append_tc_kernel(AppendTc
       if (PROD) (void)wait_bar(d2_full(i & 1), (i / 2) & 1);
     }
   } else {
-    // ---- indices and signs: thread = row of the group's tiles
-    const int ew = warp - kTaPrepWarps, g = ew >> 2, r = (ew & 3) * 32 + lane;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+    // ---- indices and signs: thread = half a row of the group's tiles
+    const int ew = warp - kTaPrepWarps, g = ew >> 3, part = (ew >> 2) & 1, r = (ew & 3) * 32 + lane;
+    float* const sq = reinterpret_cast<float*>(smem + L::kSq) + 256 * g + r;
     const uint32_t col = tmem + 256 * g + ((uint32_t)((ew & 3) * 32) << 16);
     Cells<BITS> cells;
 #pragma unroll
@@ -413,8 +428,8 @@ __global__ void __launch_bounds__(kTaThreads, 1) paged_append_tc_kernel(AppendTc
       const int ri = i & 3;
       wait(d1_full(g), (i / 2) & 1);
       tc_fence_after();
-      const int64_t at = reinterpret_cast<const int64_t*>(smem + L::kRow + ri * 2048)[r];
-      const float2 nn = reinterpret_cast<const float2*>(smem + L::kRow + ri * 2048 + 1024)[r];
+      const int64_t at = reinterpret_cast<const int64_t*>(smem + L::kRow + ri * 3072)[r];
+      const float2 nn = reinterpret_cast<const float2*>(smem + L::kRow + ri * 3072 + 1024)[r];
       const int64_t row0 = ((int64_t)blockIdx.x + (int64_t)i * gridDim.x) * 128;
       const float inv = nn.x > 0.f ? 0.00390625f / nn.x : 0.f;   // 2^-8 / |z scaled|
       const bool some = at >= 0 && nn.x > 0.f && nn.x < INFINITY;
@@ -423,17 +438,13 @@ __global__ void __launch_bounds__(kTaThreads, 1) paged_append_tc_kernel(AppendTc
         int64_t t;
         int h;
         split_row(row0 + (ew & 3) * 32 + who, a.Hkv, t, h);
-        int64_t rp = 0;
-        if (a.prep.cos_sin) {
-          const int b = last_at_or_before(a.bt.q_start, a.bt.B, (int)t);
-          rp = a.prep.pos ? (int64_t)a.prep.pos[t] : (int64_t)a.bt.len[b] - a.bt.q_start[b + 1] + t;
-        }
+        const int64_t rp = reinterpret_cast<const int64_t*>(smem + L::kRow + ri * 3072 + 2048)[(ew & 3) * 32 + who];
         exact_row<D>(a, t, h, rp, z, n);
       };
       float esq[2] = {0.f, 0.f};
       uint64_t front = 0;
 #pragma unroll 1   // 16 coordinates at a time: the unrolled row would not stay in the instruction cache
-      for (int c16 = 0; c16 < D / 16; ++c16) {
+      for (int c16 = part * (D / 32); c16 < (part + 1) * (D / 32); ++c16) {
         uint32_t v[16];
         tmem_ld16(col + 16 * c16, v);
         float near, err[PROD ? 16 : 1];
@@ -470,11 +481,14 @@ __global__ void __launch_bounds__(kTaThreads, 1) paged_append_tc_kernel(AppendTc
           const uint32_t close = cells_of(true);
           for (unsigned todo = __ballot_sync(0xffffffffu, close != 0); todo; todo &= todo - 1) {
             const int who = __ffs(todo) - 1;
-            double z[D / 32], n;
+            double z[D / 32], n, p[D / 32];
+            uint32_t m = __shfl_sync(0xffffffffu, close, who);
+            load_row64<D>(a.q.Pi64() + (size_t)(16 * c16 + __ffs(m) - 1) * D, p);   // under way while the row is prepared
             fetch_exact(who, z, n);
-            for (uint32_t m = __shfl_sync(0xffffffffu, close, who); m; m &= m - 1) {
-              const int x = __ffs(m) - 1, j = 16 * c16 + x;
-              const double y = exact_dot<D>(a.q.Pi64() + (size_t)j * D, z) / n;
+            for (; m; m &= m - 1) {
+              const int x = __ffs(m) - 1;
+              const double y = exact_dot<D>(p, z) / n;
+              if (m & (m - 1)) load_row64<D>(a.q.Pi64() + (size_t)(16 * c16 + __ffs(m & (m - 1)) - 1) * D, p);
               int k = 0;
               for (int q = 0; q < (1 << BITS) - 1; ++q) k += a.q.bnd64()[q] < y;
               // the fp32 value nearest to y for which the comparisons above give k: a positive cell holds its upper border
@@ -526,25 +540,25 @@ __global__ void __launch_bounds__(kTaThreads, 1) paged_append_tc_kernel(AppendTc
           tmem_st8(col + 128 + D / 2 + 8 * c16, lo);
         }
       }
-      if (at >= 0) store_norm(a.c.norms, a.q.norm_dtype, at, (double)nn.y);
+      if (at >= 0 && part == 0) store_norm(a.c.norms, a.q.norm_dtype, at, (double)nn.y);
       if (!PROD) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) bar_arrive(d_free(g));
         continue;
       }
+      sq[128 * part] = esq[0] + esq[1];
       etc::tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive(e_full(g));
-      if (at >= 0) a.c.rnorms[at] = __double2half((double)nn.y * sqrt((double)esq[0] + (double)esq[1]));
-      __syncwarp();   // the codes are visible to the whole warp
-      wait(d2_full(g), (i / 2) & 1);
+      wait(d2_full(g), (i / 2) & 1);   // both halves of the group have arrived before: sums and codes are there
       tc_fence_after();
+      if (at >= 0 && part == 0) a.c.rnorms[at] = __double2half((double)nn.y * sqrt((double)sq[0] + (double)sq[128]));
       const float band = kTcBandS * a.q.m_norm * 32768.f;   // D2 comes times 2^5 2^10
       uint32_t first_half = 0;
 #pragma unroll 1
-      for (int c16 = 0; c16 < D / 16; ++c16) {
+      for (int c16 = part * (D / 32); c16 < (part + 1) * (D / 32); ++c16) {
         uint32_t v[16];
         tmem_ld16(col + 16 * c16, v);
         uint32_t sg = 0;
@@ -570,7 +584,10 @@ __global__ void __launch_bounds__(kTaThreads, 1) paged_append_tc_kernel(AppendTc
             for (int c = 0; c < D / 32; ++c) cz[c] = a.q.cent64()[packed_field(cw, lane + 32 * c, BITS)];
             for (uint32_t m = __shfl_sync(0xffffffffu, close, who); m; m &= m - 1) {
               const int x = __ffs(m) - 1, j = 16 * c16 + x;
-              const double d = exact_dot<D>(a.q.S64() + (size_t)j * D, z) / n - exact_dot<D>(a.q.M64() + (size_t)j * D, cz);
+              double p[D / 32], q[D / 32];
+              load_row64<D>(a.q.S64() + (size_t)j * D, p);
+              load_row64<D>(a.q.M64() + (size_t)j * D, q);
+              const double d = exact_dot<D>(p, z) / n - exact_dot<D>(q, cz);
               if (lane == who) sg = d >= 0.0 ? sg | 1u << x : sg & ~(1u << x);
             }
           }
