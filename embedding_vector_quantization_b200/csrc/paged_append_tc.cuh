@@ -16,8 +16,8 @@
 // by |z| 2 |y|; and the 24 accumulations inside the tensor cores, whose rounding is not specified. Measured against fp64
 // over 6.7e7 coordinates of bf16 and fp32 vectors with outlier channels, with and without preparation: 1.0 u root mean
 // square, 8.5 u at most; the band is 24 u. A sign's sum gathers d such differences with weights of length m_norm: measured
-// 0.24 u m_norm root mean square, 2.3 u m_norm at most; the band is 12 u m_norm. About 0.4 % of the rows of 2-bit codes and 1 %
-// of 4-bit ones have a coordinate, and 0.3 % a sign, that is computed twice.
+// 0.24 u m_norm root mean square and at most 2.3 u m_norm, 1.1 where the sum is below 0.2; the band is 6 u m_norm. About 0.4 % of the rows of 2-bit codes and 1 %
+// of 4-bit ones have a coordinate, and 0.2 % a sign, that is computed twice.
 #pragma once
 
 #include "paged_flash.cuh"
@@ -27,7 +27,7 @@ namespace paged {
 
 constexpr float kU = 5.9604645e-8f;
 constexpr float kTcBandY = 24.f * kU;
-constexpr float kTcBandS = 12.f * kU;    // times m_norm
+constexpr float kTcBandS = 6.f * kU;    // times m_norm
 // Warps 0-7 prepare, 8-23 finish (two groups of eight, two threads per row: the chain of one thread per row took twice as
 // long), 24 issues, 25-27 fill its warpgroup. Registers: 896 threads x 72 at launch = 128 x (2 x 104 + 4 x 64 + 40).
 constexpr int kTaPrepWarps = 8, kTaEpiWarps = 16;

@@ -174,7 +174,10 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
   chunk_sums<kDcThreads>(a, pre, warp_s);
   const int64_t U = pre[a.bt.B];
   const Span sp = span_of(U, blockIdx.x, gridDim.x);
-  if (sp.u0 >= sp.u1) return;
+  if (sp.u0 >= sp.u1) {
+    grid_dep_wait();   // every CTA waits: a kernel behind this one may count on the one before
+    return;
+  }
   build_lut(a.k, tables, tid, kDcThreads);
   if (BK != BV) build_lut(a.v, tables + 32768, tid, kDcThreads);
   __syncthreads();
@@ -197,7 +200,7 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
     const int64_t item_u = pre[b] + (int64_t)h * nch;
     const int c0 = (int)(u - item_u), c1 = (int)(min(sp.u1, item_u + nch) - item_u);
     u = item_u + nch;
-    const int tok0 = a.bt.q_start[b], rows = n * a.G, len = a.bt.len[b];
+    const int rows = n * a.G, len = a.bt.len[b];
     int lo_all, hi_all;
     key_range(a.bt, b, 0, n - 1, n, a.causal, a.window, lo_all, hi_all);
     // rows 2 t, 2 t + 1 are this lane's columns: the keys they see
@@ -216,7 +219,7 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
     float fc[2], fs[2];
     {
       constexpr int DK = D + (SG ? D : 0);
-      const float* src = a.qr + ((int64_t)(tok0 + g / a.G) * a.Hq + h * a.G + g % a.G) * DK;
+      const float* src = a.qr + (((int64_t)b * a.Hkv + h) * 8 + g) * DK;
       float z[D / 4];
       float top = 0.f;
       bool blind = false;
@@ -570,43 +573,38 @@ __device__ __forceinline__ void rows_slice(const float* in, int ni, const float*
   __syncthreads();
 }
 
-// Queries of the small sequences. Grid: (8-row groups of (token, head), (d + m) / 32 column slices); 256 threads.
+// Queries of the small sequences, to qr [B][Hkv][8][d + m]. Grid: (B * Hkv, (d + m) / 32 column slices); 256 threads: warp r
+// prepares query row r of the (sequence, head).
 __global__ void __launch_bounds__(256) paged_qslice_kernel(DecodeArgs da) {
   __shared__ float zf[8 * 128], part_s[8 * 256], ys[256];
-  __shared__ int wanted;
   const AttnArgs& a = da.a;
   const int d = a.k.d, m = a.k.m, dk = d + m, tid = threadIdx.x, lane = tid & 31, r = tid >> 5;
-  const int64_t row0 = (int64_t)blockIdx.x * 8, rows = a.bt.ntok * a.Hq, row = row0 + r;
   grid_dep_launch();
-  if (tid == 0) wanted = 0;
-  __syncthreads();
-  int64_t t;
-  int h;
-  split_row(row, a.Hq, t, h);
-  int b = row < rows ? warp_find_seq(a.bt, t) : -1;
-  if (b >= 0 && small_tokens(a, b) == 0) b = -1;
+  const int b = blockIdx.x / a.Hkv, h = blockIdx.x - b * a.Hkv;
+  const int n = small_tokens(a, b);
+  if (n == 0) return;
   float z[4] = {0.f, 0.f, 0.f, 0.f};
   bool blind = false;
-  if (b >= 0) {
-    const int64_t p = a.prep.pos ? (int64_t)a.prep.pos[t] : (int64_t)a.bt.len[b] - a.bt.q_start[b + 1] + t;
-    if (lane == 0) wanted = 1;
+  if (r < n * a.G) {
+    const int i = r / a.G;
+    const int64_t t = a.bt.q_start[b] + i;
+    const int64_t p = a.prep.pos ? (int64_t)a.prep.pos[t] : (int64_t)a.bt.len[b] - n + i;
     if (a.prep.cos_sin && (p < 0 || p >= a.prep.max_pos)) {
       if (lane == 0 && (a.prep.pos || p >= 0)) report_error(a.err, kErrPaged);
       blind = true;   // it sees nothing
     } else {
-      prep_head<float, 4>(a.q, a.q_dtype, t * a.q_stride + (int64_t)h * d, d, a.prep, p, z);
+      prep_head<float, 4>(a.q, a.q_dtype, t * a.q_stride + (int64_t)(h * a.G + r - i * a.G) * d, d, a.prep, p, z);
     }
   }
 #pragma unroll
   for (int c = 0; c < 4; ++c)
     if (lane + 32 * c < d) zf[r * d + lane + 32 * c] = z[c];
   __syncthreads();
-  if (!wanted) return;
   const int col = 32 * blockIdx.y;
   const bool code = col < d;
   rows_slice(zf, d, code ? a.k.PiT : a.k.ST, code ? d : m, code ? col : col - d, part_s, ys);
   const float f = a.scale * 1.44269504089f * (code ? 1.f : kQjlScale / (float)m);
-  if (row < rows) a.qr[row * dk + col + lane] = blind ? kBlind : ys[tid] * f;
+  a.qr[((int64_t)blockIdx.x * 8 + r) * dk + col + lane] = blind ? kBlind : ys[tid] * f;
 }
 
 // Grid: (B, Hkv, d / 32): 32 coordinates of the rows of one (sequence, head): its CTAs' parts merged in order, then
@@ -615,6 +613,7 @@ __global__ void __launch_bounds__(256) paged_decode_merge_kernel(DecodeArgs da) 
   extern __shared__ __align__(16) unsigned char smem[];
   const AttnArgs& a = da.a;
   const int d = a.v.d, m = a.v.m, dv = d + m, b = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  grid_dep_launch();
   const int P = da.ctas;
   float* acc = reinterpret_cast<float*>(smem);        // [8][d], then [8][m]
   float* part_s = acc + 8 * dv;                       // [8][256]
@@ -626,7 +625,10 @@ __global__ void __launch_bounds__(256) paged_decode_merge_kernel(DecodeArgs da) 
   __shared__ float f[8];
   __shared__ int parts;
   const int n = small_tokens(a, b);
-  if (n == 0) return;
+  if (n == 0) {
+    grid_dep_wait();
+    return;
+  }
   int first;
   const int nch = small_chunks(a, b, n, first);
   // the units before this sequence, and all of them

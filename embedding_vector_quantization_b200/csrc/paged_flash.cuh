@@ -128,6 +128,7 @@ __device__ __forceinline__ int last_at_or_before(const int* start, int n, int x)
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(FlashArgs a) {
   __shared__ int warp_s[32];
   const int tid = threadIdx.x;
+  grid_dep_launch();
   int tiles = 0, items = 0, total;
   for (int b0 = 0; b0 < a.bt.B; b0 += kPlanThreads) {
     const int b = b0 + tid;
@@ -152,6 +153,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(FlashArgs a) {
       report_error(a.err, kErrPaged);
       a.p.head[0] = a.p.head[1] = a.p.head[2] = 0;
     }
+    grid_dep_wait();
     return;
   }
   if (tid == 0) a.p.tile_start[a.bt.B] = tiles, a.p.item_start[a.bt.B] = items;
@@ -175,11 +177,13 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(FlashArgs a) {
     a.p.unit[items] = units;
     a.p.head[0] = tiles, a.p.head[1] = items, a.p.head[2] = units;
   }
+  grid_dep_wait();   // nothing here needs the kernel before (single tokens); what follows may count on it
 }
 
 // ---------------------------------------------------------------- expand
 
-constexpr int kExThreads = 288;   // warps 0-3 write operands, 4-7 read results, 8 issues
+// Warps 0-7 write operands and 8-15 read results, in two groups each that take alternate tiles (and operand stages); 16 issues.
+constexpr int kExThreads = 544;
 
 template <int D>
 struct ExLayout {
@@ -189,8 +193,8 @@ struct ExLayout {
   static constexpr uint32_t kLut = kA + 2 * kAStage;                    // 32 KB
   static constexpr uint32_t kScale = kLut + 32768;                      // float [2][128]
   static constexpr uint32_t kBars = kScale + 1024;                      // op_full, a_full[2], a_empty[2], d_full[2], d_empty[2]
-  static constexpr uint32_t kMisc = kBars + 9 * 8;                      // tmem slot, abort, maxima[4]
-  static constexpr uint32_t kBytes = kMisc + 32;
+  static constexpr uint32_t kMisc = kBars + 9 * 8;                      // tmem slot, abort, maxima[2 groups][2][4]
+  static constexpr uint32_t kBytes = kMisc + 8 + 64;
 };
 static_assert(ExLayout<128>::kBytes <= 232448, "expand layout exceeds the shared memory of one CTA");
 
@@ -310,7 +314,52 @@ __host__ __device__ constexpr uint32_t flash_idesc(int N, bool bn) {
   return (1u << 4) | (bn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
-// Grid: 2 x CTAs; even CTAs keys, odd CTAs values; CTA j of a kind takes (head, tile) pairs j, j + n, ...
+// ---- issue by one lane of a whole warp: the warp stays together, so that addresses and descriptors live in uniform
+// registers (a lone thread spends longer on moving them there than the tensor cores on the instruction)
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r;
+}
+template <bool ACC>
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 q, %0, 0;\n setp.ne.u32 p, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%1], %2, %3, %4, p;\n}\n" ::"r"(leader),
+      "r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "n"(ACC ? 1 : 0));
+}
+// A in tensor memory (lane = row, 8 columns of two f16 per 16 K).
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 q, %0, 0;\n setp.ne.u32 p, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], %3, %4, p;\n}\n" ::"r"(leader),
+      "r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void commit_one(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.u32 q, %0, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n}\n" ::"r"(leader),
+      "r"(bar)
+      : "memory");
+}
+
+// Where a CTA's walk over (head, key tile) pairs stands; the sequence is looked up only when the tile leaves it.
+struct TileCursor {
+  int h, tile, b, first, last, base, hi;   // tiles [first, last) of sequence b; key 0 of tile `first` is at `base`, keys end at hi
+};
+__device__ __forceinline__ void cursor_seek(const FlashArgs& a, int tiles, TileCursor& c, int step) {
+  c.tile += step;
+  while (c.tile >= tiles) c.tile -= tiles, ++c.h;
+  if (c.tile >= c.first && c.tile < c.last) return;
+  c.b = last_at_or_before(a.p.tile_start, a.bt.B, c.tile);
+  c.first = a.p.tile_start[c.b], c.last = a.p.tile_start[c.b + 1];
+  const int n = seq_rows(a, c.b);
+  int lo;
+  flash_range(a, c.b, 0, n - 1, n, lo, c.hi);
+  c.base = lo / kKT * kKT;
+}
+
+// Grid: 2 x CTAs; even CTAs keys, odd CTAs values; CTA j of the n of a kind takes pairs [j W / n, (j + 1) W / n) of W.
 template <int D>
 __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a) {
   using L = ExLayout<D>;
@@ -321,8 +370,6 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
   const int kind = blockIdx.x & 1, j0 = blockIdx.x >> 1, step = gridDim.x >> 1;
   const Quant& Q = kind ? a.vq : a.kq;
   const CacheView& C = kind ? a.vc : a.kc;
-  const int tiles = a.p.head[0], work = tiles * a.heads;
-  const int mine = work > j0 ? (work - j0 + step - 1) / step : 0;
   const uint32_t bars = base + L::kBars;
   const uint32_t op_full = bars;
   auto a_full = [&](int s) { return bars + 8u * (1 + s); };
@@ -337,7 +384,7 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
     if (tid == 0) report_error(a.err, kErrInternal);
     return;
   }
-  if (mine == 0) return;
+  grid_dep_launch();
   if (tid == 0) {
     *abort_flag = 0;
     uint64_t* b = reinterpret_cast<uint64_t*>(smem + L::kBars);
@@ -345,7 +392,12 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
     for (int s = 0; s < 2; ++s) bar_init(b + 1 + s, 4), bar_init(b + 3 + s, 1), bar_init(b + 5 + s, 1), bar_init(b + 7 + s, 4);
   }
   build_lut(Q, smem + L::kLut, tid, kExThreads);
-  if (warp == 8) {
+  grid_dep_wait();
+  const int tiles = a.p.head[0];
+  const int64_t work = (int64_t)tiles * a.heads;
+  const int w0 = (int)(work * j0 / step), mine = (int)(work * (j0 + 1) / step) - w0;
+  if (mine == 0) return;
+  if (warp == 16) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(base + L::kMisc), "r"(256u) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
   }
@@ -360,77 +412,82 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
   };
   const int katoms = (D + Q.m) / 64;   // 64-wide slices of the contraction
 
-  if (warp < 4) {
-    // ---- operand rows: thread = token of the tile
-    auto place = [&](int i, int& b, int& tile, int& h) -> int64_t {
-      const int w = j0 + i * step;
-      h = w / tiles, tile = w - h * tiles;
-      b = last_at_or_before(a.p.tile_start, a.bt.B, tile);
-      const int n = seq_rows(a, b);
-      int lo, hi;
-      flash_range(a, b, 0, n - 1, n, lo, hi);
-      const int p = (lo / kKT + tile - a.p.tile_start[b]) * kKT + tid;
-      if (p >= hi) return -2;
-      return place_of(a.bt, b, p, a.head0 + h, a.Hkv);
+  if (warp < 8) {
+    // ---- operand rows: thread = token of the tile. Under way at a time: the page of the token after next, the next row.
+    const int g = warp >> 2, s = g, r = tid & 127;
+    float* const top_s = maxima + 8 * g;
+    TileCursor c{(int)(w0 / tiles), (int)(w0 % tiles), 0, 0, 0, 0, 0};
+    auto page_of = [&]() -> int64_t {   // row offset of the token's page and slot; -1: bad page, -2: behind the end
+      const int p = c.base + (c.tile - c.first) * kKT + r;
+      if (p >= c.hi) return -2;
+      return place_of(a.bt, c.b, p, a.head0 + c.h, a.Hkv);
     };
-    int b, tile, h, nb, ntile, nh;
     Row<D> cur, nxt;
-    int64_t at = place(0, nb, ntile, nh);
-    load_row<D>(Q, C, at, nxt);
-    for (int i = 0; i < mine; ++i) {
-      const int s = i & 1;
-      cur = nxt, b = nb, tile = ntile, h = nh;
-      const int64_t here = at;
-      if (i + 1 < mine) {
-        at = place(i + 1, nb, ntile, nh);
-        load_row<D>(Q, C, at, nxt);
+    int64_t at0 = -2, at1 = -2;      // this group's next tile, and the one after
+    int tile0 = 0, h0 = 0, tile1 = 0, h1 = 0;
+    if (g < mine) {
+      cursor_seek(a, tiles, c, g);
+      at0 = page_of(), tile0 = c.tile, h0 = c.h;
+      load_row<D>(Q, C, at0, nxt);
+    }
+    if (g + 2 < mine) {
+      cursor_seek(a, tiles, c, 2);
+      at1 = page_of(), tile1 = c.tile, h1 = c.h;
+    }
+    for (int i = g; i < mine; i += 2) {
+      cur = nxt;
+      const int64_t here = at0;
+      const int tile = tile0, h = h0;
+      at0 = at1, tile0 = tile1, h0 = h1;
+      if (i + 2 < mine) load_row<D>(Q, C, at0, nxt);
+      if (i + 4 < mine) {
+        cursor_seek(a, tiles, c, 2);
+        at1 = page_of(), tile1 = c.tile, h1 = c.h;
       }
       if (here == -1) report_error(a.err, kErrPaged);
       const unsigned there = __ballot_sync(0xffffffffu, cur.ok);
-      if (kind == 0 && h == 0 && lane == 0) a.p.seen[4 * tile + warp] = there;
+      if (kind == 0 && h == 0 && lane == 0) a.p.seen[4 * tile + (warp & 3)] = there;
       // the tile's exponent: 2^E >= every finite norm
-      const float fin = fabsf(cur.norm) < INFINITY ? fabsf(cur.norm) : 0.f;
-      float top = fin;
+      float top = fabsf(cur.norm) < INFINITY ? fabsf(cur.norm) : 0.f;
       for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      if (lane == 0) maxima[warp] = top;
-      named_sync(1, 128);
-      top = fmaxf(fmaxf(maxima[0], maxima[1]), fmaxf(maxima[2], maxima[3]));
+      float* const mt = top_s + (i & 2) * 2;   // two sets in turn: one barrier a tile is enough
+      if (lane == 0) mt[warp & 3] = top;
+      named_sync(1 + g, 128);
+      top = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
       int e = -126;
       if (top > 0.f) frexpf(top, &e);
       e = max(-126, min(126, e));
-      named_sync(1, 128);
       if (i >= 2) wait(a_empty(s), ((i >> 1) - 1) & 1);
-      scale_s[s * 128 + tid] = cur.ok ? ldexpf(cur.norm, -e) : 0.f;
-      if (tid == 0) (kind ? a.p.ve : a.p.ke)[(int64_t)h * a.p.max_tiles + tile] = e;
-      const uint32_t row = base + L::kA + s * L::kAStage + tid * 128;
+      scale_s[s * 128 + r] = cur.ok ? ldexpf(cur.norm, -e) : 0.f;
+      if (r == 0) (kind ? a.p.ve : a.p.ke)[(int64_t)h * a.p.max_tiles + tile] = e;
+      const uint32_t row = base + L::kA + s * L::kAStage + r * 128;
       if (Q.bits > 0) {
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 v = code_chunk<D>(cur, Q.bits, c, base + L::kLut, lane);
-          sts128(row + (c >> 3) * kAtomRows + (((c & 7) ^ (tid & 7)) << 4), v.x, v.y, v.z, v.w);
+        for (int ch = 0; ch < D / 8; ++ch) {
+          const uint4 v = code_chunk<D>(cur, Q.bits, ch, base + L::kLut, lane);
+          sts128(row + (ch >> 3) * kAtomRows + (((ch & 7) ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
         }
       } else {
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) sts128(row + (c >> 3) * kAtomRows + (((c & 7) ^ (tid & 7)) << 4), 0, 0, 0, 0);
+        for (int ch = 0; ch < D / 8; ++ch) sts128(row + (ch >> 3) * kAtomRows + (((ch & 7) ^ (r & 7)) << 4), 0, 0, 0, 0);
       }
       if (Q.m > 0) {
         const uint32_t r2 = half2_bits(cur.ratio, cur.ratio);
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 v = sign_chunk<D>(cur, c, r2);
-          sts128(row + (D / 64 + (c >> 3)) * kAtomRows + (((c & 7) ^ (tid & 7)) << 4), v.x, v.y, v.z, v.w);
+        for (int ch = 0; ch < D / 8; ++ch) {
+          const uint4 v = sign_chunk<D>(cur, ch, r2);
+          sts128(row + (D / 64 + (ch >> 3)) * kAtomRows + (((ch & 7) ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
         }
       }
       fence_async();
       __syncwarp();
       if (lane == 0) bar_arrive(a_full(s));
     }
-  } else if (warp < 8) {
+  } else if (warp < 16) {
     // ---- results: thread = token; the row goes out through the operand stage that produced it
-    const int r = tid - 128;
-    for (int i = 0; i < mine; ++i) {
-      const int s = i & 1;
-      const int w = j0 + i * step, h = w / tiles, tile = w - h * tiles;
+    const int g = (warp >> 2) & 1, s = g, r = tid & 127;
+    for (int i = g; i < mine; i += 2) {
+      const int h = (w0 + i) / tiles, tile = (w0 + i) - h * tiles;
       wait(d_full(s), (i >> 1) & 1);
       tc_fence_after();
       const float f = scale_s[s * 128 + r];
@@ -452,7 +509,7 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
       }
       tc_fence_before();
       fence_async();
-      named_sync(2, 128);
+      named_sync(3 + g, 128);
       if (r == 0) {
         const uint32_t bytes = (D / 64) * kAtomRows;
         uint8_t* dst = (kind ? a.p.vrows : a.p.krows) + ((int64_t)h * a.p.max_tiles + tile) * bytes;
@@ -463,23 +520,30 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
       if (lane == 0) bar_arrive(d_empty(s));
     }
     if (r == 0) bulk_store_wait();
-  } else if (lane == 0) {
+  } else {
     // ---- contraction
-    const uint32_t atom_op = D * 128;
-    expect_tx(op_full, katoms * atom_op);
-    for (int k = 0; k < katoms; ++k) bulk_load(base + k * atom_op, (kind ? a.vops : a.kops) + k * atom_op, atom_op, op_full);
+    const uint32_t lead = elect_one();
+    constexpr uint32_t kAtomOp = D * 128;
+    if (lead) {
+      expect_tx(op_full, katoms * kAtomOp);
+      for (int k = 0; k < katoms; ++k) bulk_load(base + k * kAtomOp, (kind ? a.vops : a.kops) + k * kAtomOp, kAtomOp, op_full);
+    }
     wait(op_full, 0);
+    const uint64_t a_desc = sw128_desc(base + L::kA), b_desc = sw128_desc(base);
     for (int i = 0; i < mine; ++i) {
       const int s = i & 1;
       wait(a_full(s), (i >> 1) & 1);
       if (i >= 2) wait(d_empty(s), ((i >> 1) - 1) & 1);
       tc_fence_after();
+      const uint64_t ad = a_desc + ((s * L::kAStage) >> 4);
       for (int k = 0; k < katoms; ++k)
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_f16(tmem + s * 128, sw128_desc(base + L::kA + s * L::kAStage + k * kAtomRows + kk * 32),
-                  sw128_desc(base + k * atom_op + kk * 32), flash_idesc(D, false), (k | kk) > 0 ? 1u : 0u);
-      mma_commit(d_full(s));
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint64_t x = ad + ((k * kAtomRows + kk * 32) >> 4), y = b_desc + ((k * kAtomOp + kk * 32) >> 4);
+          if (k == 0 && kk == 0) mma_ss<false>(lead, tmem + s * 128, x, y, flash_idesc(D, false));
+          else mma_ss<true>(lead, tmem + s * 128, x, y, flash_idesc(D, false));
+        }
+      commit_one(lead, d_full(s));
     }
     // tensor memory is released below: the last contractions must have ended
     for (int i = max(0, mine - 2); i < mine; ++i) (void)wait_bar(d_full(i & 1), (i >> 1) & 1);
@@ -487,7 +551,7 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(256u) : "memory");
+  if (warp == 16) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(256u) : "memory");
 }
 
 // ---------------------------------------------------------------- queries
@@ -500,6 +564,8 @@ template <int D>
 __global__ void __launch_bounds__(256) paged_qtile_kernel(FlashArgs a) {
   constexpr int C = D / 32;   // chunks per lane
   const int item = blockIdx.x >> 2, h = blockIdx.y;
+  grid_dep_launch();
+  grid_dep_wait();
   if (item >= a.p.head[1]) return;
   const int ql = threadIdx.x & 3, r = (blockIdx.x & 3) * 64 + (threadIdx.x >> 2);
   const int rot = a.prep.cos_sin ? a.prep.rot_dim : 0, half = rot >> 1;
@@ -638,40 +704,17 @@ __device__ __forceinline__ uint64_t mn_desc16(uint32_t saddr) {
   return d;
 }
 
-// ---- issue by one lane of a whole warp: the warp stays together, so that addresses and descriptors live in uniform
-// registers (a lone thread spends longer on moving them there than the tensor cores on the instruction)
-__device__ __forceinline__ uint32_t elect_one() {
-  uint32_t r;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
-  return r;
-}
-template <bool ACC>
-__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc) {
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 q, %0, 0;\n setp.ne.u32 p, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%1], %2, %3, %4, p;\n}\n" ::"r"(leader),
-      "r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "n"(ACC ? 1 : 0));
-}
-// A in tensor memory (lane = row, 8 columns of two f16 per 16 K).
-__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 q, %0, 0;\n setp.ne.u32 p, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], %3, %4, p;\n}\n" ::"r"(leader),
-      "r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc));
-}
-__device__ __forceinline__ void commit_one(uint32_t leader, uint32_t bar) {
-  asm volatile(
-      "{\n .reg .pred q;\n setp.ne.u32 q, %0, 0;\n"
-      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n}\n" ::"r"(leader),
-      "r"(bar)
-      : "memory");
-}
-
 // CTA c of P takes units [c U / P, (c + 1) U / P) of the round's U = heads * units, head by head, item by item.
 struct Span {
   int64_t u0, u1;
 };
-__device__ __forceinline__ Span span_of(int64_t U, int c, int P) { return {U * c / P, U * (c + 1) / P}; }
+__device__ __forceinline__ Span span_of(int64_t U, int c, int P) {
+  if (U <= 0x1fffff && P < 2047) {   // 32-bit quotients do
+    const uint32_t u = (uint32_t)U, p = (uint32_t)P;
+    return {u * (uint32_t)c / p, u * (uint32_t)(c + 1) / p};
+  }
+  return {U * c / P, U * (c + 1) / P};
+}
 
 // A CTA's share of one item: key tiles [t0, t1) of nt.
 struct Segment {
@@ -770,6 +813,8 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
   unsigned char* const smem = smem_tiles;
   const uint32_t base = smem_addr(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  grid_dep_launch();
+  grid_dep_wait();
   const int items = a.p.head[1], units = a.p.head[2];
   const Span sp = span_of((int64_t)units * a.heads, blockIdx.x, gridDim.x);
   if ((base & 1023u) != 0) {
@@ -1106,6 +1151,8 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
 template <int D>
 __global__ void __launch_bounds__(kItemRows) paged_flash_merge_kernel(FlashArgs a) {
   const int c = blockIdx.x, P = a.ctas, r = threadIdx.x;
+  grid_dep_launch();
+  grid_dep_wait();
   const int items = a.p.head[1], units = a.p.head[2];
   const int64_t U = (int64_t)units * a.heads;
   const Span sp = span_of(U, c, P);

@@ -347,7 +347,8 @@ FlashPlan flash_plan(const tq_view& k, const Batch& b, int Hq, int Hkv, int smal
 }
 
 template <int D>
-int attn_flash(const AttnArgs& g, const tq_view& k, const tq_view& v, const FlashPlan& p, int small_rows, char* ws, cudaStream_t s) {
+int attn_flash(const AttnArgs& g, const tq_view& k, const tq_view& v, const FlashPlan& p, int small_rows, bool behind, char* ws,
+               cudaStream_t s) {
   static std::atomic<uint64_t> s1{0}, s2{0};
   int st;
   if ((st = allow_smem(paged_expand_kernel<D>, ExLayout<D>::kBytes, k.device, s1)) ||
@@ -367,29 +368,30 @@ int attn_flash(const AttnArgs& g, const tq_view& k, const tq_view& v, const Flas
   a.p.max_tiles = (int)p.max_tiles, a.p.max_items = (int)p.max_items;
   for (a.head0 = 0; a.head0 < a.Hkv; a.head0 += p.heads) {
     a.heads = std::min(p.heads, a.Hkv - a.head0);
-    {
+    if (a.head0 == 0) {   // one plan serves every round
       tq_launch_scope scope("paged_plan", s);
-      paged_plan_kernel<<<1, kPlanThreads, 0, s>>>(a);
+      // Only behind another kernel of this call: a call's first kernel starts when all work before it is done.
+      if (behind) {
+        if ((st = launch_after(paged_plan_kernel, dim3(1), kPlanThreads, 0, s, a, "paged_plan_kernel"))) return st;
+      } else {
+        paged_plan_kernel<<<1, kPlanThreads, 0, s>>>(a);
+        if ((st = launched("paged_plan_kernel"))) return st;
+      }
     }
-    if ((st = launched("paged_plan_kernel"))) return st;
     {
       tq_launch_scope scope("paged_qtile", s);
-      paged_qtile_kernel<D><<<dim3(4 * (unsigned)p.max_items, a.heads), 256, 0, s>>>(a);
+      if ((st = launch_after(paged_qtile_kernel<D>, dim3(4 * (unsigned)p.max_items, a.heads), 256, 0, s, a, "paged_qtile_kernel"))) return st;
     }
-    if ((st = launched("paged_qtile_kernel"))) return st;
     {
       tq_launch_scope scope("paged_expand", s);
-      paged_expand_kernel<D><<<2 * ((p.ctas + 1) / 2), kExThreads, ExLayout<D>::kBytes, s>>>(a);
+      if ((st = launch_after(paged_expand_kernel<D>, dim3(2 * ((p.ctas + 1) / 2)), kExThreads, ExLayout<D>::kBytes, s, a, "paged_expand_kernel"))) return st;
     }
-    if ((st = launched("paged_expand_kernel"))) return st;
     {
       tq_launch_scope scope("paged_flash", s);
-      paged_flash_kernel<D><<<p.ctas, kFlThreads, FlLayout<D>::kBytes, s>>>(a);
+      if ((st = launch_after(paged_flash_kernel<D>, dim3(p.ctas), kFlThreads, FlLayout<D>::kBytes, s, a, "paged_flash_kernel"))) return st;
     }
-    if ((st = launched("paged_flash_kernel"))) return st;
     tq_launch_scope scope("paged_merge", s);
-    paged_flash_merge_kernel<D><<<dim3(p.ctas, D / 16), kItemRows, 0, s>>>(a);
-    if ((st = launched("paged_flash_merge_kernel"))) return st;
+    if ((st = launch_after(paged_flash_merge_kernel<D>, dim3(p.ctas, D / 16), kItemRows, 0, s, a, "paged_flash_merge_kernel"))) return st;
   }
   return st;
 }
@@ -410,11 +412,11 @@ struct DecodePlan {
   size_t qr, part, total;
 };
 
-DecodePlan decode_plan(const tq_view& k, const tq_view& v, const Batch& b, int Hq, int Hkv, int sms) {
+DecodePlan decode_plan(const tq_view& k, const tq_view& v, const Batch& b, int Hkv, int sms) {
   DecodePlan p{};
   p.ctas = 2 * sms;
   p.qr = 0;
-  p.part = up((size_t)b.ntok * Hq * (k.d + k.m) * 4, 256);
+  p.part = up((size_t)b.B * Hkv * 8 * (k.d + k.m) * 4, 256);
   p.total = p.part + up(((size_t)p.ctas + (size_t)b.B * Hkv) * 8 * (v.d + v.m + 2) * 4, 256) + 256;
   return p;
 }
@@ -448,7 +450,7 @@ int attn_decode_paged(AttnArgs a, const tq_view& k, const tq_view& v, const Deco
   da.a = a, da.ctas = p.ctas;
   {
     tq_launch_scope scope("paged_qprep", s);
-    paged_qslice_kernel<<<dim3((unsigned)((a.bt.ntok * a.Hq + 7) / 8), (k.d + k.m) / 32), 256, 0, s>>>(da);
+    paged_qslice_kernel<<<dim3((unsigned)a.bt.B * a.Hkv, (k.d + k.m) / 32), 256, 0, s>>>(da);
   }
   if ((st = launched("paged_qslice_kernel"))) return st;
   const bool h = k.norm_dtype == TQ_F16;
@@ -460,16 +462,16 @@ int attn_decode_paged(AttnArgs a, const tq_view& k, const tq_view& v, const Deco
                       "paged_decode_merge_kernel");
 }
 
-// The largest of what the paths of a call may need; they run one after the other in the same space.
+// What the paths of a call may need. The single tokens' space lies before the chunks': their kernels may overlap.
 size_t attn_workspace(const tq_view& k, const tq_view& v, const Batch& b, int Hq, int Hkv) {
   const int sms = device_sms(k.device);
-  size_t n = simt_plan(k, v, b, Hq, Hkv, sms).total;
+  size_t n = 0;
   if (flash_formats(k, v)) {
     const int small = decode_formats(k, v, b) ? kSmallRows : 0;
-    if (small) n = std::max(n, decode_plan(k, v, b, Hq, Hkv, sms).total);
-    if ((int64_t)b.max_q * (Hq / Hkv) > small) n = std::max(n, flash_plan(k, b, Hq, Hkv, small, sms).total);
+    if (small) n += decode_plan(k, v, b, Hkv, sms).total;
+    if ((int64_t)b.max_q * (Hq / Hkv) > small) n += flash_plan(k, b, Hq, Hkv, small, sms).total;
   }
-  return n;
+  return std::max(n, simt_plan(k, v, b, Hq, Hkv, sms).total);
 }
 
 }  // namespace
@@ -550,10 +552,15 @@ int tq_attn_paged(const tq_handle* hk, const tq_handle* hv, const void* q, int q
   if (q_dtype != TQ_F32 && flash_formats(kw, vw)) {
     const int G = Hq / Hkv, small = decode_formats(kw, vw, a.bt) ? kSmallRows : 0;
     st = TQ_OK;
-    if (G <= small) st = attn_decode_paged(a, kw, vw, decode_plan(kw, vw, a.bt, Hq, Hkv, sms), ws, s);
+    if (small) {
+      const DecodePlan plan = decode_plan(kw, vw, a.bt, Hkv, sms);
+      if (G <= small) st = attn_decode_paged(a, kw, vw, plan, ws, s);
+      ws += plan.total;
+    }
     if (st || (int64_t)a.bt.max_q * G <= small) return st;
     const FlashPlan plan = flash_plan(kw, a.bt, Hq, Hkv, small, sms);
-    return kw.d == 128 ? attn_flash<128>(a, kw, vw, plan, small, ws, s) : attn_flash<64>(a, kw, vw, plan, small, ws, s);
+    return kw.d == 128 ? attn_flash<128>(a, kw, vw, plan, small, G <= small, ws, s)
+                       : attn_flash<64>(a, kw, vw, plan, small, G <= small, ws, s);
   }
   return attn_simt(a, kw, vw, simt_plan(kw, vw, a.bt, Hq, Hkv, sms), ws, kw.device, s);
 }
