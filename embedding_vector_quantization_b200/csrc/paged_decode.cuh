@@ -65,34 +65,48 @@ __device__ __forceinline__ int small_chunks(const AttnArgs& a, int b, int n, int
   return hi > lo ? (hi + kChunk - 1) / kChunk - first : 0;
 }
 
-// Running sums over the sequences of chunks * Hkv into pre[0 .. B], by the whole CTA of NT threads.
+// Running sums over the sequences of chunks * Hkv into pre[0 .. B], by the whole CTA of NT threads; returns the most chunks
+// of one (sequence, head).
 template <int NT>
-__device__ __forceinline__ void chunk_sums(const AttnArgs& a, int64_t* pre, int64_t* warp_s) {
+__device__ __forceinline__ int chunk_sums(const AttnArgs& a, int64_t* pre, int64_t* warp_s) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int64_t done = 0;
+  int most = 0;
   for (int b0 = 0; b0 < a.bt.B; b0 += NT) {
     const int b = b0 + tid;
-    int64_t v = 0;
+    int nch = 0;
     if (b < a.bt.B) {
       int first;
-      v = (int64_t)small_chunks(a, b, small_tokens(a, b), first) * a.Hkv;
+      nch = small_chunks(a, b, small_tokens(a, b), first);
     }
+    const int64_t v = (int64_t)nch * a.Hkv;
     int64_t incl = v;
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += u;
     }
-    if (lane == 31) warp_s[warp] = incl;
+    const int top = __reduce_max_sync(0xffffffffu, nch);
+    if (lane == 31) warp_s[warp] = incl, warp_s[NT / 32 + warp] = top;
     __syncthreads();
     int64_t before = done;
     for (int w = 0; w < warp; ++w) before += warp_s[w];
     if (b < a.bt.B) pre[b] = before + incl - v;
-    for (int w = 0; w < NT / 32; ++w) done += warp_s[w];
+    for (int w = 0; w < NT / 32; ++w) done += warp_s[w], most = max(most, (int)warp_s[NT / 32 + w]);
     __syncthreads();
   }
   if (tid == 0) pre[a.bt.B] = done;
   __syncthreads();
+  return most;
 }
+
+// How the units are shared out. While every (sequence, head) is short and has a CTA, each CTA takes one and finishes it: no
+// partial results (up to 96 chunks, 12 for each warp: a call for 16 x 12 heads of 1200 keys takes X us so and Y us cut).
+// Otherwise evenly, with at least 8 chunks for a CTA, one for each warp.
+constexpr int kWholeChunks = 96;
+__device__ __forceinline__ bool take_whole(const AttnArgs& a, int most, int ctas) {
+  return most <= kWholeChunks && (int64_t)a.bt.B * a.Hkv <= ctas;
+}
+__device__ __forceinline__ int even_parts(int64_t U, int ctas) { return (int)min((int64_t)ctas, max((int64_t)1, U >> 3)); }
 
 __device__ __forceinline__ int last_at_or_before64(const int64_t* start, int n, int64_t x) {
   int lo = 0, hi = n;
@@ -105,7 +119,7 @@ __device__ __forceinline__ int last_at_or_before64(const int64_t* start, int n, 
 }
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -151,8 +165,8 @@ __device__ __forceinline__ float lds_half(uint32_t a) {
 // at4, at8: the lane's copy in the table's first row, at a multiple of 32 KB.
 template <int B>
 __device__ __forceinline__ uint2 lut_byte(uint32_t w, int i, uint32_t at4, uint32_t at8) {
-  if (B == 4) return make_uint2(lds32(byte128(w, i) | at4), 0);
-  return lds64(byte128(w, i) | at8);
+  if (B == 4) return make_uint2(table32(byte128(w, i) | at4), 0);
+  return table64(byte128(w, i) | at8);
 }
 
 template <int D, int BK, int BV, bool SG, bool NF16>
@@ -165,22 +179,33 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   int64_t* pre = reinterpret_cast<int64_t*>(tables + L::kPre);
   float* stat = reinterpret_cast<float*>(tables + L::kStat);   // [warp][row] maximum, then [warp][row] sum
-  __shared__ int64_t warp_s[kDcWarps];
+  __shared__ int64_t warp_s[2 * kDcWarps];
   if (lut - base < L::kFrontWarps * L::kWarpRing) {   // more static memory than expected
     if (tid == 0) report_error(a.err, kErrInternal);
     return;
   }
   grid_dep_launch();
-  chunk_sums<kDcThreads>(a, pre, warp_s);
+  const int most = chunk_sums<kDcThreads>(a, pre, warp_s);
   const int64_t U = pre[a.bt.B];
-  const Span sp = span_of(U, blockIdx.x, gridDim.x);
+  const bool whole = take_whole(a, most, gridDim.x);
+  Span sp{0, 0};
+  if (whole) {
+    const int b = blockIdx.x / a.Hkv, h = blockIdx.x - b * a.Hkv;
+    const int n = b < a.bt.B ? small_tokens(a, b) : 0;
+    if (n > 0) {
+      const int64_t nch = (pre[b + 1] - pre[b]) / a.Hkv;
+      sp = {pre[b] + h * nch, pre[b] + (h + 1) * nch};
+      if (nch == 0)   // no keys
+        for (int e = tid; e < n * a.G * D; e += kDcThreads)
+          store_any(a.out, a.q_dtype, ((a.bt.q_start[b] + e / (a.G * D)) * (int64_t)a.Hq + h * a.G) * D + e % (a.G * D), 0.f);
+    }
+  } else if ((int)blockIdx.x < even_parts(U, gridDim.x)) {
+    sp = span_of(U, blockIdx.x, even_parts(U, gridDim.x));
+  }
   if (sp.u0 >= sp.u1) {
     grid_dep_wait();   // every CTA waits: a kernel behind this one may count on the one before
     return;
   }
-  build_lut(a.k, tables, tid, kDcThreads);
-  if (BK != BV) build_lut(a.v, tables + 32768, tid, kDcThreads);
-  __syncthreads();
   const uint32_t k4 = lut | 4 * lane, k8 = lut | 8 * (lane & 15);
   const uint32_t v4 = k4 + (L::kTables - 1) * 32768, v8 = k8 + (L::kTables - 1) * 32768;
   const uint32_t ring_off = warp < L::kFrontWarps ? warp * L::kWarpRing : lut - base + L::kBack + (warp - L::kFrontWarps) * L::kWarpRing;
@@ -189,7 +214,7 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
   constexpr int KW = (KB + 3) / 4, VW = (VB + 3) / 4;
   constexpr int KS = D / 16;                               // inner steps of the score product, and row tiles of the value one
   const int tk = (g >> 1) + 4 * (g & 1);                   // the token of score row g (row g + 8: 8 later)
-  grid_dep_wait();
+  bool tables_made = false;
 
   for (int64_t u = sp.u0; u < sp.u1;) {
     const int b = last_at_or_before64(pre, a.bt.B, u);
@@ -213,6 +238,71 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
         hi[j] = min(hi[j], pos + 1);
         if (a.window > 0) lo[j] = max(0, pos - a.window + 1);
       }
+    }
+    // ---- the warp's chunks: c0 + warp, + 8, ...; the ring holds those under way
+    const int mine = c1 - c0 > warp ? (c1 - c0 - warp + kDcWarps - 1) / kDcWarps : 0;
+    unsigned there = 0;   // bit (i mod 32): chunk i lies on a valid page
+    const uint32_t cpp = a.bt.page_size / kChunk;   // chunks of a page
+    const uint32_t inv = cpp > 1 ? 0xffffffffu / cpp + 1u : 0u;   // exact below 2^26 chunks
+    const int32_t* tab = a.bt.table + (int64_t)b * a.bt.max_pages;
+    const uint32_t ch0 = first + c0 + warp;
+    auto page_of = [&](int i) -> int {
+      const uint32_t ch = ch0 + i * kDcWarps;
+      return i < mine ? tab[cpp > 1 ? __umulhi(ch, inv) : ch] : -1;
+    };
+    // This lane's part in a copy: 16 bytes of the norms (lanes 0 ..), of the signs, and of each 512 bytes of codes.
+    constexpr int NB = NF16 ? 2 : 4;   // bytes of a norm
+    constexpr int NS = kChunk * L::kRowS / 16;
+    const char* n_src = nullptr;
+    uint32_t n_row = 0, n_dst = 0;
+    if (lane < 2 * NB) {
+      n_src = static_cast<const char*>(lane < NB ? a.kc.norms : a.vc.norms) + 16 * (lane & (NB - 1));
+      n_row = kChunk * NB, n_dst = (lane < NB ? L::kNormK : L::kNormV) + 16 * (lane & (NB - 1));
+    } else if (SG && lane < 2 * NB + 4) {
+      const int x = lane - 2 * NB;
+      n_src = reinterpret_cast<const char*>(x < 2 ? a.kc.rnorms : a.vc.rnorms) + 16 * (x & 1);
+      n_row = 2 * kChunk, n_dst = (x < 2 ? L::kNormK : L::kNormV) + 64 + 16 * (x & 1);
+    }
+    const uint32_t k_dst = spot<L::kRowK>(lane / (L::kRowK / 16), lane % (L::kRowK / 16) * 16);
+    const uint32_t v_dst = L::kEndK + spot<L::kRowV>(lane / (L::kRowV / 16), lane % (L::kRowV / 16) * 16);
+    int page = -1;            // of the chunk that is fetched next
+    uint32_t fill = 0;        // its stage's offset
+    auto fetch = [&](int i) {
+      bool ok = false;
+      if (i < mine) {
+        const uint32_t ch = ch0 + i * kDcWarps, pi = cpp > 1 ? __umulhi(ch, inv) : ch;
+        ok = page >= 0 && page < a.bt.num_pages;
+        if (ok) {
+          const uint32_t at = ((uint32_t)page * a.Hkv + h) * cpp + (ch - pi * cpp);   // the chunk among all (below 2^32)
+          const uint32_t st = ring + fill;
+          const uint8_t* ck = a.kc.codes + (uint64_t)at * (kChunk * L::kRowK) + 16 * lane;
+          const uint8_t* cv = a.vc.codes + (uint64_t)at * (kChunk * L::kRowV) + 16 * lane;
+          // 32 lanes further is 8 rows (of 64 bytes) further, which the rows' places follow
+          if (kChunk * L::kRowK / 16 >= 32 || lane < kChunk * L::kRowK / 16) cp16(st + k_dst, ck);
+          if (kChunk * L::kRowK / 16 > 32) cp16(st + k_dst + 512, ck + 512);
+          if (kChunk * L::kRowV / 16 >= 32 || lane < kChunk * L::kRowV / 16) cp16(st + v_dst, cv);
+          if (kChunk * L::kRowV / 16 > 32) cp16(st + v_dst + 512, cv + 512);
+          if (SG && lane < 2 * NS)
+            cp16(st + (lane < NS ? L::kSignK + 16 * lane : L::kSignV + 16 * (lane - NS)),
+                 (lane < NS ? a.kc.signs + 16 * lane : a.vc.signs + 16 * (lane - NS)) + (uint64_t)at * (kChunk * L::kRowS));
+          if (n_src) cp16(st + n_dst, n_src + (uint64_t)at * n_row);
+        } else if (lane == 0) {
+          report_error(a.err, kErrPaged);
+        }
+        page = page_of(i + 1);
+      }
+      there = ok ? there | 1u << (i & 31) : there & ~(1u << (i & 31));
+      fill = fill + L::kStage == L::kWarpRing ? 0 : fill + L::kStage;
+      asm volatile("cp.async.commit_group;\n" ::: "memory");
+    };
+    page = page_of(0);
+    for (int i = 0; i < L::kStages - 1; ++i) fetch(i);
+    if (!tables_made) {   // while the first copies are under way
+      tables_made = true;
+      build_lut(a.k, tables, tid, kDcThreads);
+      if (BK != BV) build_lut(a.v, tables + 32768, tid, kDcThreads);
+      grid_dep_wait();
+      __syncthreads();
     }
     // ---- queries: row g, this lane's coordinates, as f16 times a power of two
     uint32_t qc[2 * KS], qs[SG ? 2 * KS : 1];
@@ -284,61 +374,15 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
     int ve = 0;           // value norms are taken times 2^-ve
     float vdn = 0.f;      // 2^-ve; 0: no value yet
 
-    // ---- the warp's chunks: c0 + warp, + 8, ...; the ring holds those under way
-    const int mine = c1 - c0 > warp ? (c1 - c0 - warp + kDcWarps - 1) / kDcWarps : 0;
-    unsigned there = 0;   // bit (i mod 32): chunk i lies on a valid page
-    const int cpp = a.bt.page_size / kChunk;   // chunks of a page
-    const uint32_t inv = cpp > 1 ? (uint32_t)(0xffffffffu / (uint32_t)cpp) + 1u : 0u;   // exact below 2^26 chunks
-    const int32_t* tab = a.bt.table + (int64_t)b * a.bt.max_pages;
-    auto fetch = [&](int i) {
-      bool ok = false;
-      if (i < mine) {
-        const uint32_t ch = first + c0 + warp + i * kDcWarps, pi = cpp > 1 ? __umulhi(ch, inv) : ch;
-        const int page = tab[pi];
-        ok = page >= 0 && page < a.bt.num_pages;
-        if (ok) {
-          const int64_t at = ((int64_t)(page * (uint64_t)a.Hkv + h) * cpp + (ch - pi * cpp)) * kChunk;   // row of its first token
-          const uint32_t st = ring + (i % L::kStages) * L::kStage;
-          const uint8_t* ck = a.kc.codes + at * L::kRowK;
-          const uint8_t* cv = a.vc.codes + at * L::kRowV;
-#pragma unroll
-          for (int x = lane; x < kChunk * L::kRowK / 16; x += 32) {
-            const int r = x / (L::kRowK / 16), o = (x % (L::kRowK / 16)) * 16;
-            cp16(st + spot<L::kRowK>(r, o), ck + 16 * x);
-          }
-#pragma unroll
-          for (int x = lane; x < kChunk * L::kRowV / 16; x += 32) {
-            const int r = x / (L::kRowV / 16), o = (x % (L::kRowV / 16)) * 16;
-            cp16(st + L::kEndK + spot<L::kRowV>(r, o), cv + 16 * x);
-          }
-          if (SG) {
-            constexpr int NS = kChunk * L::kRowS / 16;
-            if (lane < NS) cp16(st + L::kSignK + 16 * lane, a.kc.signs + at * L::kRowS + 16 * lane);
-            else if (lane < 2 * NS) cp16(st + L::kSignV + 16 * (lane - NS), a.vc.signs + at * L::kRowS + 16 * (lane - NS));
-          }
-          constexpr int NB = NF16 ? 2 : 4;   // bytes of a norm
-          const char* nk = static_cast<const char*>(a.kc.norms) + at * NB;
-          const char* nv = static_cast<const char*>(a.vc.norms) + at * NB;
-          if (lane < NB) cp16(st + L::kNormK + 16 * lane, nk + 16 * lane);
-          else if (lane < 2 * NB) cp16(st + L::kNormV + 16 * (lane - NB), nv + 16 * (lane - NB));
-          else if (SG && lane < 2 * NB + 2) cp16(st + L::kNormK + 64 + 16 * (lane - 2 * NB), a.kc.rnorms + at + 8 * (lane - 2 * NB));
-          else if (SG && lane < 2 * NB + 4) cp16(st + L::kNormV + 64 + 16 * (lane - 2 * NB - 2), a.vc.rnorms + at + 8 * (lane - 2 * NB - 2));
-        } else if (lane == 0) {
-          report_error(a.err, kErrPaged);
-        }
-      }
-      there = ok ? there | 1u << (i & 31) : there & ~(1u << (i & 31));
-      asm volatile("cp.async.commit_group;\n" ::: "memory");
-    };
-    for (int i = 0; i < L::kStages - 1; ++i) fetch(i);
-    for (int i = 0; i < mine; ++i) {
+    uint32_t use = 0;         // the offset of the stage in use
+    for (int i = 0; i < mine; ++i, use = use + L::kStage == L::kWarpRing ? 0 : use + L::kStage) {
       __syncwarp();   // the stage that is filled next has been read by every lane
       fetch(i + L::kStages - 1);
       asm volatile("cp.async.wait_group %0;\n" ::"n"(L::kStages - 1) : "memory");
       __syncwarp();
       if (!(there >> (i & 31) & 1)) continue;
-      const uint32_t st = ring + (i % L::kStages) * L::kStage;
-      const int key0 = (first + c0 + warp + i * kDcWarps) * kChunk;
+      const uint32_t st = ring + use;
+      const int key0 = (ch0 + i * kDcWarps) * kChunk;
       auto norm_at = [&](uint32_t off, int r) -> float {
         if (NF16) return lds_half(st + off + 2 * r);
         return __uint_as_float(lds32(st + off + 4 * r));
@@ -448,14 +492,21 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
 #pragma unroll
         for (int j = 0; j < 4; ++j) lds_bytes<VB>(st + L::kEndK + spot<L::kRowV>(t + 4 * j, VB * g), w[j]);
         if (BV == 4) {
+          // The low nibbles of two tokens' bytes side by side, then the high ones: one table entry is the same coordinate
+          // of both tokens (byte y: coordinate 2 y -> row g of tile y, 2 y + 1 -> row g + 8).
+          uint32_t p[2][VW], q[2][VW];
 #pragma unroll
-          for (int y = 0; y < KS; ++y) {   // byte y: coordinates 2 y, 2 y + 1 -> rows g, g + 8 of tile y
-            uint32_t v[4];
+          for (int x = 0; x < VW; ++x)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = lut_byte<4>(w[j][y >> 2], y & 3, v4, v8).x;
-            mma16816(oc[y], __byte_perm(v[0], v[1], 0x5410), __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x5410),
-                     __byte_perm(v[2], v[3], 0x7632), b0, b1);
-          }
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t wa = w[2 * j][x], wb = w[2 * j + 1][x];
+              p[j][x] = (wa & 0x0f0f0f0fu) | ((wb << 4) & 0xf0f0f0f0u);
+              q[j][x] = ((wa >> 4) & 0x0f0f0f0fu) | (wb & 0xf0f0f0f0u);
+            }
+#pragma unroll
+          for (int y = 0; y < KS; ++y)
+            mma16816(oc[y], lut_byte<4>(p[0][y >> 2], y & 3, v4, v8).x, lut_byte<4>(q[0][y >> 2], y & 3, v4, v8).x,
+                     lut_byte<4>(p[1][y >> 2], y & 3, v4, v8).x, lut_byte<4>(q[1][y >> 2], y & 3, v4, v8).x, b0, b1);
         } else {
 #pragma unroll
           for (int y = 0; y < KS / 2; ++y) {   // byte y: coordinates 4 y .. 4 y + 3 -> tiles 2 y, 2 y + 1
@@ -528,22 +579,57 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
       }
     }
     __syncthreads();
-    float* part = a.part + ((int64_t)blockIdx.x + (int64_t)b * a.Hkv + h) * 8 * (L::kDV + 2);
-    for (int e = tid; e < 8 * L::kDV; e += kDcThreads) {   // [coordinate][row]
-      float s = 0.f;
+    float sum[L::kDV / 32];   // elements tid, tid + 256, ... of [coordinate][row]
+#pragma unroll
+    for (int k = 0; k < L::kDV / 32; ++k) {
+      sum[k] = 0.f;
 #pragma unroll
       for (int w = 0; w < kDcWarps; ++w)
-        s += reinterpret_cast<const float*>(w < L::kFrontWarps ? smem_dc + w * L::kWarpRing
-                                                               : tables + L::kBack + (w - L::kFrontWarps) * L::kWarpRing)[e];
-      part[e] = s;
+        sum[k] += reinterpret_cast<const float*>(w < L::kFrontWarps ? smem_dc + w * L::kWarpRing
+                                                                    : tables + L::kBack + (w - L::kFrontWarps) * L::kWarpRing)[tid + 256 * k];
     }
-    if (tid < 8) {
-      float mt = -INFINITY, lt = 0.f;
-      for (int w = 0; w < kDcWarps; ++w) mt = fmaxf(mt, stat[w * 8 + tid]);
-      for (int w = 0; w < kDcWarps; ++w) lt += stat[w * 8 + tid] == -INFINITY ? 0.f : stat[64 + w * 8 + tid] * ex2(stat[w * 8 + tid] - mt);
-      part[8 * L::kDV + tid] = mt, part[8 * L::kDV + 8 + tid] = lt;
+    float mt = -INFINITY, lt = 0.f;   // of row tid mod 8
+    for (int w = 0; w < kDcWarps; ++w) mt = fmaxf(mt, stat[w * 8 + (tid & 7)]);
+    for (int w = 0; w < kDcWarps; ++w) {
+      const float mw = stat[w * 8 + (tid & 7)];
+      lt += mw == -INFINITY ? 0.f : stat[64 + w * 8 + (tid & 7)] * ex2(mw - mt);
     }
-    __syncthreads();   // before the ring and the statistics are written again
+    if (!whole) {
+      float* part = a.part + ((int64_t)blockIdx.x + (int64_t)b * a.Hkv + h) * 8 * (L::kDV + 2);
+#pragma unroll
+      for (int k = 0; k < L::kDV / 32; ++k) part[tid + 256 * k] = sum[k];
+      if (tid < 8) part[8 * L::kDV + tid] = mt, part[8 * L::kDV + 8 + tid] = lt;
+      __syncthreads();   // before the ring and the statistics are written again
+      continue;
+    }
+    // the only item: its result, through the first warps' rings
+    __syncthreads();
+    float* acc = reinterpret_cast<float*>(smem_dc);          // [8][D], then [8][D] of the signs
+    float* part_s = acc + 8 * L::kDV;                        // [8][256]
+    float* o1 = part_s + 8 * 256;                            // [8][D]
+    static_assert((8 * L::kDV + 2048 + 8 * D) * 4 <= L::kFrontWarps * L::kWarpRing, "the finish must fit before the tables");
+    const float inv_l = lt > 0.f ? 1.f / lt : 0.f;
+#pragma unroll
+    for (int k = 0; k < L::kDV / 32; ++k) {
+      const int e = tid + 256 * k, r = e & 7, j = e >> 3;
+      acc[j < D ? r * D + j : 8 * D + r * D + j - D] = sum[k] * inv_l;
+    }
+    __syncthreads();
+    rows_matvec<8>(acc, D, a.v.Pi, D, part_s, o1);
+    float y[D / 32];
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) y[k] = o1[tid + 256 * k];
+    if (SG) {
+      __syncthreads();
+      rows_matvec<8>(acc + 8 * D, D, a.v.S, D, part_s, o1);
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) y[k] = fmaf(kQjlScale / (float)D, o1[tid + 256 * k], y[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) {
+      const int e = tid + 256 * k, r = e / D, x = e % D;
+      if (r < rows) store_any(a.out, a.q_dtype, ((a.bt.q_start[b] + r / a.G) * (int64_t)a.Hq + h * a.G + r % a.G) * D + x, y[k]);
+    }
   }
 }
 
@@ -614,16 +700,15 @@ __global__ void __launch_bounds__(256) paged_decode_merge_kernel(DecodeArgs da) 
   const AttnArgs& a = da.a;
   const int d = a.v.d, m = a.v.m, dv = d + m, b = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_dep_launch();
-  const int P = da.ctas;
   float* acc = reinterpret_cast<float*>(smem);        // [8][d], then [8][m]
   float* part_s = acc + 8 * dv;                       // [8][256]
   float* o1 = part_s + 8 * 256;                       // [256]
   float* o2 = o1 + 256;
-  float* wgt = o2 + 256;                              // [P][8] weights of the parts
-  int* cta = reinterpret_cast<int*>(wgt + 8 * P);     // [P] the CTAs that hold one
+  float* wgt = o2 + 256;                              // [CTAs][8] weights of the parts
+  int* cta = reinterpret_cast<int*>(wgt + 8 * da.ctas);   // [CTAs] those that hold one
   __shared__ int64_t sums[8], sums2[8];
   __shared__ float f[8];
-  __shared__ int parts;
+  __shared__ int parts, tops[8];
   const int n = small_tokens(a, b);
   if (n == 0) {
     grid_dep_wait();
@@ -633,18 +718,27 @@ __global__ void __launch_bounds__(256) paged_decode_merge_kernel(DecodeArgs da) 
   const int nch = small_chunks(a, b, n, first);
   // the units before this sequence, and all of them
   int64_t before = 0, all = 0;
+  int most = 0;
   for (int x = tid; x < a.bt.B; x += 256) {
     int f0;
-    const int64_t v = (int64_t)small_chunks(a, x, small_tokens(a, x), f0) * a.Hkv;
+    const int nx = small_chunks(a, x, small_tokens(a, x), f0);
+    const int64_t v = (int64_t)nx * a.Hkv;
+    most = max(most, nx);
     all += v;
     if (x < b) before += v;
   }
   for (int o = 16; o; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o), all += __shfl_xor_sync(0xffffffffu, all, o);
-  if (lane == 0) sums[warp] = before, sums2[warp] = all;
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 0) sums[warp] = before, sums2[warp] = all, tops[warp] = most;
   if (tid == 0) parts = 0;
   __syncthreads();
   before = all = 0;
-  for (int w = 0; w < 8; ++w) before += sums[w], all += sums2[w];
+  for (int w = 0; w < 8; ++w) before += sums[w], all += sums2[w], most = max(most, tops[w]);
+  if (take_whole(a, most, da.ctas)) {   // finished already
+    grid_dep_wait();
+    return;
+  }
+  const int P = even_parts(all, da.ctas);
   const int64_t u0 = before + (int64_t)h * nch, u1 = u0 + nch;
   if (warp == 0) {   // the CTAs whose units meet [u0, u1), in order
     int np = 0;

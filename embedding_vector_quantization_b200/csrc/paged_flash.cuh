@@ -260,6 +260,23 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
 }
+// Table entries: the table does not change once it is built, so these need not stay in order (in order, each product would
+// wait for its own entries before the next ones are asked for).
+__device__ __forceinline__ uint32_t table32(uint32_t a) {
+  uint32_t v;
+  asm("ld.shared.u32 %0, [%1];\n" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 table64(uint32_t a) {
+  uint2 v;
+  asm("ld.shared.v2.u32 {%0, %1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint4 table128(uint32_t a) {
+  uint4 v;
+  asm("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
 // (w >> 8 i & 255) * 128: byte i as a table offset, one shift and one mask
 __device__ __forceinline__ uint32_t byte128(uint32_t w, int i) { return (i == 0 ? w << 7 : w >> (8 * i - 7)) & 0x7f80u; }
 
@@ -269,19 +286,19 @@ __device__ __forceinline__ uint4 code_chunk(const Row<D>& r, int bits, int c, ui
   uint4 v = make_uint4(0, 0, 0, 0);
   if (bits == 4) {
     const uint32_t w = r.code[c], b = 4 * lane;
-    v = make_uint4(lds32(lut + (byte128(w, 0) | b)), lds32(lut + (byte128(w, 1) | b)), lds32(lut + (byte128(w, 2) | b)),
-                   lds32(lut + (byte128(w, 3) | b)));
+    v = make_uint4(table32(lut + (byte128(w, 0) | b)), table32(lut + (byte128(w, 1) | b)), table32(lut + (byte128(w, 2) | b)),
+                   table32(lut + (byte128(w, 3) | b)));
   } else if (bits == 2) {
     const uint32_t w = r.code[c >> 1], b = 8 * (lane & 15);
-    const uint2 x = lds64(lut + (byte128(w, 2 * (c & 1)) | b)), y = lds64(lut + (byte128(w, 2 * (c & 1) + 1) | b));
+    const uint2 x = table64(lut + (byte128(w, 2 * (c & 1)) | b)), y = table64(lut + (byte128(w, 2 * (c & 1) + 1) | b));
     v = make_uint4(x.x, x.y, y.x, y.y);
   } else if (bits == 1) {
-    v = lds128(lut + 16 * (lane & 7) + (((r.code[c >> 2] >> (8 * (c & 3))) & 255u) << 7));
+    v = table128(lut + 16 * (lane & 7) + (((r.code[c >> 2] >> (8 * (c & 3))) & 255u) << 7));
   } else if (bits == 3) {   // 24 bits from bit 24 c on
     const int w0 = (24 * c) >> 5, sh = (24 * c) & 31;
     const uint32_t x = __funnelshift_r(r.code[w0], r.code[min(w0 + 1, D / 8 - 1)], sh), b = lut + 4 * lane;
-    v = make_uint4(lds32(b + ((x & 63u) << 7)), lds32(b + ((x >> 6 & 63u) << 7)), lds32(b + ((x >> 12 & 63u) << 7)),
-                   lds32(b + ((x >> 18 & 63u) << 7)));
+    v = make_uint4(table32(b + ((x & 63u) << 7)), table32(b + ((x >> 6 & 63u) << 7)), table32(b + ((x >> 12 & 63u) << 7)),
+                   table32(b + ((x >> 18 & 63u) << 7)));
   }
   return v;
 }

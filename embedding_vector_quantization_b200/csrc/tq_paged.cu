@@ -401,8 +401,9 @@ int attn_flash(const AttnArgs& g, const tq_view& k, const tq_view& v, const Flas
 constexpr int kSmallRows = 8;   // query rows of a sequence and KV head that the single-token kernel takes: its product's columns
 
 // Whether the single-token kernel has these formats: 4- or 2-bit codes, signs on both sides or on neither.
-bool decode_formats(const tq_view& k, const tq_view& v, const Batch& b) {
+bool decode_formats(const tq_view& k, const tq_view& v, const Batch& b, int Hkv) {
   if (!flash_formats(k, v) || k.norm_dtype != v.norm_dtype || b.B > kDcMaxB) return false;
+  if (b.num_pages * Hkv * (b.page_size / kChunk) > 0xffffffffll) return false;   // its chunk numbers have 32 bits
   if (k.m > 0 || v.m > 0) return k.m == k.d && v.m == v.d && k.bits == 2 && v.bits == 2;
   return (k.bits == 4 && (v.bits == 4 || v.bits == 2)) || (k.bits == 2 && v.bits == 2);
 }
@@ -456,7 +457,8 @@ int attn_decode_paged(AttnArgs a, const tq_view& k, const tq_view& v, const Deco
   const bool h = k.norm_dtype == TQ_F16;
   if (k.d == 128) st = h ? decode_formats_launch<128, true>(da, k.device, s) : decode_formats_launch<128, false>(da, k.device, s);
   else st = h ? decode_formats_launch<64, true>(da, k.device, s) : decode_formats_launch<64, false>(da, k.device, s);
-  if (st) return st;
+  // when every sequence fits a CTA there is nothing to merge
+  if (st || ((int64_t)a.bt.max_pages * a.bt.page_size <= kWholeChunks * kChunk && (int64_t)a.bt.B * a.Hkv <= p.ctas)) return st;
   tq_launch_scope scope("paged_dmerge", s);
   return launch_after(paged_decode_merge_kernel, dim3((unsigned)a.bt.B, (unsigned)a.Hkv, k.d / 32), 256, merge, s, da,
                       "paged_decode_merge_kernel");
@@ -467,7 +469,7 @@ size_t attn_workspace(const tq_view& k, const tq_view& v, const Batch& b, int Hq
   const int sms = device_sms(k.device);
   size_t n = 0;
   if (flash_formats(k, v)) {
-    const int small = decode_formats(k, v, b) ? kSmallRows : 0;
+    const int small = decode_formats(k, v, b, Hkv) ? kSmallRows : 0;
     if (small) n += decode_plan(k, v, b, Hkv, sms).total;
     if ((int64_t)b.max_q * (Hq / Hkv) > small) n += flash_plan(k, b, Hq, Hkv, small, sms).total;
   }
@@ -550,7 +552,7 @@ int tq_attn_paged(const tq_handle* hk, const tq_handle* hv, const void* q, int q
   char* ws = reinterpret_cast<char*>(up(reinterpret_cast<size_t>(workspace), 256));
   const int sms = device_sms(kw.device);
   if (q_dtype != TQ_F32 && flash_formats(kw, vw)) {
-    const int G = Hq / Hkv, small = decode_formats(kw, vw, a.bt) ? kSmallRows : 0;
+    const int G = Hq / Hkv, small = decode_formats(kw, vw, a.bt, Hkv) ? kSmallRows : 0;
     st = TQ_OK;
     if (small) {
       const DecodePlan plan = decode_plan(kw, vw, a.bt, Hkv, sms);
