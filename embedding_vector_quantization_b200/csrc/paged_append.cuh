@@ -23,7 +23,6 @@ namespace paged {
 
 constexpr float kBandY = 46.f * 5.9604645e-8f;
 constexpr int kAppThreads = 256;
-constexpr int kAppMaxRows = 8;
 
 struct AppendArgs {
   const void* x[2];       // keys, values
@@ -36,32 +35,33 @@ struct AppendArgs {
   int* err;
 };
 
-__host__ __device__ inline size_t append_smem_bytes(int d, int m, int R) {
+__host__ __device__ inline size_t append_smem_bytes(int d, int m, int R, int threads) {
   const int w = d > m ? d : m;
-  return (size_t)R * d * 8 + 2 * (size_t)R * w * 4 + (size_t)R * w + (size_t)kAppThreads * R * 4 + 64;
+  return (size_t)R * d * 8 + 2 * (size_t)R * w * 4 + (size_t)R * w + (size_t)threads * R * 4 + 64;
 }
 
 // out[r][j] = sum_i in[r][i] T[i][j] for the CTA's R rows: thread (j, part) sums its share of i in chunks of 32.
-template <int R>
+template <int R, int NT = kAppThreads>
 __device__ __forceinline__ void rows_matvec(const float* in, int ni, const float* T, int nj, float* part_s, float* out) {
+  constexpr int kStep = NT > 256 ? 16 : 32;   // chunk; the bound above holds for chunks of 32 and less
   const int tid = threadIdx.x;
-  const int parts = max(1, min(kAppThreads / nj, ni / 32));
+  const int parts = max(1, min(NT / nj, ni / kStep));
   const int j = tid % nj, part = tid / nj;
   float acc[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) acc[r] = 0.f;
   if (part < parts) {
-    const int chunks = ni / 32;
+    const int chunks = ni / kStep;
     for (int c = part; c < chunks; c += parts) {
       float s[R];
 #pragma unroll
       for (int r = 0; r < R; ++r) s[r] = 0.f;
-      const float* t = T + (size_t)(32 * c) * nj + j;
+      const float* t = T + (size_t)(kStep * c) * nj + j;
 #pragma unroll 16
-      for (int i = 0; i < 32; ++i) {
+      for (int i = 0; i < kStep; ++i) {
         const float p = __ldg(t + (size_t)i * nj);
 #pragma unroll
-        for (int r = 0; r < R; ++r) s[r] = fmaf(in[r * ni + 32 * c + i], p, s[r]);
+        for (int r = 0; r < R; ++r) s[r] = fmaf(in[r * ni + kStep * c + i], p, s[r]);
       }
 #pragma unroll
       for (int r = 0; r < R; ++r) acc[r] += s[r];
@@ -70,7 +70,7 @@ __device__ __forceinline__ void rows_matvec(const float* in, int ni, const float
     for (int r = 0; r < R; ++r) part_s[(r * parts + part) * nj + j] = acc[r];
   }
   __syncthreads();
-  for (int e = tid; e < R * nj; e += kAppThreads) {
+  for (int e = tid; e < R * nj; e += NT) {
     const int r = e / nj, jj = e - r * nj;
     float s = 0.f;
     for (int p = 0; p < parts; ++p) s += part_s[(r * parts + p) * nj + jj];
@@ -79,9 +79,10 @@ __device__ __forceinline__ void rows_matvec(const float* in, int ni, const float
   __syncthreads();
 }
 
-// Grid: (row groups of R, 2): y = 0 keys, 1 values; row = token * Hkv + head.
-template <int R>
-__global__ void __launch_bounds__(kAppThreads) paged_append_kernel(AppendArgs a) {
+// Grid: (row groups of R, 2): y = 0 keys, 1 values; row = token * Hkv + head. d <= 32 MAXC. One row and 1024 threads where latency counts
+// (the products' loads are then all under way at once), eight rows and 256 threads where there are many.
+template <int R, int NT, int MAXC>
+__global__ void __launch_bounds__(NT) paged_append_kernel(AppendArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   const int kind = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Quant& Q = a.q[kind];
@@ -90,7 +91,7 @@ __global__ void __launch_bounds__(kAppThreads) paged_append_kernel(AppendArgs a)
   float* zf = reinterpret_cast<float*>(zd + (size_t)R * d);      // [R][w] z, then e
   float* ys = zf + (size_t)R * w;                                // [R][w] y, then M e
   float* part_s = ys + (size_t)R * w;                            // [256 R]
-  uint8_t* idx = reinterpret_cast<uint8_t*>(part_s + (size_t)kAppThreads * R);   // [R][w] indices, then signs
+  uint8_t* idx = reinterpret_cast<uint8_t*>(part_s + (size_t)NT * R);   // [R][w] indices, then signs
   __shared__ int64_t place[R];
   __shared__ double nrm[R], cd[16], bd[16];
   __shared__ float cf[16], bf[16];
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(kAppThreads) paged_append_kernel(AppendArgs a)
     bf[tid] = (float)bd[tid], cf[tid] = (float)cd[tid];
   }
   const int64_t row0 = (int64_t)blockIdx.x * R, rows = a.bt.ntok * a.Hkv;
-  for (int r = warp; r < R; r += kAppThreads / 32) {
+  for (int r = warp; r < R; r += NT / 32) {
     const int64_t row = row0 + r;
     int64_t t;
     int h;
@@ -124,17 +125,17 @@ __global__ void __launch_bounds__(kAppThreads) paged_append_kernel(AppendArgs a)
       bad = at < 0;
     }
     if (bad && lane == 0) report_error(a.err, kErrPaged);
-    double z[8];
+    double z[MAXC];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) z[c] = 0.0;
+    for (int c = 0; c < MAXC; ++c) z[c] = 0.0;
     double ss = 0.0;
     if (at >= 0) {
       Prep pr = a.prep;
       if (kind == 1) pr.cos_sin = nullptr, pr.weight = nullptr;
-      prep_head<double, 8>(a.x[kind], a.x_dtype, t * a.stride[kind] + (int64_t)h * d, d, pr, rp, z);
+      prep_head<double, MAXC>(a.x[kind], a.x_dtype, t * a.stride[kind] + (int64_t)h * d, d, pr, rp, z);
     }
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
+    for (int c = 0; c < MAXC; ++c)
       if (lane + 32 * c < d) {
         zd[r * d + lane + 32 * c] = z[c];
         zf[r * d + lane + 32 * c] = (float)z[c];
@@ -149,10 +150,10 @@ __global__ void __launch_bounds__(kAppThreads) paged_append_kernel(AppendArgs a)
   for (int r = 0; r < R; ++r) any |= place[r] >= 0;
   if (!any) return;
 
-  rows_matvec<R>(zf, d, Q.PiT, d, part_s, ys);
+  rows_matvec<R, NT>(zf, d, Q.PiT, d, part_s, ys);
   // indices; a coordinate within the band of a border is computed again by the whole warp
   const float* one = cf;
-  for (int e0 = warp * 32; e0 < R * d; e0 += kAppThreads) {   // d % 32 = 0: the warp stays in one row
+  for (int e0 = warp * 32; e0 < R * d; e0 += NT) {   // d % 32 = 0: the warp stays in one row
     const int e = e0 + lane, r = e / d;
     const double n = nrm[r];
     float y = n > 0.0 ? ys[e] / (float)n : 0.f;
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(kAppThreads) paged_append_kernel(AppendArgs a)
   }
   // codes: word by word, LSB first
   const int cw = Q.codes_B / 4;
-  for (int e = tid; e < R * cw; e += kAppThreads) {
+  for (int e = tid; e < R * cw; e += NT) {
     const int r = e / cw, wd = e - r * cw;
     if (place[r] < 0) continue;
     uint32_t v = 0;
@@ -206,9 +207,9 @@ __global__ void __launch_bounds__(kAppThreads) paged_append_kernel(AppendArgs a)
   __syncthreads();
   if (tid < R && place[tid] >= 0 && bits > 0)
     a.c[kind].rnorms[place[tid]] = __double2half(nrm[tid] * sqrt((double)esum[tid]));
-  rows_matvec<R>(zf, d, Q.MT, m, part_s, ys);
+  rows_matvec<R, NT>(zf, d, Q.MT, m, part_s, ys);
   const float band = Q.m_abs * (kBandY + 1.2e-7f) + 43.f * 5.9604645e-8f * Q.m_norm;
-  for (int e0 = warp * 32; e0 < R * m; e0 += kAppThreads) {
+  for (int e0 = warp * 32; e0 < R * m; e0 += NT) {
     const int e = e0 + lane, r = e / m;
     const double n = nrm[r];
     bool pos = ys[e] >= 0.f;

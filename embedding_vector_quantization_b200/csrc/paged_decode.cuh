@@ -775,7 +775,7 @@ __global__ void __launch_bounds__(256) paged_decode_merge_kernel(DecodeArgs da) 
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = 0.f;
     const int nk = dv / 32;
-#pragma unroll 4
+#pragma unroll 8
     for (int c = 0; c < np; ++c) {
       const float w = wgt[c * 8 + (tid & 7)];
       const float* p = part + cta[c] * size + tid;

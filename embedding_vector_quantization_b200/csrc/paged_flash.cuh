@@ -47,7 +47,7 @@ constexpr uint32_t kAtomRows = 128 * 128;   // 128 rows of 64 f16: one swizzle a
 
 // Plan, in the workspace (ints): what plan_kernel writes.
 struct Plan {
-  int* head;         // [0] key tiles, [1] items, [2] units of one head
+  int* head;         // [0] key tiles, [1] items, [2] units of one head, [3] the largest item's units
   int* tile_start;   // [B + 1] first key tile of a sequence
   int* item_start;   // [B + 1] first item of a sequence
   int* unit;         // [items + 1] running sum of the items' costs, within one head
@@ -151,14 +151,14 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(FlashArgs a) {
   if (tiles > a.p.max_tiles || items > a.p.max_items) {   // q_start is not ascending: nothing is computed
     if (tid == 0) {
       report_error(a.err, kErrPaged);
-      a.p.head[0] = a.p.head[1] = a.p.head[2] = 0;
+      a.p.head[0] = a.p.head[1] = a.p.head[2] = a.p.head[3] = 0;
     }
     grid_dep_wait();
     return;
   }
   if (tid == 0) a.p.tile_start[a.bt.B] = tiles, a.p.item_start[a.bt.B] = items;
   __syncthreads();
-  int units = 0;
+  int units = 0, most = 0;
   for (int i0 = 0; i0 < items; i0 += kPlanThreads) {
     const int i = i0 + tid;
     int w = 0;
@@ -172,10 +172,17 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(FlashArgs a) {
     const int u = block_scan(w, warp_s, total);
     if (i < items) a.p.unit[i] = units + u;
     units += total;
+    most = max(most, w);
   }
+  __shared__ int top_s;
+  if (tid == 0) top_s = 0;
+  __syncthreads();
+  most = __reduce_max_sync(0xffffffffu, most);
+  if ((tid & 31) == 0) atomicMax(&top_s, most);
+  __syncthreads();
   if (tid == 0) {
     a.p.unit[items] = units;
-    a.p.head[0] = tiles, a.p.head[1] = items, a.p.head[2] = units;
+    a.p.head[0] = tiles, a.p.head[1] = items, a.p.head[2] = units, a.p.head[3] = top_s;
   }
   grid_dep_wait();   // nothing here needs the kernel before (single tokens); what follows may count on it
 }
@@ -401,7 +408,6 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
     if (tid == 0) report_error(a.err, kErrInternal);
     return;
   }
-  grid_dep_launch();
   if (tid == 0) {
     *abort_flag = 0;
     uint64_t* b = reinterpret_cast<uint64_t*>(smem + L::kBars);
@@ -410,6 +416,7 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
   }
   build_lut(Q, smem + L::kLut, tid, kExThreads);
   grid_dep_wait();
+  grid_dep_launch();   // only now: the next kernel reads the plan too
   const int tiles = a.p.head[0];
   const int64_t work = (int64_t)tiles * a.heads;
   const int w0 = (int)(work * j0 / step), mine = (int)(work * (j0 + 1) / step) - w0;
@@ -576,17 +583,22 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
 // Query rows to f16 tiles, as the attention wants them in shared memory: norm, rotation, then times the power of two that
 // brings every coordinate below one. Four lanes per row; lane q of them holds the 16-byte chunks q, q + 4, ...: the partners
 // of a rotation of the whole head (half a head away) are its own. Bound by latency and bytes: as many rows in flight as fit.
-// Grid: (max_items * 4, heads): 64 rows per CTA.
+// Grid: (max_items * 8, heads): 32 rows per CTA, small enough to run beside the expansion's CTAs: it is started when all of
+// those run, which have seen the plan complete, and needs nothing of theirs.
+constexpr int kQtThreads = 128;
 template <int D>
-__global__ void __launch_bounds__(256) paged_qtile_kernel(FlashArgs a) {
+__global__ void __launch_bounds__(kQtThreads) paged_qtile_kernel(FlashArgs a) {
   constexpr int C = D / 32;   // chunks per lane
-  const int item = blockIdx.x >> 2, h = blockIdx.y;
+  const int item = blockIdx.x >> 3, h = blockIdx.y;
   grid_dep_launch();
-  grid_dep_wait();
-  if (item >= a.p.head[1]) return;
-  const int ql = threadIdx.x & 3, r = (blockIdx.x & 3) * 64 + (threadIdx.x >> 2);
+  if (item >= a.p.head[1] && (item | h) > 0) return;
+  const int ql = threadIdx.x & 3, r = (blockIdx.x & 7) * 32 + (threadIdx.x >> 2);
   const int rot = a.prep.cos_sin ? a.prep.rot_dim : 0, half = rot >> 1;
   const bool f16 = a.q_dtype == TQ_F16;
+  if (item >= a.p.head[1]) {   // no item at all
+    grid_dep_wait();
+    return;
+  }
   const int b = last_at_or_before(a.p.item_start, a.bt.B, item), n = seq_rows(a, b);
   const int64_t t0 = a.bt.q_start[b], slot = (int64_t)h * a.p.max_items + item;
   const int pos0 = a.bt.len[b] - n, row = (item - a.p.item_start[b]) * kItemRows + r;
@@ -685,6 +697,7 @@ __global__ void __launch_bounds__(256) paged_qtile_kernel(FlashArgs a) {
         make_uint4(half2_bits(z[8 * c] * sc, z[8 * c + 1] * sc), half2_bits(z[8 * c + 2] * sc, z[8 * c + 3] * sc),
                    half2_bits(z[8 * c + 4] * sc, z[8 * c + 5] * sc), half2_bits(z[8 * c + 6] * sc, z[8 * c + 7] * sc));
   }
+  if (item == 0 && h == 0) grid_dep_wait();   // what follows may count on the expansion: this kernel ends behind it
 }
 
 // ---------------------------------------------------------------- flash
@@ -731,6 +744,22 @@ __device__ __forceinline__ Span span_of(int64_t U, int c, int P) {
     return {u * (uint32_t)c / p, u * (uint32_t)(c + 1) / p};
   }
   return {U * c / P, U * (c + 1) / P};
+}
+
+// What CTA c does: its even share, or one whole item where every item has a CTA and the largest is at most kWholeSlack key
+// tiles above the share (about 2.4 us each at d = 128: less than writing, reading and merging cut items takes).
+constexpr int kWholeSlack = 8;
+__device__ __forceinline__ bool whole_items(const FlashArgs& a) {
+  const int items = a.p.head[1], P = a.ctas;
+  const int64_t U = (int64_t)a.p.head[2] * a.heads;
+  return (int64_t)items * a.heads <= P && a.p.head[3] <= U / P + kWholeSlack;
+}
+__device__ __forceinline__ Span flash_span(const FlashArgs& a, int c) {
+  const int items = a.p.head[1], units = a.p.head[2];
+  if (!whole_items(a)) return span_of((int64_t)units * a.heads, c, a.ctas);
+  if (c >= items * a.heads) return {0, 0};
+  const int h = c / items, i = c - h * items;
+  return {(int64_t)h * units + a.p.unit[i], (int64_t)h * units + a.p.unit[i + 1]};
 }
 
 // A CTA's share of one item: key tiles [t0, t1) of nt.
@@ -833,7 +862,7 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
   grid_dep_launch();
   grid_dep_wait();
   const int items = a.p.head[1], units = a.p.head[2];
-  const Span sp = span_of((int64_t)units * a.heads, blockIdx.x, gridDim.x);
+  const Span sp = flash_span(a, blockIdx.x);
   if ((base & 1023u) != 0) {
     if (tid == 0) report_error(a.err, kErrInternal);
     return;
@@ -1172,6 +1201,7 @@ __global__ void __launch_bounds__(kItemRows) paged_flash_merge_kernel(FlashArgs 
   grid_dep_wait();
   const int items = a.p.head[1], units = a.p.head[2];
   const int64_t U = (int64_t)units * a.heads;
+  if (whole_items(a)) return;
   const Span sp = span_of(U, c, P);
   if (sp.u0 >= sp.u1) return;
   const Segment s = segment_at(a, items, units, sp.u1 - 1, sp.u1);

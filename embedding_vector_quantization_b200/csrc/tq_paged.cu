@@ -178,14 +178,14 @@ int device_sms(int device) {
 
 // ---------------------------------------------------------------- append
 
-template <int R>
+template <int R, int NT, int MAXC>
 int append_simt(const AppendArgs& a, int device, cudaStream_t s) {
   static std::atomic<uint64_t> seen{0};
-  if (int st = allow_smem(paged_append_kernel<R>, append_smem_bytes(256, 256, R), device, seen)) return st;
+  if (int st = allow_smem(paged_append_kernel<R, NT, MAXC>, append_smem_bytes(256, 256, R, NT), device, seen)) return st;
   const int m = std::max(a.q[0].m, a.q[1].m);
   const unsigned groups = (unsigned)((a.bt.ntok * a.Hkv + R - 1) / R);
   tq_launch_scope scope("append_paged", s);
-  paged_append_kernel<R><<<dim3(groups, 2), kAppThreads, append_smem_bytes(a.q[0].d, m, R), s>>>(a);
+  paged_append_kernel<R, NT, MAXC><<<dim3(groups, 2), NT, append_smem_bytes(a.q[0].d, m, R, NT), s>>>(a);
   return launched("paged_append_kernel");
 }
 
@@ -379,12 +379,12 @@ int attn_flash(const AttnArgs& g, const tq_view& k, const tq_view& v, const Flas
       }
     }
     {
-      tq_launch_scope scope("paged_qtile", s);
-      if ((st = launch_after(paged_qtile_kernel<D>, dim3(4 * (unsigned)p.max_items, a.heads), 256, 0, s, a, "paged_qtile_kernel"))) return st;
-    }
-    {
       tq_launch_scope scope("paged_expand", s);
       if ((st = launch_after(paged_expand_kernel<D>, dim3(2 * ((p.ctas + 1) / 2)), kExThreads, ExLayout<D>::kBytes, s, a, "paged_expand_kernel"))) return st;
+    }
+    {
+      tq_launch_scope scope("paged_qtile", s);
+      if ((st = launch_after(paged_qtile_kernel<D>, dim3(8 * (unsigned)p.max_items, a.heads), kQtThreads, 0, s, a, "paged_qtile_kernel"))) return st;
     }
     {
       tq_launch_scope scope("paged_flash", s);
@@ -507,8 +507,9 @@ int tq_append_paged(const tq_handle* hk, const tq_handle* hv, const void* k_new,
   a.err = kw.err;
   const int64_t rows = batch->ntok * Hkv;
   if (rows >= kAppendTcRows && kw.ops_app && vw.ops_app && !simt_forced()) return append_tc(a, kw, vw, s);
-  if (rows <= device_sms(kw.device)) return append_simt<1>(a, kw.device, s);
-  return append_simt<8>(a, kw.device, s);
+  const bool few = rows <= 2 * device_sms(kw.device);
+  if (kw.d <= 128) return few ? append_simt<1, 1024, 4>(a, kw.device, s) : append_simt<8, kAppThreads, 4>(a, kw.device, s);
+  return few ? append_simt<1, 1024, 8>(a, kw.device, s) : append_simt<8, kAppThreads, 8>(a, kw.device, s);
 }
 
 size_t tq_attn_paged_workspace_bytes(const tq_handle* hk, const tq_handle* hv, const tq_paged_batch* batch, int Hq, int Hkv,
