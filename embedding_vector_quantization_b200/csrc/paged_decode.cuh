@@ -169,7 +169,37 @@ __device__ __forceinline__ uint2 lut_byte(uint32_t w, int i, uint32_t at4, uint3
   return table64(byte128(w, i) | at8);
 }
 
-template <int D, int BK, int BV, bool SG, bool NF16>
+// out[r][j] = sum_i in[r][i] T[i][j] for 8 rows and a D x D matrix; a thread asks for all of its share of T at once (one
+// latency where rows_matvec has four). part_s: [8][256] floats. Not inlined: its code is fetched once for up to four products.
+template <int D>
+__device__ __noinline__ void rows_at_once(const float* in, const float* T, float* part_s, float* out) {
+  constexpr int kParts = kDcThreads / D, kShare = D / kParts;
+  const int tid = threadIdx.x, j = tid % D, part = tid / D;
+  float p[kShare], acc[8];
+#pragma unroll
+  for (int i = 0; i < kShare; ++i) p[i] = __ldg(T + (size_t)(part * kShare + i) * D + j);
+#pragma unroll
+  for (int r = 0; r < 8; ++r) acc[r] = 0.f;
+#pragma unroll
+  for (int i = 0; i < kShare; ++i)
+#pragma unroll
+    for (int r = 0; r < 8; ++r) acc[r] = fmaf(in[r * D + part * kShare + i], p[i], acc[r]);
+#pragma unroll
+  for (int r = 0; r < 8; ++r) part_s[(r * kParts + part) * D + j] = acc[r];
+  __syncthreads();
+#pragma unroll
+  for (int e = tid; e < 8 * D; e += kDcThreads) {
+    float s = 0.f;
+#pragma unroll
+    for (int q = 0; q < kParts; ++q) s += part_s[(e / D * kParts + q) * D + e % D];
+    out[e] = s;
+  }
+  __syncthreads();
+}
+
+// ONE: the tables are so narrow that every item is whole; the CTA prepares its queries itself, and this is the call's only
+// kernel.
+template <int D, int BK, int BV, bool SG, bool NF16, bool ONE>
 __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs da) {
   using L = DcLayout<D, BK, BV, SG>;
   extern __shared__ __align__(128) unsigned char smem_dc[];
@@ -187,7 +217,7 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
   grid_dep_launch();
   const int most = chunk_sums<kDcThreads>(a, pre, warp_s);
   const int64_t U = pre[a.bt.B];
-  const bool whole = take_whole(a, most, gridDim.x);
+  const bool whole = ONE || take_whole(a, most, gridDim.x);
   Span sp{0, 0};
   if (whole) {
     const int b = blockIdx.x / a.Hkv, h = blockIdx.x - b * a.Hkv;
@@ -297,19 +327,56 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
     };
     page = page_of(0);
     for (int i = 0; i < L::kStages - 1; ++i) fetch(i);
-    if (!tables_made) {   // while the first copies are under way
-      tables_made = true;
-      build_lut(a.k, tables, tid, kDcThreads);
-      if (BK != BV) build_lut(a.v, tables + 32768, tid, kDcThreads);
-      grid_dep_wait();
+    // ---- rotated queries, while the first copies are under way
+    constexpr int DK = D + (SG ? D : 0);
+    const float* src;
+    if (ONE) {   // by this CTA, in the tables' place
+      float* zf = reinterpret_cast<float*>(tables);     // [8][D]
+      float* part_s = zf + 8 * D;                       // [8][256]
+      float* o = part_s + 8 * 256;                      // [8][D]
+      float* qq = o + 8 * D;                            // [8][DK]
+      float z[D / 32];
+      bool blind = false;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) z[c] = 0.f;
+      if (warp < rows) {
+        const int i = warp / a.G;
+        const int64_t t0 = a.bt.q_start[b] + i;
+        const int64_t p = a.prep.pos ? (int64_t)a.prep.pos[t0] : (int64_t)len - n + i;
+        if (a.prep.cos_sin && (p < 0 || p >= a.prep.max_pos)) {
+          if (lane == 0 && (a.prep.pos || p >= 0)) report_error(a.err, kErrPaged);
+          blind = true;   // it sees nothing
+        } else {
+          prep_head<float, D / 32>(a.q, a.q_dtype, t0 * a.q_stride + (int64_t)(h * a.G + warp - i * a.G) * D, D, a.prep, p, z);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) zf[warp * D + lane + 32 * c] = z[c];
       __syncthreads();
+      const float f1 = a.scale * 1.44269504089f;
+      rows_at_once<D>(zf, a.k.PiT, part_s, o);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) qq[warp * DK + lane + 32 * c] = blind ? kBlind : o[warp * D + lane + 32 * c] * f1;
+      if (SG) {
+        __syncthreads();
+        rows_at_once<D>(zf, a.k.ST, part_s, o);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) qq[warp * DK + D + lane + 32 * c] = blind ? kBlind : o[warp * D + lane + 32 * c] * (f1 * kQjlScale / (float)D);
+      }
+      __syncthreads();
+      src = qq + g * DK;
+    } else {
+      if (!tables_made) {
+        build_lut(a.k, tables, tid, kDcThreads);
+        if (BK != BV) build_lut(a.v, tables + 32768, tid, kDcThreads);
+      }
+      grid_dep_wait();
+      src = a.qr + (((int64_t)b * a.Hkv + h) * 8 + g) * DK;
     }
     // ---- queries: row g, this lane's coordinates, as f16 times a power of two
     uint32_t qc[2 * KS], qs[SG ? 2 * KS : 1];
     float fc[2], fs[2];
     {
-      constexpr int DK = D + (SG ? D : 0);
-      const float* src = a.qr + (((int64_t)b * a.Hkv + h) * 8 + g) * DK;
       float z[D / 4];
       float top = 0.f;
       bool blind = false;
@@ -357,6 +424,15 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
         }
         fs[0] = __shfl_sync(0xffffffffu, upf, 8 * t), fs[1] = __shfl_sync(0xffffffffu, upf, 8 * t + 4);
       }
+    }
+    if (!tables_made) {
+      tables_made = true;
+      if (ONE) {
+        __syncthreads();   // the queries have been read
+        build_lut(a.k, tables, tid, kDcThreads);
+        if (BK != BV) build_lut(a.v, tables + 32768, tid, kDcThreads);
+      }
+      __syncthreads();
     }
     int lo_w = max(lo[0], lo[1]), hi_w = min(2 * t < rows ? hi[0] : INT_MAX, 2 * t + 1 < rows ? hi[1] : INT_MAX);
     lo_w = max(lo_w, __shfl_xor_sync(0xffffffffu, lo_w, 1)), lo_w = max(lo_w, __shfl_xor_sync(0xffffffffu, lo_w, 2));
@@ -615,13 +691,13 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
       acc[j < D ? r * D + j : 8 * D + r * D + j - D] = sum[k] * inv_l;
     }
     __syncthreads();
-    rows_matvec<8>(acc, D, a.v.Pi, D, part_s, o1);
+    rows_at_once<D>(acc, a.v.Pi, part_s, o1);
     float y[D / 32];
 #pragma unroll
     for (int k = 0; k < D / 32; ++k) y[k] = o1[tid + 256 * k];
     if (SG) {
       __syncthreads();
-      rows_matvec<8>(acc + 8 * D, D, a.v.S, D, part_s, o1);
+      rows_at_once<D>(acc + 8 * D, a.v.S, part_s, o1);
 #pragma unroll
       for (int k = 0; k < D / 32; ++k) y[k] = fmaf(kQjlScale / (float)D, o1[tid + 256 * k], y[k]);
     }

@@ -125,6 +125,19 @@ __device__ __forceinline__ int last_at_or_before(const int* start, int n, int x)
   return lo;
 }
 
+// The same by a whole warp, 32 places at a time: two steps up to 1024 places.
+__device__ __forceinline__ int warp_last_at_or_before(const int* start, int n, int x) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) >> 5, at = lo + lane * step;
+    const int count = __popc(__ballot_sync(0xffffffffu, at < hi && start[at] <= x));   // start ascends: the first ones
+    lo += max(0, count - 1) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(FlashArgs a) {
   __shared__ int warp_s[32];
   const int tid = threadIdx.x;
@@ -375,7 +388,7 @@ __device__ __forceinline__ void cursor_seek(const FlashArgs& a, int tiles, TileC
   c.tile += step;
   while (c.tile >= tiles) c.tile -= tiles, ++c.h;
   if (c.tile >= c.first && c.tile < c.last) return;
-  c.b = last_at_or_before(a.p.tile_start, a.bt.B, c.tile);
+  c.b = warp_last_at_or_before(a.p.tile_start, a.bt.B, c.tile);
   c.first = a.p.tile_start[c.b], c.last = a.p.tile_start[c.b + 1];
   const int n = seq_rows(a, c.b);
   int lo;
@@ -599,7 +612,7 @@ __global__ void __launch_bounds__(kQtThreads) paged_qtile_kernel(FlashArgs a) {
     grid_dep_wait();
     return;
   }
-  const int b = last_at_or_before(a.p.item_start, a.bt.B, item), n = seq_rows(a, b);
+  const int b = warp_last_at_or_before(a.p.item_start, a.bt.B, item), n = seq_rows(a, b);
   const int64_t t0 = a.bt.q_start[b], slot = (int64_t)h * a.p.max_items + item;
   const int pos0 = a.bt.len[b] - n, row = (item - a.p.item_start[b]) * kItemRows + r;
   const bool live = row < n * a.G;
@@ -762,7 +775,7 @@ __device__ __forceinline__ Span flash_span(const FlashArgs& a, int c) {
   return {(int64_t)h * units + a.p.unit[i], (int64_t)h * units + a.p.unit[i + 1]};
 }
 
-// A CTA's share of one item: key tiles [t0, t1) of nt.
+// A CTA's share of one item: key tiles [t0, t1) of nt. Found by whole warps.
 struct Segment {
   int h, item, b, n, row0, nrows, lo_tile, nt, t0, t1;
   int64_t next;   // first unit after the item
@@ -772,10 +785,10 @@ __device__ __forceinline__ Segment segment_at(const FlashArgs& a, int items, int
   Segment s;
   s.h = (int)(u / units);
   const int r = (int)(u - (int64_t)s.h * units);
-  s.item = last_at_or_before(a.p.unit, items, r);
+  s.item = warp_last_at_or_before(a.p.unit, items, r);
   s.first = (int64_t)s.h * units + a.p.unit[s.item];
   s.next = (int64_t)s.h * units + a.p.unit[s.item + 1];
-  s.b = last_at_or_before(a.p.item_start, a.bt.B, s.item);
+  s.b = warp_last_at_or_before(a.p.item_start, a.bt.B, s.item);
   s.n = seq_rows(a, s.b);
   s.row0 = (s.item - a.p.item_start[s.b]) * kItemRows;
   s.nrows = min(kItemRows, s.n * a.G - s.row0);
@@ -904,11 +917,12 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
 
   if (warp == 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
-    if (lane == 0) {
-      int k = 0, seg = 0;   // tiles issued (keys and values counted apart), segments with tiles
-      for (int64_t u = sp.u0; u < sp.u1;) {
-        const Segment s = segment_at(a, items, units, u, sp.u1);
-        u = s.next;
+    int k = 0, seg = 0;   // tiles issued (keys and values counted apart), segments with tiles
+    for (int64_t u = sp.u0; u < sp.u1;) {
+      const Segment s = segment_at(a, items, units, u, sp.u1);
+      u = s.next;
+      if (s.t1 <= s.t0) continue;
+      if (lane == 0) {
         const int64_t t = (int64_t)s.h * a.p.max_tiles + a.p.tile_start[s.b] + s.lo_tile;
         for (int j = s.t0; j < s.t1; ++j)
           for (int kv = 0; kv < 2; ++kv, ++k) {
@@ -928,8 +942,10 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
               ++seg;
             }
           }
-        if (*abort_flag) break;
       }
+      if (__any_sync(0xffffffffu, *abort_flag != 0)) break;   // the whole warp, or its next search would wait for a lane
+    }
+    if (lane == 0) {
       // never leave with a copy still landing in this CTA's shared memory
       for (int i = max(0, k - kFlStages); i < k; ++i) (void)wait_bar(full(i % kFlStages), (i / kFlStages) & 1);
       if (seg > 0)

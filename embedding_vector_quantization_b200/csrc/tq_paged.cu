@@ -422,21 +422,28 @@ DecodePlan decode_plan(const tq_view& k, const tq_view& v, const Batch& b, int H
   return p;
 }
 
-template <int D, int BK, int BV, bool SG, bool NF16>
-int decode_launch(const DecodeArgs& a, int device, cudaStream_t s) {
+template <int D, int BK, int BV, bool SG, bool NF16, bool ONE>
+int decode_launch_as(const DecodeArgs& a, int device, cudaStream_t s) {
   static std::atomic<uint64_t> seen{0};
   using L = DcLayout<D, BK, BV, SG>;
-  if (int st = allow_smem(paged_decode_kernel<D, BK, BV, SG, NF16>, L::bytes(kDcMaxB), device, seen)) return st;
+  constexpr auto kernel = paged_decode_kernel<D, BK, BV, SG, NF16, ONE>;
+  if (int st = allow_smem(kernel, L::bytes(kDcMaxB), device, seen)) return st;
   tq_launch_scope scope("paged_decode", s);
-  return launch_after(paged_decode_kernel<D, BK, BV, SG, NF16>, dim3(a.ctas), kDcThreads, L::bytes(a.a.bt.B), s, a,
-                      "paged_decode_kernel");
+  if (!ONE) return launch_after(kernel, dim3(a.ctas), kDcThreads, L::bytes(a.a.bt.B), s, a, "paged_decode_kernel");
+  kernel<<<a.ctas, kDcThreads, L::bytes(a.a.bt.B), s>>>(a);   // the call's first kernel
+  return launched("paged_decode_kernel");
+}
+
+template <int D, int BK, int BV, bool SG, bool NF16>
+int decode_launch(const DecodeArgs& a, bool one, int device, cudaStream_t s) {
+  return one ? decode_launch_as<D, BK, BV, SG, NF16, true>(a, device, s) : decode_launch_as<D, BK, BV, SG, NF16, false>(a, device, s);
 }
 
 template <int D, bool NF16>
-int decode_formats_launch(const DecodeArgs& a, int device, cudaStream_t s) {
-  if (a.a.k.m > 0) return decode_launch<D, 2, 2, true, NF16>(a, device, s);
-  if (a.a.k.bits == 2) return decode_launch<D, 2, 2, false, NF16>(a, device, s);
-  return a.a.v.bits == 4 ? decode_launch<D, 4, 4, false, NF16>(a, device, s) : decode_launch<D, 4, 2, false, NF16>(a, device, s);
+int decode_formats_launch(const DecodeArgs& a, bool one, int device, cudaStream_t s) {
+  if (a.a.k.m > 0) return decode_launch<D, 2, 2, true, NF16>(a, one, device, s);
+  if (a.a.k.bits == 2) return decode_launch<D, 2, 2, false, NF16>(a, one, device, s);
+  return a.a.v.bits == 4 ? decode_launch<D, 4, 4, false, NF16>(a, one, device, s) : decode_launch<D, 4, 2, false, NF16>(a, one, device, s);
 }
 
 int attn_decode_paged(AttnArgs a, const tq_view& k, const tq_view& v, const DecodePlan& p, char* ws, cudaStream_t s) {
@@ -449,16 +456,19 @@ int attn_decode_paged(AttnArgs a, const tq_view& k, const tq_view& v, const Deco
   a.small_rows = kSmallRows;
   DecodeArgs da{};
   da.a = a, da.ctas = p.ctas;
-  {
+  // The tables' width may tell that every sequence is short enough for one CTA: then one kernel does it all.
+  const bool one = (int64_t)a.bt.max_pages * a.bt.page_size <= kWholeChunks * kChunk && (int64_t)a.bt.B * a.Hkv <= p.ctas;
+  if (one) {
+    da.ctas = a.bt.B * a.Hkv;
+  } else {
     tq_launch_scope scope("paged_qprep", s);
     paged_qslice_kernel<<<dim3((unsigned)a.bt.B * a.Hkv, (k.d + k.m) / 32), 256, 0, s>>>(da);
+    if ((st = launched("paged_qslice_kernel"))) return st;
   }
-  if ((st = launched("paged_qslice_kernel"))) return st;
   const bool h = k.norm_dtype == TQ_F16;
-  if (k.d == 128) st = h ? decode_formats_launch<128, true>(da, k.device, s) : decode_formats_launch<128, false>(da, k.device, s);
-  else st = h ? decode_formats_launch<64, true>(da, k.device, s) : decode_formats_launch<64, false>(da, k.device, s);
-  // when every sequence fits a CTA there is nothing to merge
-  if (st || ((int64_t)a.bt.max_pages * a.bt.page_size <= kWholeChunks * kChunk && (int64_t)a.bt.B * a.Hkv <= p.ctas)) return st;
+  if (k.d == 128) st = h ? decode_formats_launch<128, true>(da, one, k.device, s) : decode_formats_launch<128, false>(da, one, k.device, s);
+  else st = h ? decode_formats_launch<64, true>(da, one, k.device, s) : decode_formats_launch<64, false>(da, one, k.device, s);
+  if (st || one) return st;
   tq_launch_scope scope("paged_dmerge", s);
   return launch_after(paged_decode_merge_kernel, dim3((unsigned)a.bt.B, (unsigned)a.Hkv, k.d / 32), 256, merge, s, da,
                       "paged_decode_merge_kernel");
