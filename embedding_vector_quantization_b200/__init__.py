@@ -235,6 +235,7 @@ class PagedCache:
         self.device = self.norms.device
         _need(all(t is None or t.device == self.device for t in (self.codes, self.signs, self.rnorms)),
               "the cache's tensors must be on one device")
+        self.index = self.norms.get_device()
         self.struct = make_paged_cache(self.codes, self.signs, self.norms, self.rnorms, num_pages, page_size)
 
 
@@ -252,7 +253,7 @@ class PagedBatch:
         _need(q_start.shape[0] == len_.shape[0] + 1 and block_table.shape[0] == len_.shape[0],
               "q_start [B + 1], len [B] and block_table [B, max_pages] disagree")
         self.q_start, self.len, self.block_table, self.ntok = q_start, len_, block_table, int(ntok)
-        self.device = len_.device
+        self.device, self.index = len_.device, len_.get_device()
         self.struct = make_paged_batch(q_start, len_, block_table, ntok, ntok if max_q is None else max_q)
 
 
@@ -275,27 +276,47 @@ class HeadPrep:
             _need(weight.dtype in (torch.float32, torch.float16, torch.bfloat16) and weight.dim() == 1
                   and weight.is_contiguous() and weight.is_cuda, "weight: contiguous [d] on the GPU wanted")
         self.cos_sin, self.pos, self.weight = cos_sin, pos, weight
-        self.devices = {t.device for t in (cos_sin, pos, weight) if t is not None}
+        index = {t.get_device() for t in (cos_sin, pos, weight) if t is not None}
+        _need(len(index) <= 1, "cos_sin, pos and weight are on different devices")
+        self.index = index.pop() if index else None
         self.struct = make_head_prep(cos_sin, pos, weight, interleaved, eps)
 
 
 def _head_rows(x, name, ntok, d):
     """x [ntok, H, d] with contiguous heads and 16-byte token strides; copied (on the current stream) if it is laid out
     otherwise."""
-    _need(x.is_cuda and x.dim() == 3 and x.shape[0] == ntok and x.shape[2] == d, f"{name}: [ntok, heads, {d}] on the GPU wanted")
-    if (x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != d) or x.stride(0) < x.shape[1] * d
-            or x.stride(0) * x.element_size() % 16 or x.data_ptr() % 16):
+    if x.dim() != 3 or not x.is_cuda or x.shape[0] != ntok or x.shape[2] != d:
+        _need(False, f"{name}: [{ntok}, heads, {d}] on the GPU wanted")
+    s0, s1, s2 = x.stride()
+    H = x.shape[1]
+    if (s2 != 1 or (H > 1 and s1 != d) or s0 < H * d or s0 * x.element_size() % 16 or x.data_ptr() % 16):
         x = x.clone(memory_format=_torch().contiguous_format)
     return x
 
 
 def _check_paged(kcache, vcache, batch, prep, d):
-    _need(kcache.Hkv == vcache.Hkv, "the caches differ in Hkv")
-    _need(kcache.device == vcache.device == batch.device, "caches and batch are on different devices")
+    if kcache.Hkv != vcache.Hkv:
+        _need(False, "the caches differ in Hkv")
+    if not kcache.index == vcache.index == batch.index:
+        _need(False, "caches and batch are on different devices")
     if prep is not None:
-        _need(prep.devices <= {kcache.device}, "prep is on another device")
-        _need(prep.weight is None or prep.weight.shape[0] == d, "weight: one value for each of the head's coordinates wanted")
-        _need(prep.pos is None or prep.pos.shape[0] >= batch.ntok, "pos: one position for each token row wanted")
+        if prep.index is not None and prep.index != kcache.index:
+            _need(False, "prep is on another device")
+        if prep.weight is not None and prep.weight.shape[0] != d:
+            _need(False, "weight: one value for each of the head's coordinates wanted")
+        if prep.pos is not None and prep.pos.shape[0] < batch.ntok:
+            _need(False, "pos: one position for each token row wanted")
+
+
+def _raw_stream(index):
+    """The current stream of a device, as the address the library takes."""
+    return _torch().cuda.current_stream(index).cuda_stream
+
+
+try:   # the same without a Stream object around it: calls for single tokens are bound by the host
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream  # noqa: F811
+except ImportError:
+    pass
 
 
 def _on(stream, device):
@@ -313,10 +334,12 @@ def append_paged(hk, hv, k, v, kcache, vcache, batch, prep=None, stream=None):
             return append_paged(hk, hv, k, v, kcache, vcache, batch, prep)
     _check_paged(kcache, vcache, batch, prep, hk.d)
     k, v = _head_rows(k, "k", batch.ntok, hk.d), _head_rows(v, "v", batch.ntok, hk.d)
-    _need(k.shape[1] == v.shape[1] == kcache.Hkv, "k and v need one head for each of the caches'")
-    _need(k.device == v.device == kcache.device, "k, v and the caches are on different devices")
+    if not k.shape[1] == v.shape[1] == kcache.Hkv:
+        _need(False, "k and v need one head for each of the caches'")
+    if not k.get_device() == v.get_device() == kcache.index:
+        _need(False, "k, v and the caches are on different devices")
     tq_append_paged(hk.ptr, hv.ptr, k, v, kcache.Hkv, batch.struct, None if prep is None else prep.struct, kcache.struct,
-                    vcache.struct, _torch().cuda.current_stream(kcache.device))
+                    vcache.struct, _raw_stream(kcache.index))
 
 
 def attn_paged(hk, hv, q, kcache, vcache, batch, scale, causal=True, window=0, prep=None, out=None, workspace=None,
@@ -327,21 +350,20 @@ def attn_paged(hk, hv, q, kcache, vcache, batch, scale, causal=True, window=0, p
     if stream is not None:
         with _on(stream, kcache.device):
             return attn_paged(hk, hv, q, kcache, vcache, batch, scale, causal, window, prep, out, workspace)
-    torch = _torch()
     _check_paged(kcache, vcache, batch, prep, hk.d)
     q = _head_rows(q, "q", batch.ntok, hk.d)
     Hq = q.shape[1]
-    _need(q.device == kcache.device, "q and the caches are on different devices")
+    if q.get_device() != kcache.index:
+        _need(False, "q and the caches are on different devices")
     if out is None:
-        out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
-    else:
-        _need(out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous() and out.device == q.device,
-              "out: contiguous, of q's shape, dtype and device wanted")
+        out = _torch().zeros(q.shape, dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or out.get_device() != kcache.index:
+        _need(False, "out: contiguous, of q's shape, dtype and device wanted")
     if workspace is None:
         size = tq_attn_paged_workspace_bytes(hk.ptr, hv.ptr, batch.struct, Hq, kcache.Hkv, kcache.struct)
-        workspace = torch.empty(max(16, size), dtype=torch.uint8, device=q.device)
-    else:
-        _need(workspace.is_cuda and workspace.device == q.device and workspace.is_contiguous(), "workspace on another device")
+        workspace = _torch().empty(max(16, size), dtype=_torch().uint8, device=q.device)
+    elif workspace.get_device() != kcache.index or not workspace.is_contiguous():
+        _need(False, "workspace: contiguous and on q's device wanted")
     tq_attn_paged(hk.ptr, hv.ptr, q, Hq, kcache.Hkv, batch.struct, None if prep is None else prep.struct, kcache.struct,
-                  vcache.struct, scale, causal, window, out, workspace, torch.cuda.current_stream(q.device))
+                  vcache.struct, scale, causal, window, out, workspace, _raw_stream(kcache.index))
     return out

@@ -313,12 +313,24 @@ def _ref(struct):
     return None if struct is None else ctypes.byref(struct)
 
 
+_codes = {}   # torch dtype -> code, filled at the first use
+
+
+def _code(t):
+    if not _codes:
+        import torch
+        _codes.update({torch.float32: TQ_F32, torch.float16: TQ_F16, torch.bfloat16: TQ_BF16})
+    return _codes[t.dtype]
+
+
 def tq_append_paged(hk, hv, k_new, v_new, Hkv, batch, prep, kcache, vcache, stream=None):
     """k_new, v_new [ntok, Hkv, d] with contiguous heads (the token stride is the tensors' own)."""
     if k_new.dtype != v_new.dtype:
         raise TQError(TQ_EINVAL, "tq_append_paged", "k_new and v_new must have one dtype")
-    check(lib.tq_append_paged(hk, hv, _ptr(k_new), _ptr(v_new), _dtype_code(k_new), k_new.stride(0), v_new.stride(0), Hkv,
-                              _ref(batch), _ref(prep), _ref(kcache), _ref(vcache), _stream(stream)), "tq_append_paged")
+    st = lib.tq_append_paged(hk, hv, k_new.data_ptr(), v_new.data_ptr(), _code(k_new), k_new.stride(0), v_new.stride(0), Hkv,
+                             _ref(batch), _ref(prep), _ref(kcache), _ref(vcache), _stream(stream))
+    if st:
+        check(st, "tq_append_paged")
 
 
 def tq_attn_paged_workspace_bytes(hk, hv, batch, Hq, Hkv, kcache):
@@ -328,9 +340,11 @@ def tq_attn_paged_workspace_bytes(hk, hv, batch, Hq, Hkv, kcache):
 
 def tq_attn_paged(hk, hv, q, Hq, Hkv, batch, prep, kcache, vcache, scale, causal, window, out, workspace, stream=None):
     """q [ntok, Hq, d] with contiguous heads (the token stride is the tensor's own), out contiguous of q's dtype."""
-    check(lib.tq_attn_paged(hk, hv, _ptr(q), _dtype_code(q), q.stride(0), Hq, Hkv, _ref(batch), _ref(prep), _ref(kcache),
-                            _ref(vcache), scale, int(bool(causal)), window, _ptr(out), _ptr(workspace),
-                            workspace.numel() * workspace.element_size(), _stream(stream)), "tq_attn_paged")
+    st = lib.tq_attn_paged(hk, hv, q.data_ptr(), _code(q), q.stride(0), Hq, Hkv, _ref(batch), _ref(prep), _ref(kcache),
+                           _ref(vcache), scale, 1 if causal else 0, window, out.data_ptr(), workspace.data_ptr(),
+                           workspace.numel() * workspace.element_size(), _stream(stream))
+    if st:
+        check(st, "tq_attn_paged")
 
 
 def tq_timer_enable(on):
