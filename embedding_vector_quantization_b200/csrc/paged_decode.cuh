@@ -169,26 +169,29 @@ __device__ __forceinline__ uint2 lut_byte(uint32_t w, int i, uint32_t at4, uint3
   return table64(byte128(w, i) | at8);
 }
 
-// out[r][j] = sum_i in[r][i] T[i][j] for 8 rows and a D x D matrix; a thread asks for all of its share of T at once (one
+// out[r][j] = sum_i in[r][i] T[i][j] for nr <= 8 rows (16-byte aligned) and a D x D matrix; a thread asks for all of its share of T at once (one
 // latency where rows_matvec has four). part_s: [8][256] floats. Not inlined: its code is fetched once for up to four products.
 template <int D>
-__device__ __noinline__ void rows_at_once(const float* in, const float* T, float* part_s, float* out) {
+__device__ __noinline__ void rows_at_once(const float* in, int nr, const float* T, float* part_s, float* out) {
   constexpr int kParts = kDcThreads / D, kShare = D / kParts;
   const int tid = threadIdx.x, j = tid % D, part = tid / D;
-  float p[kShare], acc[8];
+  float p[kShare];
 #pragma unroll
   for (int i = 0; i < kShare; ++i) p[i] = __ldg(T + (size_t)(part * kShare + i) * D + j);
+#pragma unroll 2
+  for (int r = 0; r < nr; ++r) {
+    const float4* x = reinterpret_cast<const float4*>(in + r * D + part * kShare);
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int r = 0; r < 8; ++r) acc[r] = 0.f;
-#pragma unroll
-  for (int i = 0; i < kShare; ++i)
-#pragma unroll
-    for (int r = 0; r < 8; ++r) acc[r] = fmaf(in[r * D + part * kShare + i], p[i], acc[r]);
-#pragma unroll
-  for (int r = 0; r < 8; ++r) part_s[(r * kParts + part) * D + j] = acc[r];
+    for (int i = 0; i < kShare / 4; ++i) {
+      const float4 v = x[i];
+      acc[0] = fmaf(v.x, p[4 * i], acc[0]), acc[1] = fmaf(v.y, p[4 * i + 1], acc[1]);
+      acc[2] = fmaf(v.z, p[4 * i + 2], acc[2]), acc[3] = fmaf(v.w, p[4 * i + 3], acc[3]);
+    }
+    part_s[(r * kParts + part) * D + j] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+  }
   __syncthreads();
-#pragma unroll
-  for (int e = tid; e < 8 * D; e += kDcThreads) {
+  for (int e = tid; e < nr * D; e += kDcThreads) {
     float s = 0.f;
 #pragma unroll
     for (int q = 0; q < kParts; ++q) s += part_s[(e / D * kParts + q) * D + e % D];
@@ -242,6 +245,8 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
   const uint32_t ring = base + ring_off;
   constexpr int KB = L::kRowK / 4, VB = L::kRowV / 8;      // bytes of a row that a lane reads
   constexpr int KW = (KB + 3) / 4, VW = (VB + 3) / 4;
+  // Two chunks are scored and weighted together (their products and table reads interleave) where the ring has room.
+  constexpr int CN = L::kStages >= 4 && !SG ? 2 : 1;   // (with signs the registers do not do: 36 -> 40 us)
   constexpr int KS = D / 16;                               // inner steps of the score product, and row tiles of the value one
   const int tk = (g >> 1) + 4 * (g & 1);                   // the token of score row g (row g + 8: 8 later)
   bool tables_made = false;
@@ -326,7 +331,7 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
       asm volatile("cp.async.commit_group;\n" ::: "memory");
     };
     page = page_of(0);
-    for (int i = 0; i < L::kStages - 1; ++i) fetch(i);
+    for (int i = 0; i < L::kStages - CN; ++i) fetch(i);
     // ---- rotated queries, while the first copies are under way
     constexpr int DK = D + (SG ? D : 0);
     const float* src;
@@ -354,12 +359,12 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
       for (int c = 0; c < D / 32; ++c) zf[warp * D + lane + 32 * c] = z[c];
       __syncthreads();
       const float f1 = a.scale * 1.44269504089f;
-      rows_at_once<D>(zf, a.k.PiT, part_s, o);
+      rows_at_once<D>(zf, rows, a.k.PiT, part_s, o);
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) qq[warp * DK + lane + 32 * c] = blind ? kBlind : o[warp * D + lane + 32 * c] * f1;
       if (SG) {
         __syncthreads();
-        rows_at_once<D>(zf, a.k.ST, part_s, o);
+        rows_at_once<D>(zf, rows, a.k.ST, part_s, o);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) qq[warp * DK + D + lane + 32 * c] = blind ? kBlind : o[warp * D + lane + 32 * c] * (f1 * kQjlScale / (float)D);
       }
@@ -451,84 +456,98 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
     float vdn = 0.f;      // 2^-ve; 0: no value yet
 
     uint32_t use = 0;         // the offset of the stage in use
-    for (int i = 0; i < mine; ++i, use = use + L::kStage == L::kWarpRing ? 0 : use + L::kStage) {
-      __syncwarp();   // the stage that is filled next has been read by every lane
-      fetch(i + L::kStages - 1);
-      asm volatile("cp.async.wait_group %0;\n" ::"n"(L::kStages - 1) : "memory");
-      __syncwarp();
-      if (!(there >> (i & 31) & 1)) continue;
-      const uint32_t st = ring + use;
-      const int key0 = (ch0 + i * kDcWarps) * kChunk;
-      auto norm_at = [&](uint32_t off, int r) -> float {
-        if (NF16) return lds_half(st + off + 2 * r);
-        return __uint_as_float(lds32(st + off + 4 * r));
-      };
-      // ---- scores of tokens tk, tk + 8 (rows g, g + 8) for query rows 2 t, 2 t + 1
-      float s1[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
-      {
-        uint32_t w0[KW], w1[KW];
-        lds_bytes<KB>(st + spot<L::kRowK>(tk, KB * t), w0);
-        lds_bytes<KB>(st + spot<L::kRowK>(tk + 8, KB * t), w1);
+    auto next = [](uint32_t at) -> uint32_t { return at + L::kStage == L::kWarpRing ? 0 : at + L::kStage; };
+    for (int i = 0; i < mine; i += CN) {
+      __syncwarp();   // the stages that are filled next have been read by every lane
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          uint32_t a0, a1, a2, a3;
-          if (BK == 4) {
-            a0 = lut_byte<4>(w0[s >> 1], 2 * (s & 1), k4, k8).x, a2 = lut_byte<4>(w0[s >> 1], 2 * (s & 1) + 1, k4, k8).x;
-            a1 = lut_byte<4>(w1[s >> 1], 2 * (s & 1), k4, k8).x, a3 = lut_byte<4>(w1[s >> 1], 2 * (s & 1) + 1, k4, k8).x;
-          } else {
-            const uint2 x = lut_byte<2>(w0[s >> 2], s & 3, k4, k8), y = lut_byte<2>(w1[s >> 2], s & 3, k4, k8);
-            a0 = x.x, a2 = x.y, a1 = y.x, a3 = y.y;
-          }
-          mma16816(s1, a0, a1, a2, a3, qc[2 * s], qc[2 * s + 1]);
-        }
-        if (SG) {
-          uint32_t x, y;
-          if (D == 128) {
-            lds_bytes<4>(st + L::kSignK + tk * L::kRowS + 4 * t, &x);
-            lds_bytes<4>(st + L::kSignK + (tk + 8) * L::kRowS + 4 * t, &y);
-          } else {   // 16 signs: the upper eight to bits 16 .. 23
-            lds_bytes<2>(st + L::kSignK + tk * L::kRowS + 2 * t, &x);
-            lds_bytes<2>(st + L::kSignK + (tk + 8) * L::kRowS + 2 * t, &y);
-            x = __byte_perm(x, 0, 0x4140), y = __byte_perm(y, 0, 0x4140);
-          }
-          x = ~x, y = ~y;
+      for (int c = 0; c < CN; ++c) fetch(i + L::kStages - CN + c);
+      asm volatile("cp.async.wait_group %0;\n" ::"n"(L::kStages - CN) : "memory");
+      __syncwarp();
+      uint32_t stage[CN];
+#pragma unroll
+      for (int c = 0; c < CN; ++c) stage[c] = ring + use, use = next(use);
+      float xs[CN][4], vn[CN][2], wn[CN][2];   // scores, then weights; value norms; their signs' norms
+#pragma unroll
+      for (int c = 0; c < CN; ++c) {
+        const uint32_t st = stage[c];
+        const bool here = i + c < mine && (there >> ((i + c) & 31) & 1);
+        const int key0 = (ch0 + (i + c) * kDcWarps) * kChunk;
+        auto norm_at = [&](uint32_t off, int r) -> float {
+          if (NF16) return lds_half(st + off + 2 * r);
+          return __uint_as_float(lds32(st + off + 4 * r));
+        };
+        // ---- scores of tokens tk, tk + 8 (rows g, g + 8) for query rows 2 t, 2 t + 1
+        float s1[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
+        {
+          uint32_t w0[KW], w1[KW];
+          lds_bytes<KB>(st + spot<L::kRowK>(tk, KB * t), w0);
+          lds_bytes<KB>(st + spot<L::kRowK>(tk + 8, KB * t), w1);
 #pragma unroll
           for (int s = 0; s < KS; ++s) {
-            auto two = [](uint32_t w, int k) { return ((w << (15 - k)) & 0x80008000u) ^ 0x3C003C00u; };
-            mma16816(s2, two(x, 2 * s), two(y, 2 * s), two(x, 2 * s + 1), two(y, 2 * s + 1), qs[2 * s], qs[2 * s + 1]);
+            uint32_t a0, a1, a2, a3;
+            if (BK == 4) {
+              a0 = lut_byte<4>(w0[s >> 1], 2 * (s & 1), k4, k8).x, a2 = lut_byte<4>(w0[s >> 1], 2 * (s & 1) + 1, k4, k8).x;
+              a1 = lut_byte<4>(w1[s >> 1], 2 * (s & 1), k4, k8).x, a3 = lut_byte<4>(w1[s >> 1], 2 * (s & 1) + 1, k4, k8).x;
+            } else {
+              const uint2 x = lut_byte<2>(w0[s >> 2], s & 3, k4, k8), y = lut_byte<2>(w1[s >> 2], s & 3, k4, k8);
+              a0 = x.x, a2 = x.y, a1 = y.x, a3 = y.y;
+            }
+            mma16816(s1, a0, a1, a2, a3, qc[2 * s], qc[2 * s + 1]);
+          }
+          if (SG) {
+            uint32_t x, y;
+            if (D == 128) {
+              lds_bytes<4>(st + L::kSignK + tk * L::kRowS + 4 * t, &x);
+              lds_bytes<4>(st + L::kSignK + (tk + 8) * L::kRowS + 4 * t, &y);
+            } else {   // 16 signs: the upper eight to bits 16 .. 23
+              lds_bytes<2>(st + L::kSignK + tk * L::kRowS + 2 * t, &x);
+              lds_bytes<2>(st + L::kSignK + (tk + 8) * L::kRowS + 2 * t, &y);
+              x = __byte_perm(x, 0, 0x4140), y = __byte_perm(y, 0, 0x4140);
+            }
+            x = ~x, y = ~y;
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+              auto two = [](uint32_t w, int k) { return ((w << (15 - k)) & 0x80008000u) ^ 0x3C003C00u; };
+              mma16816(s2, two(x, 2 * s), two(y, 2 * s), two(x, 2 * s + 1), two(y, 2 * s + 1), qs[2 * s], qs[2 * s + 1]);
+            }
           }
         }
-      }
-      const float nA = norm_at(L::kNormK, tk), nB = norm_at(L::kNormK, tk + 8);
-      float rA = 0.f, rB = 0.f;
-      if (SG) rA = lds_half(st + L::kNormK + 64 + 2 * tk), rB = lds_half(st + L::kNormK + 64 + 2 * (tk + 8));
-      float x[4];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        x[j] = s1[j] * (nA * fc[j]);
-        x[2 + j] = s1[2 + j] * (nB * fc[j]);
-        if (SG) x[j] = fmaf(s2[j], rA * fs[j], x[j]), x[2 + j] = fmaf(s2[2 + j], rB * fs[j], x[2 + j]);
-      }
-      float vA = norm_at(L::kNormV, tk), vB = norm_at(L::kNormV, tk + 8), wA = 0.f, wB = 0.f;
-      if (SG) wA = lds_half(st + L::kNormV + 64 + 2 * tk), wB = lds_half(st + L::kNormV + 64 + 2 * (tk + 8));
-      if (key0 < lo_w || key0 + kChunk > hi_w) {   // some row does not see all of the chunk
-        const int kA = key0 + tk, kB = kA + 8;
+        const float nA = norm_at(L::kNormK, tk), nB = norm_at(L::kNormK, tk + 8);
+        float rA = 0.f, rB = 0.f;
+        if (SG) rA = lds_half(st + L::kNormK + 64 + 2 * tk), rB = lds_half(st + L::kNormK + 64 + 2 * (tk + 8));
+        float (&x)[4] = xs[c];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          if (!(kA >= lo[j] && kA < hi[j])) x[j] = -INFINITY;
-          if (!(kB >= lo[j] && kB < hi[j])) x[2 + j] = -INFINITY;
+          x[j] = s1[j] * (nA * fc[j]);
+          x[2 + j] = s1[2 + j] * (nB * fc[j]);
+          if (SG) x[j] = fmaf(s2[j], rA * fs[j], x[j]), x[2 + j] = fmaf(s2[2 + j], rB * fs[j], x[2 + j]);
         }
-        // a token behind the sequence's end counts for nothing, whatever its slot holds
-        if (kA >= hi_all) vA = wA = 0.f;
-        if (kB >= hi_all) vB = wB = 0.f;
+        float vA = norm_at(L::kNormV, tk), vB = norm_at(L::kNormV, tk + 8), wA = 0.f, wB = 0.f;
+        if (SG) wA = lds_half(st + L::kNormV + 64 + 2 * tk), wB = lds_half(st + L::kNormV + 64 + 2 * (tk + 8));
+        if (!here || key0 < lo_w || key0 + kChunk > hi_w) {   // some row does not see all of the chunk
+          const int kA = key0 + tk, kB = kA + 8;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if (!(here && kA >= lo[j] && kA < hi[j])) x[j] = -INFINITY;
+            if (!(here && kB >= lo[j] && kB < hi[j])) x[2 + j] = -INFINITY;
+          }
+          // a token behind the sequence's end counts for nothing, whatever its slot holds
+          if (!here || kA >= hi_all) vA = wA = 0.f;
+          if (!here || kB >= hi_all) vB = wB = 0.f;
+        }
+        vn[c][0] = vA, vn[c][1] = vB, wn[c][0] = wA, wn[c][1] = wB;
       }
-      const float vt = fmaxf(vA, vB);
-      const bool up0 = fmaxf(x[0], x[2]) > m[0] + 8.f || fmaxf(x[1], x[3]) > m[1] + 8.f || vt * vdn > 16.f || vdn == 0.f;
+      float vt = fmaxf(vn[0][0], vn[0][1]), tops[2] = {fmaxf(xs[0][0], xs[0][2]), fmaxf(xs[0][1], xs[0][3])};
+      if (CN == 2) {
+        vt = fmaxf(vt, fmaxf(vn[CN - 1][0], vn[CN - 1][1]));
+        tops[0] = fmaxf(tops[0], fmaxf(xs[CN - 1][0], xs[CN - 1][2])), tops[1] = fmaxf(tops[1], fmaxf(xs[CN - 1][1], xs[CN - 1][3]));
+      }
+      const bool up0 = tops[0] > m[0] + 8.f || tops[1] > m[1] + 8.f || vt * vdn > 16.f || vdn == 0.f;
       if (__any_sync(0xffffffffu, up0)) {   // rarely: a reference moves
         float f[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float top = fmaxf(x[j], x[2 + j]);
+          float top = tops[j];
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
@@ -554,66 +573,71 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
           if (SG) os[y][0] *= f[0], os[y][1] *= f[1], os[y][2] *= f[0], os[y][3] *= f[1];
         }
       }
+      const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float ref = m[j] == -INFINITY ? 0.f : m[j];
-        x[j] = ex2(x[j] - ref), x[2 + j] = ex2(x[2 + j] - ref);
-        l[j] += x[j] + x[2 + j];
-      }
-      vA *= vdn, vB *= vdn;
-      const uint32_t b0 = movmatrix(half2_bits(x[0] * vA, x[1] * vA)), b1 = movmatrix(half2_bits(x[2] * vB, x[3] * vB));
-      // ---- values: lane (g, t) holds coordinates g D/8 .. of tokens t, t + 4, t + 8, t + 12
-      {
-        uint32_t w[4][VW];
+      for (int c = 0; c < CN; ++c) {
+        float (&x)[4] = xs[c];
+        const uint32_t st = stage[c];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) lds_bytes<VB>(st + L::kEndK + spot<L::kRowV>(t + 4 * j, VB * g), w[j]);
-        if (BV == 4) {
-          // The low nibbles of two tokens' bytes side by side, then the high ones: one table entry is the same coordinate
-          // of both tokens (byte y: coordinate 2 y -> row g of tile y, 2 y + 1 -> row g + 8).
-          uint32_t p[2][VW], q[2][VW];
-#pragma unroll
-          for (int x = 0; x < VW; ++x)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint32_t wa = w[2 * j][x], wb = w[2 * j + 1][x];
-              p[j][x] = (wa & 0x0f0f0f0fu) | ((wb << 4) & 0xf0f0f0f0u);
-              q[j][x] = ((wa >> 4) & 0x0f0f0f0fu) | (wb & 0xf0f0f0f0u);
-            }
-#pragma unroll
-          for (int y = 0; y < KS; ++y)
-            mma16816(oc[y], lut_byte<4>(p[0][y >> 2], y & 3, v4, v8).x, lut_byte<4>(q[0][y >> 2], y & 3, v4, v8).x,
-                     lut_byte<4>(p[1][y >> 2], y & 3, v4, v8).x, lut_byte<4>(q[1][y >> 2], y & 3, v4, v8).x, b0, b1);
-        } else {
-#pragma unroll
-          for (int y = 0; y < KS / 2; ++y) {   // byte y: coordinates 4 y .. 4 y + 3 -> tiles 2 y, 2 y + 1
-            uint2 v[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = lut_byte<2>(w[j][y >> 2], y & 3, v4, v8);
-            mma16816(oc[2 * y], __byte_perm(v[0].x, v[1].x, 0x5410), __byte_perm(v[0].x, v[1].x, 0x7632),
-                     __byte_perm(v[2].x, v[3].x, 0x5410), __byte_perm(v[2].x, v[3].x, 0x7632), b0, b1);
-            mma16816(oc[2 * y + 1], __byte_perm(v[0].y, v[1].y, 0x5410), __byte_perm(v[0].y, v[1].y, 0x7632),
-                     __byte_perm(v[2].y, v[3].y, 0x5410), __byte_perm(v[2].y, v[3].y, 0x7632), b0, b1);
-          }
+        for (int j = 0; j < 2; ++j) {
+          x[j] = ex2(x[j] - ref[j]), x[2 + j] = ex2(x[2 + j] - ref[j]);
+          l[j] += x[j] + x[2 + j];
         }
-        if (SG) {   // lane (g, t): signs of projections g D/8 .. of its four tokens; two tokens in one word
-          wA *= vdn, wB *= vdn;
-          const uint32_t r0 = movmatrix(half2_bits(x[0] * wA, x[1] * wA)), r1 = movmatrix(half2_bits(x[2] * wB, x[3] * wB));
-          uint32_t sg[4];
+        const float vA = vn[c][0] * vdn, vB = vn[c][1] * vdn;
+        const uint32_t b0 = movmatrix(half2_bits(x[0] * vA, x[1] * vA)), b1 = movmatrix(half2_bits(x[2] * vB, x[3] * vB));
+        // ---- values: lane (g, t) holds coordinates g D/8 .. of tokens t, t + 4, t + 8, t + 12
+        {
+          uint32_t w[4][VW];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (D == 128) {
-              lds_bytes<2>(st + L::kSignV + (t + 4 * j) * L::kRowS + 2 * g, &sg[j]);
-            } else {
-              uint32_t v;
-              asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(v) : "r"(st + L::kSignV + (t + 4 * j) * L::kRowS + g));
-              sg[j] = v;
+          for (int j = 0; j < 4; ++j) lds_bytes<VB>(st + L::kEndK + spot<L::kRowV>(t + 4 * j, VB * g), w[j]);
+          if (BV == 4) {
+            // The low nibbles of two tokens' bytes side by side, then the high ones: one table entry is the same coordinate
+            // of both tokens (byte y: coordinate 2 y -> row g of tile y, 2 y + 1 -> row g + 8).
+            uint32_t p[2][VW], q[2][VW];
+#pragma unroll
+            for (int x = 0; x < VW; ++x)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const uint32_t wa = w[2 * j][x], wb = w[2 * j + 1][x];
+                p[j][x] = (wa & 0x0f0f0f0fu) | ((wb << 4) & 0xf0f0f0f0u);
+                q[j][x] = ((wa >> 4) & 0x0f0f0f0fu) | (wb & 0xf0f0f0f0u);
+              }
+#pragma unroll
+            for (int y = 0; y < KS; ++y)
+              mma16816(oc[y], lut_byte<4>(p[0][y >> 2], y & 3, v4, v8).x, lut_byte<4>(q[0][y >> 2], y & 3, v4, v8).x,
+                       lut_byte<4>(p[1][y >> 2], y & 3, v4, v8).x, lut_byte<4>(q[1][y >> 2], y & 3, v4, v8).x, b0, b1);
+          } else {
+#pragma unroll
+            for (int y = 0; y < KS / 2; ++y) {   // byte y: coordinates 4 y .. 4 y + 3 -> tiles 2 y, 2 y + 1
+              uint2 v[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) v[j] = lut_byte<2>(w[j][y >> 2], y & 3, v4, v8);
+              mma16816(oc[2 * y], __byte_perm(v[0].x, v[1].x, 0x5410), __byte_perm(v[0].x, v[1].x, 0x7632),
+                       __byte_perm(v[2].x, v[3].x, 0x5410), __byte_perm(v[2].x, v[3].x, 0x7632), b0, b1);
+              mma16816(oc[2 * y + 1], __byte_perm(v[0].y, v[1].y, 0x5410), __byte_perm(v[0].y, v[1].y, 0x7632),
+                       __byte_perm(v[2].y, v[3].y, 0x5410), __byte_perm(v[2].y, v[3].y, 0x7632), b0, b1);
             }
           }
-          const uint32_t p = ~__byte_perm(sg[0], sg[1], 0x5410), q = ~__byte_perm(sg[2], sg[3], 0x5410);
+          if (SG) {   // lane (g, t): signs of projections g D/8 .. of its four tokens; two tokens in one word
+            const float wA = wn[c][0] * vdn, wB = wn[c][1] * vdn;
+            const uint32_t r0 = movmatrix(half2_bits(x[0] * wA, x[1] * wA)), r1 = movmatrix(half2_bits(x[2] * wB, x[3] * wB));
+            uint32_t sg[4];
 #pragma unroll
-          for (int y = 0; y < KS; ++y) {
-            auto two = [](uint32_t w2, int k) { return ((w2 << (15 - k)) & 0x80008000u) ^ 0x3C003C00u; };
-            mma16816(os[y], two(p, 2 * y), two(p, 2 * y + 1), two(q, 2 * y), two(q, 2 * y + 1), r0, r1);
+            for (int j = 0; j < 4; ++j) {
+              if (D == 128) {
+                lds_bytes<2>(st + L::kSignV + (t + 4 * j) * L::kRowS + 2 * g, &sg[j]);
+              } else {
+                uint32_t v;
+                asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(v) : "r"(st + L::kSignV + (t + 4 * j) * L::kRowS + g));
+                sg[j] = v;
+              }
+            }
+            const uint32_t p = ~__byte_perm(sg[0], sg[1], 0x5410), q = ~__byte_perm(sg[2], sg[3], 0x5410);
+#pragma unroll
+            for (int y = 0; y < KS; ++y) {
+              auto two = [](uint32_t w2, int k) { return ((w2 << (15 - k)) & 0x80008000u) ^ 0x3C003C00u; };
+              mma16816(os[y], two(p, 2 * y), two(p, 2 * y + 1), two(q, 2 * y), two(q, 2 * y + 1), r0, r1);
+            }
           }
         }
       }
@@ -691,13 +715,13 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
       acc[j < D ? r * D + j : 8 * D + r * D + j - D] = sum[k] * inv_l;
     }
     __syncthreads();
-    rows_at_once<D>(acc, a.v.Pi, part_s, o1);
+    rows_at_once<D>(acc, rows, a.v.Pi, part_s, o1);
     float y[D / 32];
 #pragma unroll
     for (int k = 0; k < D / 32; ++k) y[k] = o1[tid + 256 * k];
     if (SG) {
       __syncthreads();
-      rows_at_once<D>(acc + 8 * D, a.v.S, part_s, o1);
+      rows_at_once<D>(acc + 8 * D, rows, a.v.S, part_s, o1);
 #pragma unroll
       for (int k = 0; k < D / 32; ++k) y[k] = fmaf(kQjlScale / (float)D, o1[tid + 256 * k], y[k]);
     }

@@ -368,6 +368,105 @@ def test_attention_rotation_out_of_range(tq, news, dtype):
         assert (got[1] == 0).all() and torch.equal(got[keep.cuda()], want[keep.cuda()])
 
 
+@pytest.mark.parametrize("kf,vf,kn,vn", [("mse4", "mse4", "f32", "f32"), ("prod3", "prod3", "f32", "f32"), ("mse4", "mse2", "f32", "f16"),
+                                         ("prod3", "prod3", "f16", "f32"), ("mse2", "mse2", "f32", "f32")])
+def test_attention_norm_types(tq, kf, vf, kn, vn):
+    """fp32 norms, and keys' and values' norms of different types."""
+    fk, fv = fmt(tq, 128, kf, 0, kn), fmt(tq, 128, vf, 1, vn)
+    for news, lens in (([1, 2, 1], [300, 77, 1700]), ([130, 1], [400, 900])):
+        bt = pu.make_batch(tq, news, lens, 48)
+        kc, vc = pu.garbage_cache(tq, fk, bt, 2, 1), pu.garbage_cache(tq, fv, bt, 2, 2)
+        kr = pu.fill_cache(kc, fk, bt, [heads(1 + b, L, 2, 128) for b, L in enumerate(lens)])
+        vr = pu.fill_cache(vc, fv, bt, [heads(9 + b, L, 2, 128) for b, L in enumerate(lens)])
+        q = heads(8, bt.ntok, 8, 128, torch.bfloat16, outliers=False)
+        check_case(tq, (fk, fv, bt, kc, vc, kr, vr, q, None), 0.09, True, 0, H_F16)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("scale", [-0.08, 0.0])
+def test_attention_scale(tq, scale, dtype):
+    """A negative scale turns the order of the scores round, a scale of zero averages."""
+    c = attention_case(tq, 128, "mse4", "mse4", 2, 4, [1, 70], [200, 150], 16, dtype)
+    check_case(tq, c, scale, True, 0, H_FP32 if dtype == "fp32" else H_F16)
+
+
+@pytest.mark.parametrize("G", [3, 16, 40])
+def test_attention_group_sizes(tq, G):
+    for news, lens in (([1, 1], [77, 300]), ([50, 1], [60, 300])):
+        c = attention_case(tq, 128, "mse4", "mse4", 1, G, news, lens, 16, "bf16", "half")
+        check_case(tq, c, 0.09, True, 0, H_F16)
+
+
+@pytest.mark.parametrize("B", [300, 2100])
+def test_attention_many_sequences(tq, B):
+    """More sequences than CTAs, than threads, than the single-token kernel takes."""
+    lens = [1 + (7 * b) % 40 for b in range(B)]
+    news = [1 + (b % 3 == 0) * min(1, lens[b] - 1) for b in range(B)]
+    c = attention_case(tq, 64, "mse4", "mse4", 2, 2, news, lens, 16, "fp16")
+    check_case(tq, c, 0.12, True, 0, H_F16)
+
+
+def test_attention_wide_tables(tq):
+    """A table far wider than the sequences: the f16 rows of all heads would not fit their space, the heads go in rounds."""
+    c = attention_case(tq, 128, "prod3", "prod3", 10, 4, [40, 1], [300, 100], 1024, "bf16", "half", max_pages=300)
+    fk, bt, kc = c[0], c[2], c[3]
+    size = tq.tq_attn_paged_workspace_bytes(fk.handle.ptr, c[1].handle.ptr, bt.struct, 40, 10, kc.struct)
+    assert size < 1.5 * 2 ** 30
+    check_case(tq, c, 0.09, True, 0, H_F16)
+
+
+def test_simt_switch_agrees(tq, monkeypatch):
+    """TQ_SIMT=1 sends every call to the general kernels: the same codes and, to f16's roundings, the same attention."""
+    c = attention_case(tq, 128, "prod3", "mse4", 2, 4, [140, 1], [400, 900], 32, "bf16", "norm+half")
+    fk, fv, bt, kc, vc, kr, vr, q, pr = c
+    fast = tq.attn_paged(fk.handle, fv.handle, q, kc, vc, bt, 0.09, prep=pr)
+    k, v = heads(2, 600, 4, 128, torch.bfloat16), heads(3, 600, 4, 128, torch.bfloat16)
+    ab = pu.make_batch(tq, [600], [600], 32)
+    a = run_append(tq, fk, fv, ab, k, v, pr, 4)
+    monkeypatch.setenv("TQ_SIMT", "1")
+    check_case(tq, c, 0.09, True, 0, H_FP32)
+    slow = tq.attn_paged(fk.handle, fv.handle, q, kc, vc, bt, 0.09, prep=pr)
+    assert not torch.equal(fast, slow)
+    b = run_append(tq, fk, fv, ab, k, v, pr, 4)
+    check_cache(a[0], b[0]), check_cache(a[1], b[1])
+
+
+def test_two_streams_at_once(tq):
+    """Two batches on two streams, each with its own workspace, appended and attended to at the same time."""
+    jobs = []
+    for i in range(2):
+        c = attention_case(tq, 128, "mse4", "mse4", 2, 4, [200, 1, 1], [500, 300, 40], 16, "bf16", "half", seed=i)
+        fk, fv, bt, kc, vc, kr, vr, q, pr = c
+        size = tq.tq_attn_paged_workspace_bytes(fk.handle.ptr, fv.handle.ptr, bt.struct, 8, 2, kc.struct)
+        jobs.append((c, torch.empty(size, dtype=torch.uint8, device="cuda"), torch.cuda.Stream(), torch.zeros_like(q),
+                     tq.attn_paged(fk.handle, fv.handle, q, kc, vc, bt, 0.09, prep=pr)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, ws, s, out, want in jobs:
+            fk, fv, bt, kc, vc, kr, vr, q, pr = c
+            tq.attn_paged(fk.handle, fv.handle, q, kc, vc, bt, 0.09, prep=pr, out=out, workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    for c, ws, s, out, want in jobs:
+        assert torch.equal(out, want)
+
+
+def test_batches_that_are_not_what_they_say(tq):
+    """Bounds that leave the batch's rows, or descend: those sequences are not computed, nothing else is touched."""
+    for dtype in ("fp32", "bf16"):
+        for news in ([1, 1, 1], [40, 1, 30]):
+            c = attention_case(tq, 128, "mse4", "mse4", 2, 4, news, [100, 60, 90], 16, dtype)
+            fk, fv, bt, kc, vc, kr, vr, q, pr = c
+            want = tq.attn_paged(fk.handle, fv.handle, q, kc, vc, bt, 0.09)
+            n0 = news[0]
+            for start in ([0, n0, n0, bt.ntok + 7], [-5, 0, n0 + 1, n0], [0, n0, bt.ntok + 1, 2 ** 31 - 1]):
+                bad = tq.PagedBatch(torch.tensor(start, dtype=torch.int32).cuda(), bt.len, bt.block_table, bt.ntok)
+                out = torch.full_like(q, 3.0)
+                tq.attn_paged(fk.handle, fv.handle, q, kc, vc, bad, 0.09, out=out)
+                assert fk.handle.status() in (tq.TQ_OK, tq.TQ_EINVAL)
+                if start[:2] == [0, n0]:
+                    assert torch.equal(out[:n0], want[:n0]) and (out[n0:] == 3.0).all()
+
+
 def test_append_then_attend_as_a_server_does(tq):
     """Prompts in chunks, then decode steps, some sequences joining late: append and attend each step, both on a side
     stream, against attention over the package's own rows in 64 bits."""
