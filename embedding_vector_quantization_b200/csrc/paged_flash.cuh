@@ -208,51 +208,71 @@ constexpr int kExThreads = 544;
 template <int D>
 struct ExLayout {
   static constexpr uint32_t kOpBytes = 2 * (D / 64) * D * 128;          // Pi^T and S^T, K-major
-  static constexpr uint32_t kAStage = 2 * (D / 64) * kAtomRows;         // operand rows of 128 tokens (codes, signs)
+  // operand rows of 128 tokens: two stages of codes and signs, or four of codes alone
+  static constexpr uint32_t kABytes = 4 * (D / 64) * kAtomRows;
   static constexpr uint32_t kA = kOpBytes;
-  static constexpr uint32_t kLut = kA + 2 * kAStage;                    // 32 KB
-  static constexpr uint32_t kScale = kLut + 32768;                      // float [2][128]
-  static constexpr uint32_t kBars = kScale + 1024;                      // op_full, a_full[2], a_empty[2], d_full[2], d_empty[2]
-  static constexpr uint32_t kMisc = kBars + 9 * 8;                      // tmem slot, abort, maxima[2 groups][2][4]
+  static constexpr uint32_t kLut = kA + kABytes;                        // 32 KB
+  static constexpr uint32_t kScale = kLut + 32768;                      // float [4][128]
+  static constexpr uint32_t kBars = kScale + 2048;                      // op_full, a_full[4], a_empty[4], d_full[4], d_empty[4]
+  static constexpr uint32_t kMisc = kBars + 17 * 8;                     // tmem slot, abort, maxima[2 groups][2][4]
   static constexpr uint32_t kBytes = kMisc + 8 + 64;
 };
 static_assert(ExLayout<128>::kBytes <= 232448, "expand layout exceeds the shared memory of one CTA");
+
+// Loads that stay where they are written: ahead of the work on the row before (left to itself, the compiler puts them off to
+// where they are used, and every tile waits for memory).
+__device__ __forceinline__ uint2 load_ahead64(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t load_ahead32(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.u32 %0, [%1];\n" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint16_t load_ahead16(const void* p) {
+  uint16_t v;
+  asm volatile("ld.global.nc.u16 %0, [%1];\n" : "=h"(v) : "l"(p));
+  return v;
+}
 
 // One token's packed row, loaded ahead.
 template <int D>
 struct Row {
   uint32_t code[D / 8];   // 4 bits: all of them
   uint32_t sign[D / 32];
-  float norm, ratio;      // ratio: what a sign weighs relative to the norm
+  uint32_t norm;          // as loaded (fp16 or fp32): nothing here waits for a load
+  uint16_t rnorm;
   bool ok;
 };
 
 template <int D>
 __device__ __forceinline__ void load_row(const Quant& Q, const CacheView& c, int64_t at, Row<D>& r) {
   r.ok = at >= 0;
-  r.norm = 0.f, r.ratio = 0.f;
+  r.norm = 0, r.rnorm = 0;
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) r.code[i] = 0;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) r.sign[i] = 0;
   if (at < 0) return;
-  r.norm = load_norm(c.norms, Q.norm_dtype, at);
+  if (Q.norm_dtype == TQ_F16) r.norm = load_ahead16(static_cast<const __half*>(c.norms) + at);
+  else r.norm = load_ahead32(static_cast<const float*>(c.norms) + at);
   const uint2* w = reinterpret_cast<const uint2*>(c.codes + at * Q.codes_B);   // rows are multiples of 8 bytes
 #pragma unroll
   for (int i = 0; i < D / 16; ++i)
     if (8 * i < Q.codes_B) {
-      const uint2 v = __ldg(w + i);
+      const uint2 v = load_ahead64(w + i);
       r.code[2 * i] = v.x, r.code[2 * i + 1] = v.y;
     }
   if (Q.m > 0) {
     const uint2* s = reinterpret_cast<const uint2*>(c.signs + at * Q.signs_B);
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
-      const uint2 v = __ldg(s + i);
+      const uint2 v = load_ahead64(s + i);
       r.sign[2 * i] = v.x, r.sign[2 * i + 1] = v.y;
     }
-    r.ratio = 1.f;
-    if (Q.bits > 0) r.ratio = r.norm != 0.f ? __half2float(c.rnorms[at]) / r.norm : 0.f;
+    if (Q.bits > 0) r.rnorm = load_ahead16(c.rnorms + at);
   }
 }
 
@@ -410,9 +430,11 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
   const uint32_t bars = base + L::kBars;
   const uint32_t op_full = bars;
   auto a_full = [&](int s) { return bars + 8u * (1 + s); };
-  auto a_empty = [&](int s) { return bars + 8u * (3 + s); };
-  auto d_full = [&](int s) { return bars + 8u * (5 + s); };
-  auto d_empty = [&](int s) { return bars + 8u * (7 + s); };
+  auto a_empty = [&](int s) { return bars + 8u * (5 + s); };
+  auto d_full = [&](int s) { return bars + 8u * (9 + s); };
+  auto d_empty = [&](int s) { return bars + 8u * (13 + s); };
+  const int NS = Q.m > 0 ? 2 : 4;                                      // stages: tile i uses i mod NS
+  const uint32_t stage_bytes = L::kABytes / NS;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
   float* maxima = reinterpret_cast<float*>(smem + L::kMisc + 8);   // [4]
@@ -425,7 +447,7 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
     *abort_flag = 0;
     uint64_t* b = reinterpret_cast<uint64_t*>(smem + L::kBars);
     bar_init(b, 1);
-    for (int s = 0; s < 2; ++s) bar_init(b + 1 + s, 4), bar_init(b + 3 + s, 1), bar_init(b + 5 + s, 1), bar_init(b + 7 + s, 4);
+    for (int s = 0; s < 4; ++s) bar_init(b + 1 + s, 4), bar_init(b + 5 + s, 1), bar_init(b + 9 + s, 1), bar_init(b + 13 + s, 4);
   }
   build_lut(Q, smem + L::kLut, tid, kExThreads);
   grid_dep_wait();
@@ -435,7 +457,7 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
   const int w0 = (int)(work * j0 / step), mine = (int)(work * (j0 + 1) / step) - w0;
   if (mine == 0) return;
   if (warp == 16) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(base + L::kMisc), "r"(256u) : "memory");
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(base + L::kMisc), "r"(512u) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
   }
   tc_fence_before();
@@ -451,41 +473,61 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
 
   if (warp < 8) {
     // ---- operand rows: thread = token of the tile. Under way at a time: the page of the token after next, the next row.
-    const int g = warp >> 2, s = g, r = tid & 127;
+    const int g = warp >> 2, r = tid & 127;
     float* const top_s = maxima + 8 * g;
     TileCursor c{(int)(w0 / tiles), (int)(w0 % tiles), 0, 0, 0, 0, 0};
-    auto page_of = [&]() -> int64_t {   // row offset of the token's page and slot; -1: bad page, -2: behind the end
-      const int p = c.base + (c.tile - c.first) * kKT + r;
-      if (p >= c.hi) return -2;
-      return place_of(a.bt, c.b, p, a.head0 + c.h, a.Hkv);
+    // The cursor's token: its page as loaded (nothing waits for it yet), and where in the page.
+    struct Spot {
+      int page, slot, h, tile;
+      bool in;
+    };
+    auto spot = [&]() -> Spot {
+      Spot p;
+      const int pos = c.base + (c.tile - c.first) * kKT + r;
+      p.in = pos < c.hi, p.h = c.h, p.tile = c.tile;
+      const uint32_t pi = (uint32_t)pos / (uint32_t)a.bt.page_size;
+      p.slot = pos - (int)pi * a.bt.page_size;
+      p.page = p.in ? (int)load_ahead32(a.bt.table + (int64_t)c.b * a.bt.max_pages + pi) : -1;
+      return p;
+    };
+    auto row_of = [&](const Spot& p) -> int64_t {   // -1: bad page, -2: behind the end
+      if (!p.in) return -2;
+      if (p.page < 0 || p.page >= a.bt.num_pages) return -1;
+      return ((int64_t)p.page * a.Hkv + a.head0 + p.h) * a.bt.page_size + p.slot;
     };
     Row<D> cur, nxt;
-    int64_t at0 = -2, at1 = -2;      // this group's next tile, and the one after
-    int tile0 = 0, h0 = 0, tile1 = 0, h1 = 0;
+    Spot s0{-1, 0, 0, 0, false}, s1 = s0;   // this group's next tile, and the one after
+    int64_t at0 = -2;
     if (g < mine) {
       cursor_seek(a, tiles, c, g);
-      at0 = page_of(), tile0 = c.tile, h0 = c.h;
+      s0 = spot();
+      at0 = row_of(s0);
       load_row<D>(Q, C, at0, nxt);
     }
     if (g + 2 < mine) {
       cursor_seek(a, tiles, c, 2);
-      at1 = page_of(), tile1 = c.tile, h1 = c.h;
+      s1 = spot();
     }
     for (int i = g; i < mine; i += 2) {
+      const int s = i % NS;
       cur = nxt;
       const int64_t here = at0;
-      const int tile = tile0, h = h0;
-      at0 = at1, tile0 = tile1, h0 = h1;
-      if (i + 2 < mine) load_row<D>(Q, C, at0, nxt);
+      const int tile = s0.tile, h = s0.h;
+      s0 = s1;
+      if (i + 2 < mine) {
+        at0 = row_of(s0);
+        load_row<D>(Q, C, at0, nxt);
+      }
       if (i + 4 < mine) {
         cursor_seek(a, tiles, c, 2);
-        at1 = page_of(), tile1 = c.tile, h1 = c.h;
+        s1 = spot();
       }
+      const float norm = Q.norm_dtype == TQ_F16 ? __half2float(__ushort_as_half((uint16_t)cur.norm)) : __uint_as_float(cur.norm);
       if (here == -1) report_error(a.err, kErrPaged);
       const unsigned there = __ballot_sync(0xffffffffu, cur.ok);
       if (kind == 0 && h == 0 && lane == 0) a.p.seen[4 * tile + (warp & 3)] = there;
       // the tile's exponent: 2^E >= every finite norm
-      float top = fabsf(cur.norm) < INFINITY ? fabsf(cur.norm) : 0.f;
+      float top = fabsf(norm) < INFINITY ? fabsf(norm) : 0.f;
       for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       float* const mt = top_s + (i & 2) * 2;   // two sets in turn: one barrier a tile is enough
       if (lane == 0) mt[warp & 3] = top;
@@ -494,10 +536,10 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
       int e = -126;
       if (top > 0.f) frexpf(top, &e);
       e = max(-126, min(126, e));
-      if (i >= 2) wait(a_empty(s), ((i >> 1) - 1) & 1);
-      scale_s[s * 128 + r] = cur.ok ? ldexpf(cur.norm, -e) : 0.f;
+      if (i >= NS) wait(a_empty(s), (i / NS - 1) & 1);
+      scale_s[s * 128 + r] = cur.ok ? ldexpf(norm, -e) : 0.f;
       if (r == 0) (kind ? a.p.ve : a.p.ke)[(int64_t)h * a.p.max_tiles + tile] = e;
-      const uint32_t row = base + L::kA + s * L::kAStage + r * 128;
+      const uint32_t row = base + L::kA + s * stage_bytes + r * 128;
       if (Q.bits > 0) {
 #pragma unroll
         for (int ch = 0; ch < D / 8; ++ch) {
@@ -509,7 +551,8 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
         for (int ch = 0; ch < D / 8; ++ch) sts128(row + (ch >> 3) * kAtomRows + (((ch & 7) ^ (r & 7)) << 4), 0, 0, 0, 0);
       }
       if (Q.m > 0) {
-        const uint32_t r2 = half2_bits(cur.ratio, cur.ratio);
+        const float ratio = Q.bits == 0 ? 1.f : norm != 0.f ? __half2float(__ushort_as_half(cur.rnorm)) / norm : 0.f;   // relative to the norm
+        const uint32_t r2 = half2_bits(ratio, ratio);
 #pragma unroll
         for (int ch = 0; ch < D / 8; ++ch) {
           const uint4 v = sign_chunk<D>(cur, ch, r2);
@@ -522,13 +565,13 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
     }
   } else if (warp < 16) {
     // ---- results: thread = token; the row goes out through the operand stage that produced it
-    const int g = (warp >> 2) & 1, s = g, r = tid & 127;
+    const int g = (warp >> 2) & 1, r = tid & 127;
     for (int i = g; i < mine; i += 2) {
-      const int h = (w0 + i) / tiles, tile = (w0 + i) - h * tiles;
-      wait(d_full(s), (i >> 1) & 1);
+      const int s = i % NS, h = (w0 + i) / tiles, tile = (w0 + i) - h * tiles;
+      wait(d_full(s), (i / NS) & 1);
       tc_fence_after();
       const float f = scale_s[s * 128 + r];
-      const uint32_t row = base + L::kA + s * L::kAStage + r * 128;
+      const uint32_t row = base + L::kA + s * stage_bytes + r * 128;
 #pragma unroll 1
       for (int c4 = 0; c4 < D / 32; ++c4) {
         uint32_t v[32];
@@ -550,7 +593,7 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
       if (r == 0) {
         const uint32_t bytes = (D / 64) * kAtomRows;
         uint8_t* dst = (kind ? a.p.vrows : a.p.krows) + ((int64_t)h * a.p.max_tiles + tile) * bytes;
-        bulk_store(dst, base + L::kA + s * L::kAStage, bytes);
+        bulk_store(dst, base + L::kA + s * stage_bytes, bytes);
         bulk_store_read_wait();
         bar_arrive(a_empty(s));
       }
@@ -568,11 +611,11 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
     wait(op_full, 0);
     const uint64_t a_desc = sw128_desc(base + L::kA), b_desc = sw128_desc(base);
     for (int i = 0; i < mine; ++i) {
-      const int s = i & 1;
-      wait(a_full(s), (i >> 1) & 1);
-      if (i >= 2) wait(d_empty(s), ((i >> 1) - 1) & 1);
+      const int s = i % NS;
+      wait(a_full(s), (i / NS) & 1);
+      if (i >= NS) wait(d_empty(s), (i / NS - 1) & 1);
       tc_fence_after();
-      const uint64_t ad = a_desc + ((s * L::kAStage) >> 4);
+      const uint64_t ad = a_desc + ((s * stage_bytes) >> 4);
       for (int k = 0; k < katoms; ++k)
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
@@ -583,12 +626,12 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
       commit_one(lead, d_full(s));
     }
     // tensor memory is released below: the last contractions must have ended
-    for (int i = max(0, mine - 2); i < mine; ++i) (void)wait_bar(d_full(i & 1), (i >> 1) & 1);
+    for (int i = max(0, mine - NS); i < mine; ++i) (void)wait_bar(d_full(i % NS), (i / NS) & 1);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 16) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(256u) : "memory");
+  if (warp == 16) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512u) : "memory");
 }
 
 // ---------------------------------------------------------------- queries
