@@ -41,8 +41,9 @@ struct TaLayout {
   static constexpr uint32_t kTile = (D / 64) * kAtomRows;         // 128 rows
   static constexpr int kStages = PROD && D == 128 ? 1 : 2;        // z tiles (pairs)
   static constexpr uint32_t kA = kOps;
+  static constexpr uint32_t kRowInfo = 128 * 24;
   static constexpr uint32_t kRow = kA + kStages * 2 * kTile;      // per tile of four: int64 place[128], float2 (N_s, N)[128], int64 rp[128]
-  static constexpr uint32_t kSq = kRow + 4 * 3072;                // float [2 groups][2][128]: halves of |e|^2
+  static constexpr uint32_t kSq = kRow + 4 * kRowInfo;              // float [2 groups][2][128]: halves of |e|^2
   static constexpr uint32_t kBars = kSq + 2048;
   // op_full, a_full[2], a_empty[2], d1_full[2], e_full[2], d2_full[2], d_free[2]
   static constexpr int kNumBars = 13;
@@ -63,6 +64,18 @@ struct AppendTcArgs {
   const uint8_t* ops;
   int* err;
 };
+
+// Whether a barrier's phase has ended, without waiting (the caller counts its polls; as many as a second takes).
+constexpr int kPollLimit = 1 << 23;
+__device__ __forceinline__ bool test_bar(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done;
+}
 
 // Index of |y| among the positive half of a symmetric codebook (H = 2^(BITS - 1) cells, H - 1 positive borders b[1 ..]), the
 // distance to the nearest border met, and the cell's centroid (positive).
@@ -195,9 +208,9 @@ __global__ void __launch_bounds__(kTaThreads, 1) paged_append_tc_kernel(AppendTc
     const int64_t start0 = a.bt.q_start[0], end = a.bt.q_start[a.bt.B];
     for (int i = 0; i < mine; ++i) {
       const int s = i % L::kStages, ri = i & 3;
-      int64_t* place_s = reinterpret_cast<int64_t*>(smem + L::kRow + ri * 3072);
-      float2* norm_s = reinterpret_cast<float2*>(smem + L::kRow + ri * 3072 + 1024);
-      int64_t* rp_s = reinterpret_cast<int64_t*>(smem + L::kRow + ri * 3072 + 2048);   // for the rows that are computed twice
+      int64_t* place_s = reinterpret_cast<int64_t*>(smem + L::kRow + ri * L::kRowInfo);
+      float2* norm_s = reinterpret_cast<float2*>(smem + L::kRow + ri * L::kRowInfo + 1024);
+      int64_t* rp_s = reinterpret_cast<int64_t*>(smem + L::kRow + ri * L::kRowInfo + 2048);   // for the rows that are computed twice
       // places and (16-bit) values of both halves first: one latency for them all
       int64_t at2[2], rp2[2], from2[2];
       uint4 raw[2][C];
@@ -428,8 +441,8 @@ __global__ void __launch_bounds__(kTaThreads, 1) paged_append_tc_kernel(AppendTc
       const int ri = i & 3;
       wait(d1_full(g), (i / 2) & 1);
       tc_fence_after();
-      const int64_t at = reinterpret_cast<const int64_t*>(smem + L::kRow + ri * 3072)[r];
-      const float2 nn = reinterpret_cast<const float2*>(smem + L::kRow + ri * 3072 + 1024)[r];
+      const int64_t at = reinterpret_cast<const int64_t*>(smem + L::kRow + ri * L::kRowInfo)[r];
+      const float2 nn = reinterpret_cast<const float2*>(smem + L::kRow + ri * L::kRowInfo + 1024)[r];
       const int64_t row0 = ((int64_t)blockIdx.x + (int64_t)i * gridDim.x) * 128;
       const float inv = nn.x > 0.f ? 0.00390625f / nn.x : 0.f;   // 2^-8 / |z scaled|
       const bool some = at >= 0 && nn.x > 0.f && nn.x < INFINITY;
@@ -438,7 +451,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) paged_append_tc_kernel(AppendTc
         int64_t t;
         int h;
         split_row(row0 + (ew & 3) * 32 + who, a.Hkv, t, h);
-        const int64_t rp = reinterpret_cast<const int64_t*>(smem + L::kRow + ri * 3072 + 2048)[(ew & 3) * 32 + who];
+        const int64_t rp = reinterpret_cast<const int64_t*>(smem + L::kRow + ri * L::kRowInfo + 2048)[(ew & 3) * 32 + who];
         exact_row<D>(a, t, h, rp, z, n);
       };
       float esq[2] = {0.f, 0.f};
