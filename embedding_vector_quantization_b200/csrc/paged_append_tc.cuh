@@ -77,6 +77,24 @@ __device__ __forceinline__ bool test_bar(uint32_t bar, uint32_t parity) {
   return done;
 }
 
+// The sum of squares of a row that four lanes hold. Eights are summed in fp32 and those in fp64: a norm stored in fp32 is off
+// by half a step for the root, a quarter for this result's rounding and about 0.15 for the eights (one sum of 32 in fp32: a
+// step more).
+template <int C>
+__device__ __forceinline__ float row_squares(const float (&z)[8 * C]) {
+  double ss = 0.0;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    float p = z[8 * c] * z[8 * c];
+#pragma unroll
+    for (int x = 1; x < 8; ++x) p = fmaf(z[8 * c + x], z[8 * c + x], p);
+    ss += (double)p;
+  }
+  ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+  ss += __shfl_xor_sync(0xffffffffu, ss, 2);
+  return (float)ss;
+}
+
 // Index of |y| among the positive half of a symmetric codebook (H = 2^(BITS - 1) cells, H - 1 positive borders b[1 ..]), the
 // distance to the nearest border met, and the cell's centroid (positive).
 template <int BITS>
@@ -266,12 +284,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) paged_append_tc_kernel(AppendTc
         }
         float rms = 1.f;
         if (a.prep.weight) {
-          float ss = 0.f;
-#pragma unroll
-          for (int x = 0; x < 8 * C; ++x) ss = fmaf(z[x], z[x], ss);
-          ss += __shfl_xor_sync(0xffffffffu, ss, 1);
-          ss += __shfl_xor_sync(0xffffffffu, ss, 2);
-          rms = rsqrtf(ss / (float)D + a.prep.eps);
+          rms = 1.f / sqrtf(row_squares<C>(z) / (float)D + a.prep.eps);
 #pragma unroll
           for (int x = 0; x < 8 * C; ++x)
             z[x] *= rms * load_any(a.prep.weight, a.prep.weight_dtype, 8 * (ql + 4 * (x >> 3)) + (x & 7));
@@ -320,11 +333,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) paged_append_tc_kernel(AppendTc
               }
           }
         }
-        float ss = 0.f;
-#pragma unroll
-        for (int x = 0; x < 8 * C; ++x) ss = fmaf(z[x], z[x], ss);
-        ss += __shfl_xor_sync(0xffffffffu, ss, 1);
-        ss += __shfl_xor_sync(0xffffffffu, ss, 2);
+        float ss = row_squares<C>(z);
         float n = sqrtf(ss);
         const bool odd = !(ss >= 1e-30f && ss < 1e37f);
         if (__any_sync(0xffffffffu, odd)) {   // squares out of fp32's range: once more about the largest coordinate
