@@ -53,7 +53,23 @@ struct DecodeArgs {
 
 __device__ __forceinline__ int small_tokens(const AttnArgs& a, int b) {
   const int n = seq_tokens(a.bt, b);
-  return n > 0 && n * a.G <= a.small_rows ? n : 0;
+  return n > 0 && (int64_t)n * a.G <= a.small_rows ? n : 0;
+}
+// The query rows of one KV head come in eights. Each (KV head, eight) is a head of its own to the kernels here, a strip; a
+// sequence has at most most_strips, which the grids and the workspace are made for.
+__device__ __forceinline__ int eights(const AttnArgs& a, int n) { return (n * a.G + 7) >> 3; }
+__device__ __forceinline__ int most_strips(const AttnArgs& a) { return a.Hkv * (a.small_rows >> 3); }
+struct Strip {
+  int h, row0, rows;   // KV head; its first query row (row = token * G + head within the group), their number
+};
+__device__ __forceinline__ Strip strip_of(const AttnArgs& a, int n, int hv) {
+  const int e = eights(a, n), h = hv / e, row0 = 8 * (hv - h * e);
+  return {h, row0, min(8, n * a.G - row0)};
+}
+// Query row `row` of KV head h among the rows of the call's q and out.
+__device__ __forceinline__ int64_t row_of(const AttnArgs& a, int b, int h, int row) {
+  const int i = row / a.G;
+  return ((int64_t)a.bt.q_start[b] + i) * a.Hq + h * a.G + row - i * a.G;
 }
 // Chunks of one head of sequence b, and its first.
 __device__ __forceinline__ int small_chunks(const AttnArgs& a, int b, int n, int& first) {
@@ -65,7 +81,7 @@ __device__ __forceinline__ int small_chunks(const AttnArgs& a, int b, int n, int
   return hi > lo ? (hi + kChunk - 1) / kChunk - first : 0;
 }
 
-// Running sums over the sequences of chunks * Hkv into pre[0 .. B], by the whole CTA of NT threads; returns the most chunks
+// Running sums over the sequences of chunks * strips into pre[0 .. B], by the whole CTA of NT threads; returns the most chunks
 // of one (sequence, head).
 template <int NT>
 __device__ __forceinline__ int chunk_sums(const AttnArgs& a, int64_t* pre, int64_t* warp_s) {
@@ -74,12 +90,13 @@ __device__ __forceinline__ int chunk_sums(const AttnArgs& a, int64_t* pre, int64
   int most = 0;
   for (int b0 = 0; b0 < a.bt.B; b0 += NT) {
     const int b = b0 + tid;
-    int nch = 0;
+    int nch = 0, n = 0;
     if (b < a.bt.B) {
       int first;
-      nch = small_chunks(a, b, small_tokens(a, b), first);
+      n = small_tokens(a, b);
+      nch = small_chunks(a, b, n, first);
     }
-    const int64_t v = (int64_t)nch * a.Hkv;
+    const int64_t v = (int64_t)nch * (a.Hkv * eights(a, n));
     int64_t incl = v;
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
@@ -104,7 +121,7 @@ __device__ __forceinline__ int chunk_sums(const AttnArgs& a, int64_t* pre, int64
 // Otherwise evenly, with at least 8 chunks for a CTA, one for each warp.
 constexpr int kWholeChunks = 96;
 __device__ __forceinline__ bool take_whole(const AttnArgs& a, int most, int ctas) {
-  return most <= kWholeChunks && (int64_t)a.bt.B * a.Hkv <= ctas;
+  return most <= kWholeChunks && (int64_t)a.bt.B * most_strips(a) <= ctas;
 }
 __device__ __forceinline__ int even_parts(int64_t U, int ctas) { return (int)min((int64_t)ctas, max((int64_t)1, U >> 3)); }
 
@@ -223,14 +240,16 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
   const bool whole = ONE || take_whole(a, most, gridDim.x);
   Span sp{0, 0};
   if (whole) {
-    const int b = blockIdx.x / a.Hkv, h = blockIdx.x - b * a.Hkv;
-    const int n = b < a.bt.B ? small_tokens(a, b) : 0;
-    if (n > 0) {
-      const int64_t nch = (pre[b + 1] - pre[b]) / a.Hkv;
-      sp = {pre[b] + h * nch, pre[b] + (h + 1) * nch};
-      if (nch == 0)   // no keys
-        for (int e = tid; e < n * a.G * D; e += kDcThreads)
-          store_any(a.out, a.q_dtype, ((a.bt.q_start[b] + e / (a.G * D)) * (int64_t)a.Hq + h * a.G) * D + e % (a.G * D), 0.f);
+    const int b = blockIdx.x / most_strips(a), hv = blockIdx.x - b * most_strips(a);
+    const int n = b < a.bt.B ? small_tokens(a, b) : 0, strips = a.Hkv * eights(a, n);
+    if (hv < strips) {
+      const int64_t nch = (pre[b + 1] - pre[b]) / strips;
+      sp = {pre[b] + hv * nch, pre[b] + (hv + 1) * nch};
+      if (nch == 0) {   // no keys
+        const Strip l = strip_of(a, n, hv);
+        for (int e = tid; e < l.rows * D; e += kDcThreads)
+          store_any(a.out, a.q_dtype, row_of(a, b, l.h, l.row0 + e / D) * D + e % D, 0.f);
+      }
     }
   } else if ((int)blockIdx.x < even_parts(U, gridDim.x)) {
     sp = span_of(U, blockIdx.x, even_parts(U, gridDim.x));
@@ -256,18 +275,19 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
     const int n = small_tokens(a, b);
     int first;
     const int nch = small_chunks(a, b, n, first);
-    const int h = (int)((u - pre[b]) / nch);
-    const int64_t item_u = pre[b] + (int64_t)h * nch;
+    const int hv = (int)((u - pre[b]) / nch);
+    const int64_t item_u = pre[b] + (int64_t)hv * nch;
     const int c0 = (int)(u - item_u), c1 = (int)(min(sp.u1, item_u + nch) - item_u);
     u = item_u + nch;
-    const int rows = n * a.G, len = a.bt.len[b];
+    const Strip strip = strip_of(a, n, hv);
+    const int h = strip.h, rows = strip.rows, len = a.bt.len[b];
     int lo_all, hi_all;
     key_range(a.bt, b, 0, n - 1, n, a.causal, a.window, lo_all, hi_all);
     // rows 2 t, 2 t + 1 are this lane's columns: the keys they see
     int lo[2], hi[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int r = 2 * t + j, pos = len - n + r / a.G;
+      const int r = 2 * t + j, pos = len - n + (strip.row0 + r) / a.G;
       lo[j] = 0, hi[j] = r < rows ? hi_all : 0;
       if (a.causal) {
         hi[j] = min(hi[j], pos + 1);
@@ -345,14 +365,14 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) z[c] = 0.f;
       if (warp < rows) {
-        const int i = warp / a.G;
+        const int i = (strip.row0 + warp) / a.G;
         const int64_t t0 = a.bt.q_start[b] + i;
         const int64_t p = a.prep.pos ? (int64_t)a.prep.pos[t0] : (int64_t)len - n + i;
         if (a.prep.cos_sin && (p < 0 || p >= a.prep.max_pos)) {
           if (lane == 0 && (a.prep.pos || p >= 0)) report_error(a.err, kErrPaged);
           blind = true;   // it sees nothing
         } else {
-          prep_head<float, D / 32>(a.q, a.q_dtype, t0 * a.q_stride + (int64_t)(h * a.G + warp - i * a.G) * D, D, a.prep, p, z);
+          prep_head<float, D / 32>(a.q, a.q_dtype, t0 * a.q_stride + (int64_t)(h * a.G + strip.row0 + warp - i * a.G) * D, D, a.prep, p, z);
         }
       }
 #pragma unroll
@@ -376,7 +396,7 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
         if (BK != BV) build_lut(a.v, tables + 32768, tid, kDcThreads);
       }
       grid_dep_wait();
-      src = a.qr + (((int64_t)b * a.Hkv + h) * 8 + g) * DK;
+      src = a.qr + (((int64_t)b * most_strips(a) + hv) * 8 + g) * DK;
     }
     // ---- queries: row g, this lane's coordinates, as f16 times a power of two
     uint32_t qc[2 * KS], qs[SG ? 2 * KS : 1];
@@ -695,7 +715,7 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
       lt += mw == -INFINITY ? 0.f : stat[64 + w * 8 + (tid & 7)] * ex2(mw - mt);
     }
     if (!whole) {
-      float* part = a.part + ((int64_t)blockIdx.x + (int64_t)b * a.Hkv + h) * 8 * (L::kDV + 2);
+      float* part = a.part + ((int64_t)blockIdx.x + (int64_t)b * most_strips(a) + hv) * 8 * (L::kDV + 2);
 #pragma unroll
       for (int k = 0; k < L::kDV / 32; ++k) part[tid + 256 * k] = sum[k];
       if (tid < 8) part[8 * L::kDV + tid] = mt, part[8 * L::kDV + 8 + tid] = lt;
@@ -728,7 +748,7 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
 #pragma unroll
     for (int k = 0; k < D / 32; ++k) {
       const int e = tid + 256 * k, r = e / D, x = e % D;
-      if (r < rows) store_any(a.out, a.q_dtype, ((a.bt.q_start[b] + r / a.G) * (int64_t)a.Hq + h * a.G + r % a.G) * D + x, y[k]);
+      if (r < rows) store_any(a.out, a.q_dtype, row_of(a, b, h, strip.row0 + r) * D + x, y[k]);
     }
   }
 }
@@ -759,27 +779,28 @@ __device__ __forceinline__ void rows_slice(const float* in, int ni, const float*
   __syncthreads();
 }
 
-// Queries of the small sequences, to qr [B][Hkv][8][d + m]. Grid: (B * Hkv, (d + m) / 32 column slices); 256 threads: warp r
-// prepares query row r of the (sequence, head).
+// Queries of the small sequences, to qr [B][most strips][8][d + m]. Grid: (B * most strips, (d + m) / 32 column slices); 256
+// threads: warp r prepares query row r of the strip.
 __global__ void __launch_bounds__(256) paged_qslice_kernel(DecodeArgs da) {
   __shared__ float zf[8 * 128], part_s[8 * 256], ys[256];
   const AttnArgs& a = da.a;
   const int d = a.k.d, m = a.k.m, dk = d + m, tid = threadIdx.x, lane = tid & 31, r = tid >> 5;
   grid_dep_launch();
-  const int b = blockIdx.x / a.Hkv, h = blockIdx.x - b * a.Hkv;
+  const int b = blockIdx.x / most_strips(a), hv = blockIdx.x - b * most_strips(a);
   const int n = small_tokens(a, b);
-  if (n == 0) return;
+  if (hv >= a.Hkv * eights(a, n)) return;
+  const Strip l = strip_of(a, n, hv);
   float z[4] = {0.f, 0.f, 0.f, 0.f};
   bool blind = false;
-  if (r < n * a.G) {
-    const int i = r / a.G;
+  if (r < l.rows) {
+    const int i = (l.row0 + r) / a.G;
     const int64_t t = a.bt.q_start[b] + i;
     const int64_t p = a.prep.pos ? (int64_t)a.prep.pos[t] : (int64_t)a.bt.len[b] - n + i;
     if (a.prep.cos_sin && (p < 0 || p >= a.prep.max_pos)) {
       if (lane == 0 && (a.prep.pos || p >= 0)) report_error(a.err, kErrPaged);
       blind = true;   // it sees nothing
     } else {
-      prep_head<float, 4>(a.q, a.q_dtype, t * a.q_stride + (int64_t)(h * a.G + r - i * a.G) * d, d, a.prep, p, z);
+      prep_head<float, 4>(a.q, a.q_dtype, t * a.q_stride + (int64_t)(l.h * a.G + l.row0 + r - i * a.G) * d, d, a.prep, p, z);
     }
   }
 #pragma unroll
@@ -793,12 +814,12 @@ __global__ void __launch_bounds__(256) paged_qslice_kernel(DecodeArgs da) {
   a.qr[((int64_t)blockIdx.x * 8 + r) * dk + col + lane] = blind ? kBlind : ys[tid] * f;
 }
 
-// Grid: (B, Hkv, d / 32): 32 coordinates of the rows of one (sequence, head): its CTAs' parts merged in order, then
+// Grid: (B, most strips, d / 32): 32 coordinates of the rows of one (sequence, strip): its CTAs' parts merged in order, then
 // o = (Pi_V^T acc + c S_V^T acc_s) / sum.
 __global__ void __launch_bounds__(256) paged_decode_merge_kernel(DecodeArgs da) {
   extern __shared__ __align__(16) unsigned char smem[];
   const AttnArgs& a = da.a;
-  const int d = a.v.d, m = a.v.m, dv = d + m, b = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int d = a.v.d, m = a.v.m, dv = d + m, b = blockIdx.x, hv = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_dep_launch();
   float* acc = reinterpret_cast<float*>(smem);        // [8][d], then [8][m]
   float* part_s = acc + 8 * dv;                       // [8][256]
@@ -810,7 +831,7 @@ __global__ void __launch_bounds__(256) paged_decode_merge_kernel(DecodeArgs da) 
   __shared__ float f[8];
   __shared__ int parts, tops[8];
   const int n = small_tokens(a, b);
-  if (n == 0) {
+  if (hv >= a.Hkv * eights(a, n)) {
     grid_dep_wait();
     return;
   }
@@ -821,8 +842,8 @@ __global__ void __launch_bounds__(256) paged_decode_merge_kernel(DecodeArgs da) 
   int most = 0;
   for (int x = tid; x < a.bt.B; x += 256) {
     int f0;
-    const int nx = small_chunks(a, x, small_tokens(a, x), f0);
-    const int64_t v = (int64_t)nx * a.Hkv;
+    const int tx = small_tokens(a, x), nx = small_chunks(a, x, tx, f0);
+    const int64_t v = (int64_t)nx * (a.Hkv * eights(a, tx));
     most = max(most, nx);
     all += v;
     if (x < b) before += v;
@@ -839,7 +860,7 @@ __global__ void __launch_bounds__(256) paged_decode_merge_kernel(DecodeArgs da) 
     return;
   }
   const int P = even_parts(all, da.ctas);
-  const int64_t u0 = before + (int64_t)h * nch, u1 = u0 + nch;
+  const int64_t u0 = before + (int64_t)hv * nch, u1 = u0 + nch;
   if (warp == 0) {   // the CTAs whose units meet [u0, u1), in order
     int np = 0;
     for (int c0 = 0; c0 < P; c0 += 32) {
@@ -855,7 +876,7 @@ __global__ void __launch_bounds__(256) paged_decode_merge_kernel(DecodeArgs da) 
   __syncthreads();
   const int np = parts;
   const int64_t size = 8 * (int64_t)(dv + 2);
-  const float* part = a.part + ((int64_t)b * a.Hkv + h) * size;
+  const float* part = a.part + ((int64_t)b * most_strips(a) + hv) * size;
   {   // warp r: the weights of row r
     float top = -INFINITY, sum = 0.f;
     for (int c = lane; c < np; c += 32) top = fmaxf(top, part[cta[c] * size + 8 * dv + warp]);
@@ -893,10 +914,11 @@ __global__ void __launch_bounds__(256) paged_decode_merge_kernel(DecodeArgs da) 
   const int col = 32 * blockIdx.z;
   rows_slice(acc, d, a.v.Pi, d, col, part_s, o1);
   if (m > 0) rows_slice(acc + 8 * d, m, a.v.S, d, col, part_s, o2);
-  if (warp >= n * a.G) return;
+  const Strip l = strip_of(a, n, hv);
+  if (warp >= l.rows) return;
   float v = o1[tid];
   if (m > 0) v = fmaf(kQjlScale / (float)m, o2[tid], v);
-  store_any(a.out, a.q_dtype, ((a.bt.q_start[b] + warp / a.G) * (int64_t)a.Hq + h * a.G + warp % a.G) * d + col + lane, v * f[warp]);
+  store_any(a.out, a.q_dtype, row_of(a, b, l.h, l.row0 + warp) * d + col + lane, v * f[warp]);
 }
 
 }  // namespace paged

@@ -231,8 +231,6 @@ int append_tc_bits(const AppendTcArgs& a, int device, bool beside, cudaStream_t 
   }
 }
 
-constexpr int64_t kAppendTcRows = 1024;   // vectors of a kind from which the tensor cores take over
-
 // Keys on one half of the SMs, values on the other: the second kernel starts beside the first and waits for it before it ends.
 int append_tc(const AppendArgs& g, const tq_view& k, const tq_view& v, cudaStream_t s) {
   for (int kind = 0; kind < 2; ++kind) {
@@ -398,7 +396,11 @@ int attn_flash(const AttnArgs& g, const tq_view& k, const tq_view& v, const Flas
 
 // ---------------------------------------------------------------- attention of single tokens
 
-constexpr int kSmallRows = 8;   // query rows of a sequence and KV head that the single-token kernel takes: its product's columns
+// Query rows of a sequence and KV head up to which the single-token kernel takes them, eight at a time (each eight reads the
+// packed rows again; the chunks' kernels expand them once, whatever the rows). Measured at 4 KV heads, d = 128, for 1 to 64
+// sequences of 512 to 32768 tokens, against the chunks' kernels: 4-bit codes 8 rows 31..130 us to 58..817, 32 rows 37..427
+// (174 to 158 in one case of six), 48 rows up to 246 to 158; with signs 16 rows 46..473 to 60..891, 24 rows up to 223 to 174.
+int small_rows(const tq_view& k) { return k.m > 0 ? 16 : 32; }
 
 // Whether the single-token kernel has these formats: 4- or 2-bit codes, signs on both sides or on neither.
 bool decode_formats(const tq_view& k, const tq_view& v, const Batch& b, int Hkv) {
@@ -409,16 +411,19 @@ bool decode_formats(const tq_view& k, const tq_view& v, const Batch& b, int Hkv)
 }
 
 struct DecodePlan {
-  int ctas;
+  int ctas, rows;   // rows: the most that a sequence and KV head have here, a multiple of 8
+  int64_t strips;    // eights of rows, at most
   size_t qr, part, total;
 };
 
-DecodePlan decode_plan(const tq_view& k, const tq_view& v, const Batch& b, int Hkv, int sms) {
+DecodePlan decode_plan(const tq_view& k, const tq_view& v, const Batch& b, int Hq, int Hkv, int sms) {
   DecodePlan p{};
   p.ctas = 2 * sms;
+  p.rows = (int)std::min<int64_t>(small_rows(k), up((size_t)b.max_q * (Hq / Hkv), 8));
+  p.strips = (int64_t)b.B * Hkv * (p.rows / 8);
   p.qr = 0;
-  p.part = up((size_t)b.B * Hkv * 8 * (k.d + k.m) * 4, 256);
-  p.total = p.part + up(((size_t)p.ctas + (size_t)b.B * Hkv) * 8 * (v.d + v.m + 2) * 4, 256) + 256;
+  p.part = up((size_t)p.strips * 8 * (k.d + k.m) * 4, 256);
+  p.total = p.part + up(((size_t)p.ctas + (size_t)p.strips) * 8 * (v.d + v.m + 2) * 4, 256) + 256;
   return p;
 }
 
@@ -453,16 +458,16 @@ int attn_decode_paged(AttnArgs a, const tq_view& k, const tq_view& v, const Deco
   if ((st = allow_smem(paged_decode_merge_kernel, merge, k.device, s1))) return st;
   a.qr = reinterpret_cast<float*>(ws + p.qr);
   a.part = reinterpret_cast<float*>(ws + p.part);
-  a.small_rows = kSmallRows;
+  a.small_rows = p.rows;
   DecodeArgs da{};
   da.a = a, da.ctas = p.ctas;
   // The tables' width may tell that every sequence is short enough for one CTA: then one kernel does it all.
-  const bool one = (int64_t)a.bt.max_pages * a.bt.page_size <= kWholeChunks * kChunk && (int64_t)a.bt.B * a.Hkv <= p.ctas;
+  const bool one = (int64_t)a.bt.max_pages * a.bt.page_size <= kWholeChunks * kChunk && p.strips <= p.ctas;
   if (one) {
-    da.ctas = a.bt.B * a.Hkv;
+    da.ctas = (int)p.strips;
   } else {
     tq_launch_scope scope("paged_qprep", s);
-    paged_qslice_kernel<<<dim3((unsigned)a.bt.B * a.Hkv, (k.d + k.m) / 32), 256, 0, s>>>(da);
+    paged_qslice_kernel<<<dim3((unsigned)p.strips, (k.d + k.m) / 32), 256, 0, s>>>(da);
     if ((st = launched("paged_qslice_kernel"))) return st;
   }
   const bool h = k.norm_dtype == TQ_F16;
@@ -470,7 +475,7 @@ int attn_decode_paged(AttnArgs a, const tq_view& k, const tq_view& v, const Deco
   else st = h ? decode_formats_launch<64, true>(da, one, k.device, s) : decode_formats_launch<64, false>(da, one, k.device, s);
   if (st || one) return st;
   tq_launch_scope scope("paged_dmerge", s);
-  return launch_after(paged_decode_merge_kernel, dim3((unsigned)a.bt.B, (unsigned)a.Hkv, k.d / 32), 256, merge, s, da,
+  return launch_after(paged_decode_merge_kernel, dim3((unsigned)a.bt.B, (unsigned)(a.Hkv * (p.rows / 8)), k.d / 32), 256, merge, s, da,
                       "paged_decode_merge_kernel");
 }
 
@@ -479,8 +484,8 @@ size_t attn_workspace(const tq_view& k, const tq_view& v, const Batch& b, int Hq
   const int sms = device_sms(k.device);
   size_t n = 0;
   if (flash_formats(k, v)) {
-    const int small = decode_formats(k, v, b, Hkv) ? kSmallRows : 0;
-    if (small) n += decode_plan(k, v, b, Hkv, sms).total;
+    const int small = decode_formats(k, v, b, Hkv) ? small_rows(k) : 0;
+    if (small) n += decode_plan(k, v, b, Hq, Hkv, sms).total;
     if ((int64_t)b.max_q * (Hq / Hkv) > small) n += flash_plan(k, b, Hq, Hkv, small, sms).total;
   }
   return std::max(n, simt_plan(k, v, b, Hq, Hkv, sms).total);
@@ -516,8 +521,12 @@ int tq_append_paged(const tq_handle* hk, const tq_handle* hv, const void* k_new,
   a.c[0] = view_of(kw, k), a.c[1] = view_of(vw, v);
   a.err = kw.err;
   const int64_t rows = batch->ntok * Hkv;
-  if (rows >= kAppendTcRows && kw.ops_app && vw.ops_app && !simt_forced()) return append_tc(a, kw, vw, s);
-  const bool few = rows <= 2 * device_sms(kw.device);
+  // While all rows of keys and values run at once, each with 1024 threads, that is quickest: at d = 128, 144 rows of 4-bit codes
+  // take 18.5 us, 19.4 on the tensor cores and 22.6 with eight rows to a CTA; 160 rows 24.6, 20.5 and 22.6 (at d = 64 the
+  // sides meet at 64 rows: 12 us both; 96 rows 16 and 14). More go to the tensor cores, where they have the format (4096
+  // rows: 21 us, 45 otherwise), else eight to a CTA.
+  const bool few = rows <= device_sms(kw.device) / (kw.d <= 64 ? 2 : 1);
+  if (!few && kw.ops_app && vw.ops_app && !simt_forced()) return append_tc(a, kw, vw, s);
   if (kw.d <= 128) return few ? append_simt<1, 1024, 4>(a, kw.device, s) : append_simt<8, kAppThreads, 4>(a, kw.device, s);
   return few ? append_simt<1, 1024, 8>(a, kw.device, s) : append_simt<8, kAppThreads, 8>(a, kw.device, s);
 }
@@ -563,10 +572,10 @@ int tq_attn_paged(const tq_handle* hk, const tq_handle* hv, const void* q, int q
   char* ws = reinterpret_cast<char*>(up(reinterpret_cast<size_t>(workspace), 256));
   const int sms = device_sms(kw.device);
   if (q_dtype != TQ_F32 && flash_formats(kw, vw)) {
-    const int G = Hq / Hkv, small = decode_formats(kw, vw, a.bt, Hkv) ? kSmallRows : 0;
+    const int G = Hq / Hkv, small = decode_formats(kw, vw, a.bt, Hkv) ? small_rows(kw) : 0;
     st = TQ_OK;
     if (small) {
-      const DecodePlan plan = decode_plan(kw, vw, a.bt, Hkv, sms);
+      const DecodePlan plan = decode_plan(kw, vw, a.bt, Hq, Hkv, sms);
       if (G <= small) st = attn_decode_paged(a, kw, vw, plan, ws, s);
       ws += plan.total;
     }

@@ -132,6 +132,20 @@ def test_append(tq, d, kf, vf, Hkv, news, lens, page, dtype, prep):
     check_cache(vc, expected_cache(tq, fv, bt, Hkv, 2, v, None))
 
 
+@pytest.mark.parametrize("d,kf,vf", [(64, "mse4", "prod3"), (128, "prod3", "mse4"), (256, "mse4", "mse2"), (96, "prod3x32", "mse3")])
+@pytest.mark.parametrize("n", [73, 75, 147, 149])
+def test_append_around_the_kernels_borders(tq, d, kf, vf, n):
+    """One row to a CTA, eight, or tiles for the tensor cores: the same indices and signs."""
+    fk, fv = fmt(tq, d, kf, 0), fmt(tq, d, vf, 1)
+    bt = pu.make_batch(tq, [n], [n + 5], 32)
+    k, v = heads(11, n, 1, d, torch.bfloat16), heads(12, n, 1, d, torch.bfloat16)
+    pr = make_prep(tq, "norm+half", d, torch.bfloat16)
+    kc, vc = run_append(tq, fk, fv, bt, k, v, pr, 1)
+    assert fk.handle.status() == tq.TQ_OK
+    check_cache(kc, expected_cache(tq, fk, bt, 1, 1, k, pr))
+    check_cache(vc, expected_cache(tq, fv, bt, 1, 2, v, None))
+
+
 def test_append_pieces_give_the_same_bytes(tq):
     """A prompt appended at once, in chunks and token by token: the same indices and signs; norms at most one step apart
     (the kernels sum their squares in different orders and precisions)."""
@@ -395,6 +409,45 @@ def test_attention_group_sizes(tq, G):
     for news, lens in (([1, 1], [77, 300]), ([50, 1], [60, 300])):
         c = attention_case(tq, 128, "mse4", "mse4", 1, G, news, lens, 16, "bf16", "half")
         check_case(tq, c, 0.09, True, 0, H_F16)
+
+
+EIGHTS = [
+    # d, keys, values, Hkv, G, new, cached, page, prep, causal, window: 9 to 32 (16 with signs) rows for some sequences
+    (128, "mse4", "mse4", 2, 4, [4, 1, 8, 3], [40, 700, 3000, 3], 16, "half", True, 0),
+    (128, "mse4", "mse2", 2, 8, [2, 4, 1], [1500, 1537, 129], 64, "norm+half", True, 0),
+    (128, "mse2", "mse2", 1, 3, [7, 10, 2], [900, 2500, 64], 32, "none", True, 50),
+    (128, "prod3", "prod3", 2, 16, [1, 1], [77, 2000], 32, "half", True, 0),
+    (128, "prod3", "prod3", 2, 5, [3, 2, 1], [300, 1700, 9], 16, "partial", True, 200),
+    (64, "prod3", "prod3", 1, 4, [4, 3], [90, 4000], 256, "half", True, 0),
+    (64, "mse4", "mse4", 3, 1, [32, 9, 17, 33, 200], [1500, 16, 444, 800, 1000], 32, "none", False, 0),
+    (64, "mse4", "mse4", 12, 1, [17, 25], [600, 1536], 16, "none", False, 0),
+    (128, "mse4", "mse4", 1, 32, [1, 1], [31, 5000], 48, "half", True, 1000),
+    (128, "mse4", "mse4", 2, 4, [8, 5, 0, 6], [3, 0, 4, 6], 16, "none", True, 0),   # rows before the first position, no keys
+    (128, "mse4", "mse4", 2, 4, [7, 100, 1, 5], [4000, 400, 1, 5], 16, "half", True, 0),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("d,kf,vf,Hkv,G,news,lens,page,prep,causal,window", EIGHTS)
+def test_attention_of_several_eights_of_rows(tq, d, kf, vf, Hkv, G, news, lens, page, prep, causal, window, dtype):
+    c = attention_case(tq, d, kf, vf, Hkv, G, news, lens, page, dtype, prep, causal, window)
+    check_case(tq, c, 1 / np.sqrt(d), causal, window, H_F16)
+
+
+def test_eights_of_rows_stay_in_their_workspace(tq):
+    """A batch with more tokens than max_q in a sequence: nothing is written behind the workspace or in other sequences' rows."""
+    c = attention_case(tq, 128, "mse4", "mse4", 2, 4, [2, 6, 1], [700, 900, 30], 16, "bf16")
+    fk, fv, bt, kc, vc, kr, vr, q, pr = c
+    less = tq.PagedBatch(bt.q_start, bt.len, bt.block_table, bt.ntok, 2)
+    size = tq.tq_attn_paged_workspace_bytes(fk.handle.ptr, fv.handle.ptr, less.struct, 8, 2, kc.struct)
+    guard = torch.full((size + 65536,), 77, dtype=torch.uint8, device="cuda")
+    out = torch.full_like(q, float("nan"))
+    tq.attn_paged(fk.handle, fv.handle, q, kc, vc, less, 0.09, out=out, workspace=guard[:size])
+    fk.handle.status()
+    assert (guard[size:] == 77).all()
+    ref, tol = pu.attention_ref(bt, q, fk, fv, kr, vr, 0.09, True, 0, None, H_F16)
+    for rows in (slice(0, 2), slice(8, 9)):
+        pu.check_attention(out[rows], ref[rows], tol[rows], q.dtype)
 
 
 @pytest.mark.parametrize("B", [300, 2100])
