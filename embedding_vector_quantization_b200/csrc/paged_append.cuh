@@ -14,6 +14,9 @@
 //      and m_norm the largest row of M in the 1-norm and the 2-norm, and |e| <= 1. The exact value is then taken as
 //      (S z)_j / N - (M c[idx])_j: two dot products, no further rotation.
 // At d = 128 about 5e-4 of the 4-bit indices and 6e-4 of the signs are computed twice.
+//
+// Bound by latency where rows are few (32 tokens of 4 heads, keys and values: 18 us, 25 with signs) and by fp32 products
+// from shared memory where they are many (16384 tokens of 8 heads with signs: 1.8 ms, 0.13 on the tensor cores).
 #pragma once
 
 #include "paged_common.cuh"

@@ -15,6 +15,11 @@
 //
 // Roundings: c[idx], Pi, S, rnorm / norm, x_hat, the prepared query (scaled by a power of two below 1) and the weights
 // to f16 (11 bits; outputs have 8 or 11); every sum, maximum and exponent in fp32.
+//
+// Measured at 8 KV heads, 32 query heads, d = 128: a chunk of 1024 tokens over 32768 with signs takes 685 us (expansion 80,
+// flash 550: 1.05 PFLOP/s, 0.64 of what a plain matrix product reaches); four prompts of up to 4096 tokens 376 us (flash 265).
+// The flash kernel is bound by the softmax between its two products: a tile's exponents, scales and conversions occupy the
+// issue slots as long as its contractions the tensor pipe (46 % busy with the triangles' half tiles counted, XU 37 %, ALU 29 %).
 #pragma once
 
 #include <climits>
@@ -906,7 +911,9 @@ __device__ __forceinline__ bool bar_any(int id, int n, bool pred) {
       : "memory");
   return r != 0;
 }
-constexpr int kPolyEvery = 4;   // of so many pairs one goes to the polynomial
+// Of so many pairs of exponentials one goes to the polynomial: 546 us with a fourth for a chunk of 1024 tokens over 32768
+// (8 KV heads, 32 query heads, d = 128), 549 with a third, 559 with half and 557 without.
+constexpr int kPolyEvery = 4;
 
 template <int D>
 __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a) {

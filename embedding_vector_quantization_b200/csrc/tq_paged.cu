@@ -313,14 +313,17 @@ struct FlashPlan {
 
 constexpr size_t kRowsCap = (size_t)1 << 30;   // f16 rows held at a time, unless one KV head needs more
 
-FlashPlan flash_plan(const tq_view& k, const Batch& b, int Hq, int Hkv, int small_rows, int sms) {
+// other: whether sequences with up to 8 query rows of a KV head go elsewhere (those with more may, which changes no size).
+FlashPlan flash_plan(const tq_view& k, const Batch& b, int Hq, int Hkv, bool other, int sms) {
   FlashPlan p{};
   const int64_t G = Hq / Hkv;
-  p.max_seqs = std::min<int64_t>(b.B, b.ntok * G / (small_rows + 1));
+  p.max_seqs = std::min<int64_t>(b.B, std::min(b.ntok, other ? b.ntok * G / 9 : b.ntok));
   p.max_tiles = std::max<int64_t>(1, p.max_seqs * (((int64_t)b.max_pages * b.page_size + kKT - 1) / kKT));
   p.max_items = std::max<int64_t>(1, b.ntok * G / kItemRows + p.max_seqs);
   const size_t tile = (size_t)(k.d / 64) * kAtomRows;
   p.heads = (int)std::max<size_t>(1, std::min<size_t>(Hkv, kRowsCap / (2 * tile * (size_t)p.max_tiles)));
+  // Sizes that grow with every argument, unlike heads: a smaller batch never needs more.
+  const size_t rows = std::min((size_t)Hkv * p.max_tiles * tile, std::max(kRowsCap / 2, (size_t)p.max_tiles * tile));
   p.ctas = sms;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -332,14 +335,14 @@ FlashPlan flash_plan(const tq_view& k, const Batch& b, int Hq, int Hkv, int smal
   p.tile_start = take((size_t)(b.B + 1) * 4);
   p.item_start = take((size_t)(b.B + 1) * 4);
   p.unit = take((size_t)(p.max_items + 1) * 4);
-  p.ke = take((size_t)p.heads * p.max_tiles * 4);
-  p.ve = take((size_t)p.heads * p.max_tiles * 4);
+  p.ke = take((size_t)Hkv * p.max_tiles * 4);
+  p.ve = take((size_t)Hkv * p.max_tiles * 4);
   p.seen = take((size_t)p.max_tiles * 16);
   p.part = take((size_t)2 * p.ctas * kItemRows * (k.d + 4) * 4);
-  p.krows = take((size_t)p.heads * p.max_tiles * tile);
-  p.vrows = take((size_t)p.heads * p.max_tiles * tile);
-  p.qrows = take((size_t)p.heads * p.max_items * 2 * tile);
-  p.qfactor = take((size_t)p.heads * p.max_items * kItemRows * 4);
+  p.krows = take(rows);
+  p.vrows = take(rows);
+  p.qrows = take((size_t)Hkv * p.max_items * 2 * tile);
+  p.qfactor = take((size_t)Hkv * p.max_items * kItemRows * 4);
   p.total = at + 256;
   return p;
 }
@@ -413,6 +416,7 @@ bool decode_formats(const tq_view& k, const tq_view& v, const Batch& b, int Hkv)
 struct DecodePlan {
   int ctas, rows;   // rows: the most that a sequence and KV head have here, a multiple of 8
   int64_t strips;    // eights of rows, at most
+  bool one;
   size_t qr, part, total;
 };
 
@@ -420,10 +424,18 @@ DecodePlan decode_plan(const tq_view& k, const tq_view& v, const Batch& b, int H
   DecodePlan p{};
   p.ctas = 2 * sms;
   p.rows = (int)std::min<int64_t>(small_rows(k), up((size_t)b.max_q * (Hq / Hkv), 8));
-  p.strips = (int64_t)b.B * Hkv * (p.rows / 8);
+  const int64_t heads = (int64_t)b.B * Hkv;
+  p.strips = heads * (p.rows / 8);
   p.qr = 0;
   p.part = up((size_t)p.strips * 8 * (k.d + k.m) * 4, 256);
   p.total = p.part + up(((size_t)p.ctas + (size_t)p.strips) * 8 * (v.d + v.m + 2) * 4, 256) + 256;
+  // The tables' width may tell that every sequence is short enough for one CTA: then one kernel does it all, for as many
+  // rows as the CTAs hold (16 sequences x 12 heads of 512 keys, d = 64: 24 us, 51 with more, 47 on the chunks' kernels).
+  p.one = (int64_t)b.max_pages * b.page_size <= kWholeChunks * kChunk && heads <= p.ctas;
+  if (p.one) {
+    p.rows = (int)std::min<int64_t>(p.rows, p.ctas / heads * 8);
+    p.strips = heads * (p.rows / 8);
+  }
   return p;
 }
 
@@ -461,8 +473,7 @@ int attn_decode_paged(AttnArgs a, const tq_view& k, const tq_view& v, const Deco
   a.small_rows = p.rows;
   DecodeArgs da{};
   da.a = a, da.ctas = p.ctas;
-  // The tables' width may tell that every sequence is short enough for one CTA: then one kernel does it all.
-  const bool one = (int64_t)a.bt.max_pages * a.bt.page_size <= kWholeChunks * kChunk && p.strips <= p.ctas;
+  const bool one = p.one;
   if (one) {
     da.ctas = (int)p.strips;
   } else {
@@ -484,9 +495,11 @@ size_t attn_workspace(const tq_view& k, const tq_view& v, const Batch& b, int Hq
   const int sms = device_sms(k.device);
   size_t n = 0;
   if (flash_formats(k, v)) {
-    const int small = decode_formats(k, v, b, Hkv) ? small_rows(k) : 0;
-    if (small) n += decode_plan(k, v, b, Hq, Hkv, sms).total;
-    if ((int64_t)b.max_q * (Hq / Hkv) > small) n += flash_plan(k, b, Hq, Hkv, small, sms).total;
+    const bool other = decode_formats(k, v, b, Hkv);
+    Batch fewer = b;   // no smaller batch needs more
+    fewer.B = std::min(b.B, kDcMaxB);
+    if (decode_formats(k, v, fewer, Hkv)) n += decode_plan(k, v, fewer, Hq, Hkv, sms).total;
+    if (!other || (int64_t)b.max_q * (Hq / Hkv) > 8) n += flash_plan(k, b, Hq, Hkv, other, sms).total;
   }
   return std::max(n, simt_plan(k, v, b, Hq, Hkv, sms).total);
 }
@@ -572,15 +585,18 @@ int tq_attn_paged(const tq_handle* hk, const tq_handle* hv, const void* q, int q
   char* ws = reinterpret_cast<char*>(up(reinterpret_cast<size_t>(workspace), 256));
   const int sms = device_sms(kw.device);
   if (q_dtype != TQ_F32 && flash_formats(kw, vw)) {
-    const int G = Hq / Hkv, small = decode_formats(kw, vw, a.bt, Hkv) ? small_rows(kw) : 0;
+    const int G = Hq / Hkv;
+    const bool other = decode_formats(kw, vw, a.bt, Hkv);
+    int small = 0;
     st = TQ_OK;
-    if (small) {
+    if (other) {
       const DecodePlan plan = decode_plan(kw, vw, a.bt, Hq, Hkv, sms);
+      small = plan.rows;
       if (G <= small) st = attn_decode_paged(a, kw, vw, plan, ws, s);
       ws += plan.total;
     }
     if (st || (int64_t)a.bt.max_q * G <= small) return st;
-    const FlashPlan plan = flash_plan(kw, a.bt, Hq, Hkv, small, sms);
+    const FlashPlan plan = flash_plan(kw, a.bt, Hq, Hkv, other, sms);
     return kw.d == 128 ? attn_flash<128>(a, kw, vw, plan, small, G <= small, ws, s)
                        : attn_flash<64>(a, kw, vw, plan, small, G <= small, ws, s);
   }

@@ -338,7 +338,7 @@ typedef struct tq_head_prep {
  *  hk, hv        MSE, prod or QJL-only handles of one d <= 256 (m <= 256), on one device
  * The indices and signs are those of exact arithmetic: a coordinate that lies within the rounding of the fast
  * path of a border is computed again in 64 bits, so a token's codes and signs depend neither on the batch it
- * came in nor on the kernel that wrote it (norms, sums in fp32 or fp64, may differ by one step).
+ * came in nor on the kernel that wrote it (norms may differ by one step of fp16, two of fp32).
  * A token whose page (outside 0 .. num_pages - 1, position outside 0 .. max_pages * page_size - 1) or rotation
  * position (outside 0 .. max_pos - 1) is out of range is skipped and recorded in hk's error word (TQ_EINVAL
  * from tq_last_status). Two tokens with the same place race; which one stays is undefined. */
@@ -378,7 +378,10 @@ int tq_attn_paged(const tq_handle* hk, const tq_handle* hv, const void* q, int q
 /* While enabled, every kernel launched by the library is bracketed by two CUDA
  * events recorded on the launching stream (events come from a pool owned by
  * the library). Kernels are named "encode", "advance_len", "pack", "qprep",
- * "score", "attn_split", "attn_combine", "search", "topk_merge".
+ * "score", "attn_split", "attn_combine", "search", "topk_merge"; those of the paged calls
+ * "append_paged", "paged_qprep", "paged_decode", "paged_dmerge" (few query rows), "paged_plan",
+ * "paged_expand", "paged_qtile", "paged_flash", "paged_merge" (chunks), "paged_attn",
+ * "paged_combine" (with "paged_qprep": general formats).
  * tq_timer_enable(0) stops recording; recorded events are kept until read. */
 int tq_timer_enable(int on);
 

@@ -11,6 +11,10 @@ value; independent roundings, six standard deviations, each bounded by its large
 * the mapped-back sum o = Pi^T acc + c S^T acc_s: acc, Pi (and S) rounded once: 2 h sqrt(sum_j Pi_ji^2 acc_j^2);
 * the output's own rounding: eps / 2 |o|, not a matter of chance and outside the factor of six.
 
+The kernels for chunks expand the keys and values to the original basis first and leave queries and outputs there. Their
+roundings are as many and as large: centroid, Pi (S), the expanded row and the prepared query, once each, move a score by
+the same four terms, because Pi keeps lengths; the weights and the expanded values by 2 h; nothing is mapped back.
+
 The general kernels keep everything in fp32; sums of n <= 512 products grow a rounding by at most sqrt(n) < 23: h = 23 / 2^24.
 """
 

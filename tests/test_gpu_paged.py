@@ -484,6 +484,29 @@ def test_simt_switch_agrees(tq, monkeypatch):
     check_cache(a[0], b[0]), check_cache(a[1], b[1])
 
 
+def test_workspaces_serve_smaller_batches(tq):
+    """The size for a batch is enough for every batch with no argument larger."""
+    g = np.random.default_rng(0)
+    one = torch.zeros(2, dtype=torch.int32, device="cuda")
+    for d, kf in ((128, "mse4"), (128, "prod3"), (64, "mse4"), (96, "mse3")):
+        h = fmt(tq, d, kf, 0).handle
+        cache = tq.PagedCache(h, 1, 1, 64)
+
+        def size(B, ntok, pages, max_q, Hq, Hkv):
+            s = tq.PagedBatch(one, one[:1], one[:1, None], 1).struct
+            s.B, s.ntok, s.max_pages, s.max_q = B, ntok, pages, max_q
+            return tq.tq_attn_paged_workspace_bytes(h.ptr, h.ptr, s, Hq, Hkv, cache.struct)
+
+        for _ in range(3000):
+            Hkv = int(g.choice([1, 2, 8, 12, 32]))
+            Hq = Hkv * int(g.choice([1, 3, 4, 8, 16, 32]))
+            B, ntok, pages = (int(2 ** g.uniform(0, top)) for top in (13, 16, 10))
+            max_q = int(g.integers(1, ntok + 1))
+            B2, n2, p2 = (int(x if g.random() < 0.4 else g.integers(1, x + 1)) for x in (B, ntok, pages))
+            q2 = min(n2, int(max_q if g.random() < 0.4 else g.integers(1, max_q + 1)))
+            assert 0 < size(B2, n2, p2, q2, Hq, Hkv) <= size(B, ntok, pages, max_q, Hq, Hkv)
+
+
 def test_two_streams_at_once(tq):
     """Two batches on two streams, each with its own workspace, appended and attended to at the same time."""
     jobs = []
