@@ -294,7 +294,11 @@ def _head_rows(x, name, ntok, d):
     return x
 
 
-def _check_paged(kcache, vcache, batch, prep, d):
+def _check_paged(hk, hv, kcache, vcache, batch, prep):
+    for h, own in ((hk, kcache.handle), (hv, vcache.handle)):
+        if h is not own and (h.codes_B, h.signs_B, h.norm_dtype, h.prod) != (own.codes_B, own.signs_B, own.norm_dtype, own.prod):
+            _need(False, "a cache was made for rows of another format than its handle's")
+    d = hk.d
     if kcache.Hkv != vcache.Hkv:
         _need(False, "the caches differ in Hkv")
     if not kcache.index == vcache.index == batch.index:
@@ -332,7 +336,7 @@ def append_paged(hk, hv, k, v, kcache, vcache, batch, prep=None, stream=None):
     if stream is not None:
         with _on(stream, kcache.device):
             return append_paged(hk, hv, k, v, kcache, vcache, batch, prep)
-    _check_paged(kcache, vcache, batch, prep, hk.d)
+    _check_paged(hk, hv, kcache, vcache, batch, prep)
     k, v = _head_rows(k, "k", batch.ntok, hk.d), _head_rows(v, "v", batch.ntok, hk.d)
     if not k.shape[1] == v.shape[1] == kcache.Hkv:
         _need(False, "k and v need one head for each of the caches'")
@@ -350,7 +354,7 @@ def attn_paged(hk, hv, q, kcache, vcache, batch, scale, causal=True, window=0, p
     if stream is not None:
         with _on(stream, kcache.device):
             return attn_paged(hk, hv, q, kcache, vcache, batch, scale, causal, window, prep, out, workspace)
-    _check_paged(kcache, vcache, batch, prep, hk.d)
+    _check_paged(hk, hv, kcache, vcache, batch, prep)
     q = _head_rows(q, "q", batch.ntok, hk.d)
     Hq = q.shape[1]
     if q.get_device() != kcache.index:

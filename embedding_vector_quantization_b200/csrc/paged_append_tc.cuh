@@ -80,22 +80,34 @@ __device__ __forceinline__ bool test_bar(uint32_t bar, uint32_t parity) {
   return done;
 }
 
-// The sum of squares of a row that four lanes hold. Eights are summed in fp32 and those in fp64: a norm stored in fp32 is off
+// The sum of squares of a row that four lanes hold, times f^2. Eights are summed in fp32 and those in fp64: a norm stored in fp32 is off
 // by half a step for the root, a quarter for this result's rounding and about 0.15 for the eights (one sum of 32 in fp32: a
 // step more).
 template <int C>
-__device__ __forceinline__ float row_squares(const float (&z)[8 * C]) {
+__device__ __forceinline__ float row_squares(const float (&z)[8 * C], float f = 1.f) {
   double ss = 0.0;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    float p = z[8 * c] * z[8 * c];
+    float p = (z[8 * c] * f) * (z[8 * c] * f);
 #pragma unroll
-    for (int x = 1; x < 8; ++x) p = fmaf(z[8 * c + x], z[8 * c + x], p);
+    for (int x = 1; x < 8; ++x) p = fmaf(z[8 * c + x] * f, z[8 * c + x] * f, p);
     ss += (double)p;
   }
   ss += __shfl_xor_sync(0xffffffffu, ss, 1);
   ss += __shfl_xor_sync(0xffffffffu, ss, 2);
   return (float)ss;
+}
+
+// 1 / sqrt(mean of squares + eps) of such a row; the whole warp calls it.
+template <int C>
+__device__ __forceinline__ float row_rms(const float (&z)[8 * C], int d, float eps) {
+  const float ss = row_squares<C>(z);
+  const bool many = !(ss < kManySquares);
+  if (__any_sync(0xffffffffu, many)) {
+    const float s2 = row_squares<C>(z, kSmaller);
+    if (many) return kSmaller / sqrtf(s2 / (float)d);
+  }
+  return 1.f / sqrtf(ss / (float)d + eps);
 }
 
 // Index of |y| among the positive half of a symmetric codebook (H = 2^(BITS - 1) cells, H - 1 positive borders b[1 ..]), the
@@ -287,7 +299,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) paged_append_tc_kernel(AppendTc
         }
         float rms = 1.f;
         if (a.prep.weight) {
-          rms = 1.f / sqrtf(row_squares<C>(z) / (float)D + a.prep.eps);
+          rms = row_rms<C>(z, D, a.prep.eps);
 #pragma unroll
           for (int x = 0; x < 8 * C; ++x)
             z[x] *= rms * load_any(a.prep.weight, a.prep.weight_dtype, 8 * (ql + 4 * (x >> 3)) + (x & 7));

@@ -82,6 +82,10 @@ __device__ __forceinline__ int64_t place_of(const Batch& bt, int b, int64_t p, i
   return (page * Hkv + h) * bt.page_size + slot;
 }
 
+// Squares above this are summed again of vectors times 2^-70 (exact): the sum of 256 stays within fp32. eps is nothing to them.
+constexpr float kManySquares = 1e37f;
+constexpr float kSmaller = 8.4703295e-22f;   // 2^-70
+
 // The warp's lanes prepare one head x[0 .. d) (d <= 256): lane l holds coordinates l, l + 32, ... in z[]. T is
 // double where a code's exact index is at stake, float for queries. p: the rotation position (checked by the caller).
 template <typename T, int MAXC>
@@ -97,7 +101,14 @@ __device__ __forceinline__ void prep_head(const void* x, int x_dtype, int64_t at
   }
   if (pr.weight) {
     for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const T r = (T)1 / sqrt(ss / (T)d + (T)pr.eps);
+    T r = (T)1 / sqrt(ss / (T)d + (T)pr.eps);
+    if (sizeof(T) == 4 && !(ss < (T)kManySquares)) {   // the whole warp's
+      ss = 0;
+#pragma unroll
+      for (int c = 0; c < MAXC; ++c) ss += (z[c] * (T)kSmaller) * (z[c] * (T)kSmaller);
+      for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      r = (T)kSmaller / sqrt(ss / (T)d);
+    }
 #pragma unroll
     for (int c = 0; c < MAXC; ++c) {
       const int i = lane + 32 * c;

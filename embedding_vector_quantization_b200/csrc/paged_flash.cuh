@@ -694,6 +694,15 @@ __global__ void __launch_bounds__(kQtThreads) paged_qtile_kernel(FlashArgs a) {
   ss += __shfl_xor_sync(0xffffffffu, ss, 2);
   if (a.prep.weight) {
     rms = rsqrtf(ss / (float)D + a.prep.eps);
+    const bool many = !(ss < kManySquares);
+    if (__any_sync(0xffffffffu, many)) {
+      float s2 = 0.f;
+#pragma unroll
+      for (int x = 0; x < 8 * C; ++x) s2 = fmaf(z[x] * kSmaller, z[x] * kSmaller, s2);
+      s2 += __shfl_xor_sync(0xffffffffu, s2, 1);
+      s2 += __shfl_xor_sync(0xffffffffu, s2, 2);
+      if (many) rms = kSmaller * rsqrtf(s2 / (float)D);
+    }
     ss = 0.f;
 #pragma unroll
     for (int x = 0; x < 8 * C; ++x) {

@@ -484,6 +484,64 @@ def test_simt_switch_agrees(tq, monkeypatch):
     check_cache(a[0], b[0]), check_cache(a[1], b[1])
 
 
+@pytest.mark.parametrize("n", [2, 300])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_norm_of_vectors_whose_squares_overflow(tq, n, dtype):
+    """Heads of 1e25 (their squares pass fp32) come out of the norm like heads of one: codes, signs and attention."""
+    fk, fv = fmt(tq, 128, "prod3", 0), fmt(tq, 128, "mse4", 1)
+    bt = pu.make_batch(tq, [n], [n], 16)
+    x, v = heads(13, n, 2, 128, DT[dtype]), heads(14, n, 2, 128, DT[dtype])
+    x[::2] *= 2.0 ** 83
+    pr = make_prep(tq, "norm+half", 128, DT[dtype])
+    kc, vc = run_append(tq, fk, fv, bt, x, v, pr, 2)
+    check_cache(kc, expected_cache(tq, fk, bt, 2, 1, x, pr))
+    fk, fv, bt, kc, vc, kr, vr, q, pr = attention_case(tq, 128, "mse4", "mse4", 2, 4, [n, 1], [400, 90], 16, dtype, "norm+half")
+    q[::2] *= 2.0 ** 83
+    check_case(tq, (fk, fv, bt, kc, vc, kr, vr, q, pr), 0.09, True, 0, H_FP32 if dtype == "fp32" else H_F16)
+
+
+def test_caches_of_another_format_are_refused(tq):
+    c = attention_case(tq, 128, "mse4", "mse4", 2, 4, [1], [40], 16, "bf16")
+    fk, fv, bt, kc, vc, kr, vr, q, pr = c
+    for name, norm in (("mse2", "f16"), ("prod3", "f16"), ("mse4", "f32")):
+        other = fmt(tq, 128, name, 5, norm).handle
+        for hk, hv in ((other, fv.handle), (fk.handle, other)):
+            with pytest.raises(tq.TQError, match="another format"):
+                tq.attn_paged(hk, hv, q, kc, vc, bt, 0.09)
+            with pytest.raises(tq.TQError, match="another format"):
+                tq.append_paged(hk, hv, q[:, :2], q[:, 2:4], kc, vc, bt)
+    again = fmt(tq, 128, "mse4", 0).handle   # one with the rows' format is taken
+    tq.attn_paged(again, fv.handle, q, kc, vc, bt, 0.09)
+
+
+def test_offsets_past_32_bits(tq):
+    """The last pages of caches whose codes and f16 rows' places pass 2^32 bytes: the same bytes and results as in small ones."""
+    fk, fv = fmt(tq, 128, "mse4", 0), fmt(tq, 128, "mse4", 1)
+    Hkv, page, big = 2, 64, 2 ** 19 + 1024           # 2^19 pages x 2 heads x 64 rows x 64 bytes = 2^32
+    news, lens = [150, 1, 5], [700, 900, 40]
+    bt = pu.make_batch(tq, news, lens, page)
+    full = pu.make_batch(tq, lens, lens, page)
+    shift = big - bt.num_pages
+    x, v = heads(15, full.ntok, Hkv, 128, torch.bfloat16), heads(16, full.ntok, Hkv, 128, torch.bfloat16)
+    q = heads(17, bt.ntok, 4 * Hkv, 128, torch.bfloat16, outliers=False)
+    small = [tq.PagedCache(f.handle, bt.num_pages, Hkv, page) for f in (fk, fv)]
+    large = [tq.PagedCache(f.handle, big, Hkv, page) for f in (fk, fv)]
+    for caches, off in ((small, 0), (large, shift)):
+        table = torch.where(full.block_table >= 0, full.block_table + off, full.block_table)
+        tq.append_paged(fk.handle, fv.handle, x, v, *caches, tq.PagedBatch(full.q_start, full.len, table, full.ntok))
+    assert fk.handle.status() == tq.TQ_OK
+    for a, b in zip(small, large):
+        assert torch.equal(a.codes, b.codes[shift:]) and torch.equal(a.norms, b.norms[shift:])
+        assert not b.codes[:shift].any()
+    for dtype in (torch.bfloat16, torch.float32):
+        outs = []
+        for caches, off in ((small, 0), (large, shift)):
+            table = torch.where(full.block_table >= 0, full.block_table + off, full.block_table)
+            b = tq.PagedBatch(bt.q_start, bt.len, table, bt.ntok)
+            outs.append(tq.attn_paged(fk.handle, fv.handle, q.to(dtype), *caches, b, 0.09))
+        assert fk.handle.status() == tq.TQ_OK and torch.equal(*outs) and outs[0].abs().sum() > 0
+
+
 def test_workspaces_serve_smaller_batches(tq):
     """The size for a batch is enough for every batch with no argument larger."""
     g = np.random.default_rng(0)
