@@ -762,20 +762,32 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
 
 // ---- the small products around it: 8 rows times 32 columns of a constant matrix per CTA
 
-// out[r][0 .. 31] = sum_i in[r][i] T[i][col .. col + 31] (row length ld) for 8 rows: warp w sums its eighth of i; the eight
-// parts meet in part_s ([8 warps][8 rows][32]) in a fixed order.
-__device__ __forceinline__ void rows_slice(const float* in, int ni, const float* T, int ld, int col, float* part_s, float* out) {
+// out[r][0 .. 31] = sum_i in[r][i] T[i][col .. col + 31] (row length ld) for 8 rows and ni <= 128: warp w sums its eighth of
+// i; the eight parts meet in part_s ([8 warps][8 rows][32]) in a fixed order. The matrix's share is asked for at once, by
+// the queries' kernel while its vectors are on their way (10 -> 8 us); the merge asks when its sums are made (asked before
+// they are read, the registers cost those reads their overlap: 22 -> 31 us).
+struct Slice {
+  float p[16];
+};
+__device__ __forceinline__ Slice slice_of(const float* T, int ni, int ld, int col) {
+  Slice s;
+  const int share = ni / 8;
+  const float* t = T + (size_t)((threadIdx.x >> 5) * share) * ld + col + (threadIdx.x & 31);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s.p[i] = i < share ? __ldg(t + (size_t)i * ld) : 0.f;
+  return s;
+}
+__device__ __forceinline__ void rows_slice(const float* in, int ni, const Slice& T, float* part_s, float* out) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, share = ni / 8;   // ni: a multiple of 32
   float acc[8];
 #pragma unroll
   for (int r = 0; r < 8; ++r) acc[r] = 0.f;
-  const float* t = T + (size_t)(warp * share) * ld + col + lane;
-#pragma unroll 16
-  for (int i = 0; i < share; ++i) {
-    const float p = __ldg(t + (size_t)i * ld);
 #pragma unroll
-    for (int r = 0; r < 8; ++r) acc[r] = fmaf(in[r * ni + warp * share + i], p, acc[r]);
-  }
+  for (int i = 0; i < 16; ++i)
+    if (i < share) {
+#pragma unroll
+      for (int r = 0; r < 8; ++r) acc[r] = fmaf(in[r * ni + warp * share + i], T.p[i], acc[r]);
+    }
 #pragma unroll
   for (int r = 0; r < 8; ++r) part_s[(warp * 8 + r) * 32 + lane] = acc[r];
   __syncthreads();
@@ -797,6 +809,9 @@ __global__ void __launch_bounds__(256) paged_qslice_kernel(DecodeArgs da) {
   const int n = small_tokens(a, b);
   if (hv >= a.Hkv * eights(a, n)) return;
   const Strip l = strip_of(a, n, hv);
+  const int col = 32 * blockIdx.y;
+  const bool code = col < d;
+  const Slice T = slice_of(code ? a.k.PiT : a.k.ST, d, code ? d : m, code ? col : col - d);
   float z[4] = {0.f, 0.f, 0.f, 0.f};
   bool blind = false;
   if (r < l.rows) {
@@ -814,9 +829,7 @@ __global__ void __launch_bounds__(256) paged_qslice_kernel(DecodeArgs da) {
   for (int c = 0; c < 4; ++c)
     if (lane + 32 * c < d) zf[r * d + lane + 32 * c] = z[c];
   __syncthreads();
-  const int col = 32 * blockIdx.y;
-  const bool code = col < d;
-  rows_slice(zf, d, code ? a.k.PiT : a.k.ST, code ? d : m, code ? col : col - d, part_s, ys);
+  rows_slice(zf, d, T, part_s, ys);
   const float f = a.scale * 1.44269504089f * (code ? 1.f : kQjlScale / (float)m);
   a.qr[((int64_t)blockIdx.x * 8 + r) * dk + col + lane] = blind ? kBlind : ys[tid] * f;
 }
@@ -886,18 +899,28 @@ __global__ void __launch_bounds__(256) paged_decode_merge_kernel(DecodeArgs da) 
   const float* part = a.part + ((int64_t)b * most_strips(a) + hv) * size;
   {   // warp r: the weights of row r
     float top = -INFINITY, sum = 0.f;
-    for (int c = lane; c < np; c += 32) top = fmaxf(top, part[cta[c] * size + 8 * dv + warp]);
+    float mine = -INFINITY, part_sum = 0.f;   // of part `lane`; the others are read twice
+    if (lane < np) {
+      const float* p = part + cta[lane] * size + 8 * dv;
+      mine = p[warp], part_sum = p[8 + warp];
+    }
+    top = mine;
+    for (int c = lane + 32; c < np; c += 32) top = fmaxf(top, part[cta[c] * size + 8 * dv + warp]);
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     for (int c = lane; c < np; c += 32) {
-      const float* p = part + cta[c] * size + 8 * dv;
-      const float w = p[warp] == -INFINITY ? 0.f : ex2(p[warp] - top);
+      if (c >= 32) {
+        const float* p = part + cta[c] * size + 8 * dv;
+        mine = p[warp], part_sum = p[8 + warp];
+      }
+      const float w = mine == -INFINITY ? 0.f : ex2(mine - top);
       wgt[c * 8 + warp] = w;
-      sum = fmaf(w, p[8 + warp], sum);
+      sum = fmaf(w, part_sum, sum);
     }
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) f[warp] = sum > 0.f ? 1.f / sum : 0.f;
   }
   __syncthreads();
+  const int col = 32 * blockIdx.z;
   {   // thread: elements tid, tid + 256, ... of the sums, all of row tid mod 8
     float v[8];
 #pragma unroll
@@ -917,10 +940,12 @@ __global__ void __launch_bounds__(256) paged_decode_merge_kernel(DecodeArgs da) 
       if (k < nk) acc[j < d ? r * d + j : 8 * d + r * m + j - d] = v[k];
     }
   }
+  const Slice tc = slice_of(a.v.Pi, d, d, col);
+  Slice ts;
+  if (m > 0) ts = slice_of(a.v.S, m, d, col);
   __syncthreads();
-  const int col = 32 * blockIdx.z;
-  rows_slice(acc, d, a.v.Pi, d, col, part_s, o1);
-  if (m > 0) rows_slice(acc + 8 * d, m, a.v.S, d, col, part_s, o2);
+  rows_slice(acc, d, tc, part_s, o1);
+  if (m > 0) rows_slice(acc + 8 * d, m, ts, part_s, o2);
   const Strip l = strip_of(a, n, hv);
   if (warp >= l.rows) return;
   float v = o1[tid];
