@@ -10,7 +10,7 @@
 //   signs of D2.
 // Bound by the preparation: its loads of positions, pages, cosines and vectors depend on one another, and two tiles of two
 // stages do not hide them (tensor pipe 21 %, ALU 45 % busy). 8 heads x 16384 tokens of bf16 with rotation and signs, keys and values:
-// 124 us warm, 130 cold, where the bytes alone would take 14.
+// 126 us warm, 131 cold, where the bytes alone would take 14.
 // Two tiles are under way at a time, each with its own 256 columns: D1, then D2 in the same 128; e_h and e_l in the others.
 //
 // Exactness. A coordinate closer to a border than kTcBandY, and a sign closer to 0 than kTcBandS, is computed again by its

@@ -881,9 +881,9 @@ __global__ void __launch_bounds__(256) paged_decode_merge_kernel(DecodeArgs da) 
   }
   const int P = even_parts(all, da.ctas);
   const int64_t u0 = before + (int64_t)hv * nch, u1 = u0 + nch;
-  if (warp == 0) {   // the CTAs whose units meet [u0, u1), in order
+  if (warp == 0) {   // the CTAs whose units meet [u0, u1), in order; none if it is empty, though it may lie inside one's share
     int np = 0;
-    for (int c0 = 0; c0 < P; c0 += 32) {
+    for (int c0 = 0; c0 < P && nch > 0; c0 += 32) {
       const Span q = span_of(all, c0 + lane, P);
       const bool in = c0 + lane < P && q.u0 < q.u1 && q.u0 < u1 && q.u1 > u0;
       const unsigned who = __ballot_sync(0xffffffffu, in);

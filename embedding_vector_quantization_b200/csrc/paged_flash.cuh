@@ -16,8 +16,8 @@
 // Roundings: c[idx], Pi, S, rnorm / norm, x_hat, the prepared query (scaled by a power of two below 1) and the weights
 // to f16 (11 bits; outputs have 8 or 11); every sum, maximum and exponent in fp32.
 //
-// Measured at 8 KV heads, 32 query heads, d = 128: a chunk of 1024 tokens over 32768 with signs takes 685 us (expansion 80,
-// flash 550: 1.05 PFLOP/s, 0.64 of what a plain matrix product reaches); four prompts of up to 4096 tokens 376 us (flash 265).
+// Measured at 8 KV heads, 32 query heads, d = 128: a chunk of 1024 tokens over 32768 with signs takes 680 us (expansion 80,
+// flash 550: 1.05 PFLOP/s, 0.64 of what a plain matrix product reaches); four prompts of up to 4096 tokens 362 us (flash 265).
 // The flash kernel is bound by the softmax between its two products: a tile's exponents, scales and conversions occupy the
 // issue slots as long as its contractions the tensor pipe (46 % busy with the triangles' half tiles counted, XU 37 %, ALU 29 %).
 #pragma once
@@ -70,7 +70,7 @@ struct Plan {
 struct FlashArgs {
   const void* q;
   int64_t q_stride;
-  int q_dtype, Hq, Hkv, G, head0, heads;   // this round's KV heads: head0 .. head0 + heads - 1
+  int q_dtype, Hq, Hkv, G, head0, heads;   // the KV heads of this pass: head0 .. head0 + heads - 1
   Batch bt;
   Prep prep;
   Quant kq, vq;

@@ -542,6 +542,23 @@ def test_offsets_past_32_bits(tq):
         assert fk.handle.status() == tq.TQ_OK and torch.equal(*outs) and outs[0].abs().sum() > 0
 
 
+@pytest.mark.parametrize("d,kf,news,lens,causal", [
+    (128, "mse4", [1, 2, 1, 1, 5], [3000, 0, 2500, 0, 1700], False),          # sequences without keys between long ones
+    (128, "prod3", [1, 3, 1], [4000, 2, 1999], True),                         # a row before the first position
+    (64, "mse4", [1, 1, 1, 1] * 16, [20, 0, 33, 0] * 16, False),              # more items than CTAs
+])
+def test_sequences_without_keys_among_others(tq, d, kf, news, lens, causal):
+    """Empty sequences get zeros, whatever their neighbours' parts and the workspace hold."""
+    c = attention_case(tq, d, kf, kf, 6, 2, news, lens, 16, "bf16")
+    fk, fv, bt, kc, vc, kr, vr, q, pr = c
+    size = tq.tq_attn_paged_workspace_bytes(fk.handle.ptr, fv.handle.ptr, bt.struct, 12, 6, kc.struct)
+    ws = torch.full((size,), 68, dtype=torch.uint8, device="cuda")   # finite numbers
+    got = check_case(tq, c, 0.09, causal, 0, H_F16, workspace=ws)
+    for b, L in enumerate(lens):
+        if L == 0:
+            assert not got[sum(news[:b]):sum(news[:b + 1])].any()
+
+
 def test_workspaces_serve_smaller_batches(tq):
     """The size for a batch is enough for every batch with no argument larger."""
     g = np.random.default_rng(0)
