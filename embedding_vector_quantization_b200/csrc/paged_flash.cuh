@@ -1208,7 +1208,9 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
         const float2 sum2 = unpair2(add2(sums[0], sums[1]));
         const float sum = sum2.x + sum2.y;
         etc::tmem_wait_st();
-        l = fmaf(sum, exp2f(-dv), l);
+        // A row that has seen nothing has no weights: its masked scores leave 2^-126 each in a quarter of the exponentials, and a
+        // sum of those is not a sum to divide by.
+        l = fmaf(m == -INFINITY ? 0.f : sum, exp2f(-dv), l);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) bar_arrive(p_full(i));

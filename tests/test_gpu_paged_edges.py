@@ -1,0 +1,73 @@
+"""Paged attention at its edges: rows that see nothing, freed pages, lengths past the table, norms far apart, values and keys that
+are not finite, queries at the ends of their type's range; against 64 bits."""
+
+import numpy as np
+import pytest
+import torch
+
+import paged_util as pu
+from test_gpu_paged import DT, H_F16, H_FP32, attention_case, check_case, fmt, heads, tq  # noqa: F401  (tq: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def h_of(dtype):
+    return H_FP32 if dtype == "fp32" else H_F16
+
+
+def cached(tq, fk, fv, news, lens, page, Hkv, k, v, seed=0):
+    """A batch whose sequences hold the vectors k[b], v[b]: batch, caches and their stored rows."""
+    bt = pu.make_batch(tq, news, lens, page, seed=seed)
+    kc, vc = pu.garbage_cache(tq, fk, bt, Hkv, 1), pu.garbage_cache(tq, fv, bt, Hkv, 2)
+    return bt, kc, vc, pu.fill_cache(kc, fk, bt, k), pu.fill_cache(vc, fv, bt, v)
+
+
+# ------------------------------------------------------------------ rows that see nothing
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("size", [100.0, 1000.0])   # value norms of about 1e3 and 1e4
+@pytest.mark.parametrize("news,lens", [([40], [10]), ([3, 340, 45], [2, 300, 20])])
+def test_rows_before_the_first_position_are_zeros(tq, news, lens, size, dtype):
+    """More new tokens than cached ones: the first see nothing, however large the values that the others see."""
+    fk, fv = fmt(tq, 128, "mse4", 0), fmt(tq, 128, "mse4", 1)
+    k, v = [heads(1 + b, L, 2, 128) for b, L in enumerate(lens)], [size * heads(9 + b, L, 2, 128) for b, L in enumerate(lens)]
+    bt, kc, vc, kr, vr = cached(tq, fk, fv, news, lens, 16, 2, k, v)
+    q = heads(3, bt.ntok, 8, 128, DT[dtype], outliers=False)
+    got = check_case(tq, (fk, fv, bt, kc, vc, kr, vr, q, None), 0.09, True, 0, h_of(dtype))
+    for b, (n, L) in enumerate(zip(news, lens)):
+        t0 = sum(news[:b])
+        assert (got[t0:t0 + max(0, n - L)] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("news", [[1, 2], [60, 1], [340, 50]])
+def test_refused_rotation_positions_are_zeros(tq, news, dtype):
+    """The same for rows without a rotation, among one and several key tiles of large values."""
+    fk, fv = fmt(tq, 128, "mse4", 0), fmt(tq, 128, "prod3", 1)
+    lens = [700, 90]
+    k, v = [heads(1 + b, L, 1, 128) for b, L in enumerate(lens)], [1000 * heads(9 + b, L, 1, 128) for b, L in enumerate(lens)]
+    bt, kc, vc, kr, vr = cached(tq, fk, fv, news, lens, 16, 1, k, v)
+    q = heads(3, bt.ntok, 4, 128, DT[dtype], outliers=False)
+    pos = torch.randint(0, 4096, (bt.ntok,), generator=torch.Generator().manual_seed(3), dtype=torch.int32).cuda()
+    table = pu.rope_table(4096, 128)
+    want = check_case(tq, (fk, fv, bt, kc, vc, kr, vr, q, tq.HeadPrep(cos_sin=table, pos=pos)), 0.09, False, 0, h_of(dtype))
+    bad = torch.arange(bt.ntok, device="cuda") % 3 == 1
+    pos = torch.where(bad, torch.full_like(pos, 4096), pos)
+    got = tq.attn_paged(fk.handle, fv.handle, q, kc, vc, bt, 0.09, causal=False, prep=tq.HeadPrep(cos_sin=table, pos=pos))
+    assert fk.handle.status() == tq.TQ_EINVAL
+    assert (got[bad] == 0).all() and torch.equal(got[~bad], want[~bad])
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+def test_sequences_whose_pages_are_all_bad_are_zeros(tq, dtype):
+    fk, fv = fmt(tq, 128, "mse4", 0), fmt(tq, 128, "mse4", 1)
+    news, lens = [50, 60, 1, 2], [300, 200, 400, 90]
+    k, v = [heads(1 + b, L, 2, 128) for b, L in enumerate(lens)], [1000 * heads(9 + b, L, 2, 128) for b, L in enumerate(lens)]
+    bt, kc, vc, kr, vr = cached(tq, fk, fv, news, lens, 16, 2, k, v)
+    q = heads(3, bt.ntok, 8, 128, DT[dtype], outliers=False)
+    want = check_case(tq, (fk, fv, bt, kc, vc, kr, vr, q, None), 0.09, True, 0, h_of(dtype))
+    t = bt.block_table.clone()
+    t[0], t[2] = -1, bt.num_pages
+    got = tq.attn_paged(fk.handle, fv.handle, q, kc, vc, tq.PagedBatch(bt.q_start, bt.len, t, bt.ntok), 0.09)
+    assert fk.handle.status() == tq.TQ_EINVAL
+    assert (got[:50] == 0).all() and (got[110] == 0).all()
+    assert torch.equal(got[50:110], want[50:110]) and torch.equal(got[111:], want[111:])
