@@ -407,7 +407,7 @@ __device__ __forceinline__ void commit_one(uint32_t leader, uint32_t bar) {
 
 // Where a CTA's walk over (head, key tile) pairs stands; the sequence is looked up only when the tile leaves it.
 struct TileCursor {
-  int h, tile, b, first, last, base, hi;   // tiles [first, last) of sequence b; key 0 of tile `first` is at `base`, keys end at hi
+  int h, tile, b, first, last, base, lo, hi;   // tiles [first, last) of sequence b; key 0 of tile `first` is at `base`, keys are [lo, hi)
 };
 __device__ __forceinline__ void cursor_seek(const FlashArgs& a, int tiles, TileCursor& c, int step) {
   c.tile += step;
@@ -416,9 +416,8 @@ __device__ __forceinline__ void cursor_seek(const FlashArgs& a, int tiles, TileC
   c.b = warp_last_at_or_before(a.p.tile_start, a.bt.B, c.tile);
   c.first = a.p.tile_start[c.b], c.last = a.p.tile_start[c.b + 1];
   const int n = seq_rows(a, c.b);
-  int lo;
-  flash_range(a, c.b, 0, n - 1, n, lo, c.hi);
-  c.base = lo / kKT * kKT;
+  flash_range(a, c.b, 0, n - 1, n, c.lo, c.hi);
+  c.base = c.lo / kKT * kKT;
 }
 
 // Grid: 2 x CTAs; even CTAs keys, odd CTAs values; CTA j of the n of a kind takes pairs [j W / n, (j + 1) W / n) of W.
@@ -480,7 +479,7 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
     // ---- operand rows: thread = token of the tile. Under way at a time: the page of the token after next, the next row.
     const int g = warp >> 2, r = tid & 127;
     float* const top_s = maxima + 8 * g;
-    TileCursor c{(int)(w0 / tiles), (int)(w0 % tiles), 0, 0, 0, 0, 0};
+    TileCursor c{(int)(w0 / tiles), (int)(w0 % tiles), 0, 0, 0, 0, 0, 0};
     // The cursor's token: its page as loaded (nothing waits for it yet), and where in the page.
     struct Spot {
       int page, slot, h, tile;
@@ -489,13 +488,13 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
     auto spot = [&]() -> Spot {
       Spot p;
       const int pos = c.base + (c.tile - c.first) * kKT + r;
-      p.in = pos < c.hi, p.h = c.h, p.tile = c.tile;
+      p.in = pos >= c.lo && pos < c.hi, p.h = c.h, p.tile = c.tile;   // pages behind the window may be someone else's
       const uint32_t pi = (uint32_t)pos / (uint32_t)a.bt.page_size;
       p.slot = pos - (int)pi * a.bt.page_size;
       p.page = p.in ? (int)load_ahead32(a.bt.table + (int64_t)c.b * a.bt.max_pages + pi) : -1;
       return p;
     };
-    auto row_of = [&](const Spot& p) -> int64_t {   // -1: bad page, -2: behind the end
+    auto row_of = [&](const Spot& p) -> int64_t {   // -1: bad page, -2: not among the keys
       if (!p.in) return -2;
       if (p.page < 0 || p.page >= a.bt.num_pages) return -1;
       return ((int64_t)p.page * a.Hkv + a.head0 + p.h) * a.bt.page_size + p.slot;

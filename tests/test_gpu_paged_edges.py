@@ -71,3 +71,26 @@ def test_sequences_whose_pages_are_all_bad_are_zeros(tq, dtype):
     assert fk.handle.status() == tq.TQ_EINVAL
     assert (got[:50] == 0).all() and (got[110] == 0).all()
     assert torch.equal(got[50:110], want[50:110]) and torch.equal(got[111:], want[111:])
+
+
+# ------------------------------------------------------------------ pages behind the window
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("kf,vf", [("mse4", "mse4"), ("prod3", "mse4")])
+@pytest.mark.parametrize("news,lens,window", [([1, 60, 3], [700, 500, 333], 100), ([200], [1000], 16), ([64, 1], [640, 2000], 257)])
+def test_pages_behind_the_window_may_be_freed(tq, news, lens, window, kf, vf, dtype):
+    """Table entries of pages that lie behind the window of a sequence's first new token are not used: -1, or a page that belongs
+    to someone else by now."""
+    fk, fv = fmt(tq, 128, kf, 0), fmt(tq, 128, vf, 1)
+    k, v = [heads(1 + b, L, 2, 128) for b, L in enumerate(lens)], [heads(9 + b, L, 2, 128) for b, L in enumerate(lens)]
+    bt, kc, vc, kr, vr = cached(tq, fk, fv, news, lens, 16, 2, k, v)
+    q = heads(3, bt.ntok, 8, 128, DT[dtype], outliers=False)
+    want = check_case(tq, (fk, fv, bt, kc, vc, kr, vr, q, None), 0.09, True, window, h_of(dtype))
+    spare = next(p for p in range(bt.num_pages) if not (bt.block_table == p).any())
+    for page in (-1, spare):   # the spare pages' norms are NaN
+        for b, (n, L) in enumerate(zip(news, lens)):
+            bt.block_table[b, :(L - n - window + 1) // 16] = page
+        got = tq.attn_paged(fk.handle, fv.handle, q, kc, vc, bt, 0.09, window=window)
+        assert fk.handle.status() == tq.TQ_OK
+        assert torch.equal(got, want)
