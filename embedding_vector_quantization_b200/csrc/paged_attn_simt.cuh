@@ -189,6 +189,9 @@ __global__ void __launch_bounds__(kAttThreads) paged_attn_simt_kernel(AttnArgs a
   __shared__ int64_t at_k[kKeyTile], at_v[kKeyTile];
   __shared__ float ck[16], cv[16], mx[kTileRows], sm[kTileRows], al[kTileRows];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hk = blockIdx.y, split = blockIdx.z;
+  if ((blockIdx.x | blockIdx.y | blockIdx.z) == 0)
+    for (int b = tid; b < a.bt.B; b += kAttThreads)
+      if (seq_cut_short(a.bt, b)) report_error(a.err, kErrPaged);
   const Tile tl = warp_find_tile(a.bt, a.G, kTileRows, blockIdx.x);
   if (tl.b < 0) return;
   const int b = tl.b, tok0 = a.bt.q_start[b], n = a.bt.q_start[b + 1] - tok0;

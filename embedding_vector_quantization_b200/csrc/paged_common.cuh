@@ -57,10 +57,17 @@ __device__ __forceinline__ int warp_find_seq(const Batch& bt, int64_t t) {
   return ended;
 }
 
-// Token rows of sequence b; none if its bounds lie outside the batch's rows.
+// Token rows of sequence b; none if its bounds lie outside the batch's rows or hold more than max_q, which grids and workspaces
+// are made for.
 __device__ __forceinline__ int seq_tokens(const Batch& bt, int b) {
   const int lo = bt.q_start[b], hi = bt.q_start[b + 1];
-  return lo >= 0 && hi > lo && hi <= bt.ntok ? hi - lo : 0;
+  return lo >= 0 && hi > lo && hi <= bt.ntok && hi - lo <= bt.max_q ? hi - lo : 0;
+}
+
+// Whether attention leaves sequence b out for such bounds, or some of its keys because the table is too narrow for its length.
+__device__ __forceinline__ bool seq_cut_short(const Batch& bt, int b) {
+  const int lo = bt.q_start[b], hi = bt.q_start[b + 1];
+  return hi != lo && (seq_tokens(bt, b) == 0 || bt.len[b] > (int64_t)bt.max_pages * bt.page_size);
 }
 
 // Token and head of row `row` = token * H + head (a 64-bit quotient only where 32 bits do not do).

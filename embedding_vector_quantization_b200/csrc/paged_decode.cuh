@@ -102,6 +102,7 @@ __device__ __forceinline__ int chunk_sums(const AttnArgs& a, int64_t* pre, int64
       int first;
       n = small_tokens(a, b);
       nch = small_chunks(a, b, n, first);
+      if (blockIdx.x == 0 && seq_cut_short(a.bt, b)) report_error(a.err, kErrPaged);
     }
     const int64_t v = (int64_t)nch * (a.Hkv * eights(a, n));
     int64_t incl = v;

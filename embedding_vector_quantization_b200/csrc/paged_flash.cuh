@@ -153,6 +153,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(FlashArgs a) {
     int nt = 0, ni = 0;
     if (b < a.bt.B) {
       const int n = seq_rows(a, b);
+      if (seq_cut_short(a.bt, b)) report_error(a.err, kErrPaged);
       if (n > 0) {
         int lo, hi;
         flash_range(a, b, 0, n - 1, n, lo, hi);

@@ -1860,7 +1860,7 @@ int tq_last_status(const tq_handle* h, void* stream) {
   if (word & tqk::kErrInternal) return fail(TQ_ECUDA, "a kernel found its shared memory misaligned");
   if (word & tqk::kErrBounds) return fail(TQ_EINVAL, "a length len[b] outside 0 .. L_cap (found by TQ_CHECK=1)");
   if (word & tqk::kErrPaged)
-    return fail(TQ_EINVAL, "a paged batch named a page, a position or a rotation position out of range (its rows were skipped)");
+    return fail(TQ_EINVAL, "a paged batch named a page, a position, a rotation position or token rows out of range (those were skipped)");
   if (word & tqk::kErrTimeout) return fail(TQ_ETIMEOUT, "a bounded device wait timed out");
   if (word & tqk::kErrCapacity) return fail(TQ_ECAPACITY, "append skipped a full sequence (len == L_cap)");
   return ok();

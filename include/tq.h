@@ -308,7 +308,8 @@ typedef struct tq_paged_cache {
 typedef struct tq_paged_batch {
   const int32_t* q_start;     /* device [B + 1], ascending from q_start[0] >= 0  */
   const int32_t* len;         /* device [B]                                      */
-  const int32_t* block_table; /* device [B][max_pages]; entries past a sequence's pages are not read */
+  const int32_t* block_table; /* device [B][max_pages]; entries past a sequence's pages, and
+                               * tq_attn_paged's behind the window of its first token, are not read */
   int32_t B, max_pages;
   int64_t ntok;               /* token rows of the arrays (>= q_start[B])        */
   int32_t max_q;              /* no sequence has more token rows than this       */
@@ -363,8 +364,9 @@ size_t tq_attn_paged_workspace_bytes(const tq_handle* hk, const tq_handle* hv, c
  *  out         device [ntok][Hq][d] of q_dtype, contiguous, 16-byte aligned
  *  workspace   device scratch, 16-byte aligned; calls that overlap need one each
  * A query that sees no key (len[b] == 0, or a position < 0) gets zeros, as does one whose rotation position is out
- * of range (recorded as above); keys on a page out of range are not seen (recorded). Padding rows of out keep what
- * they held. Arithmetic: fp32 queries in fp32 throughout; 16-bit queries with f16 operands on the tensor cores where
+ * of range (recorded as above); keys on a page out of range, or at positions behind the block table's last column, are
+ * not seen (recorded). A sequence whose token rows leave 0 .. ntok - 1, descend or are more than max_q is left out
+ * (recorded): its rows of out, like those of padding, keep what they held. Arithmetic: fp32 queries in fp32 throughout; 16-bit queries with f16 operands on the tensor cores where
  * the formats allow (d 64 or 128, m 0 or d), sums and softmax statistics in fp32. */
 int tq_attn_paged(const tq_handle* hk, const tq_handle* hv, const void* q, int q_dtype, int64_t q_stride, int Hq,
                   int Hkv, const tq_paged_batch* batch, const tq_head_prep* prep, const tq_paged_cache* k,

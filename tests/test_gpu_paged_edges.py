@@ -94,3 +94,67 @@ def test_pages_behind_the_window_may_be_freed(tq, news, lens, window, kf, vf, dt
         got = tq.attn_paged(fk.handle, fv.handle, q, kc, vc, bt, 0.09, window=window)
         assert fk.handle.status() == tq.TQ_OK
         assert torch.equal(got, want)
+
+
+# ------------------------------------------------------------------ lengths and bounds that are not what they say
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("news", [[1, 2, 1], [50, 40, 1], [50, 60, 70]])
+@pytest.mark.parametrize("which", [0, 2])
+def test_lengths_past_the_table_are_recorded(tq, which, news, dtype):
+    """What the table has of the sequence is seen, the call is recorded; the others stay as they are."""
+    lens = [160, 130, 158]
+    c = attention_case(tq, 128, "mse4", "mse4", 2, 4, news, lens, 16, dtype)
+    fk, fv, bt, kc, vc, kr, vr, q, pr = c
+    full = bt.len.clone()
+    full[which] = 160                       # all slots of its pages: the reference's rows are those up to its length
+    for t in (kc.norms, vc.norms):
+        t.nan_to_num_(nan=1.0)
+    for causal in (False, True):
+        # causal: every token of the long sequence stands behind the table's end, and sees all of it
+        want = tq.attn_paged(fk.handle, fv.handle, q, kc, vc, tq.PagedBatch(bt.q_start, full, bt.block_table, bt.ntok), 0.09, causal=False)
+        others = tq.attn_paged(fk.handle, fv.handle, q, kc, vc, bt, 0.09, causal=causal)
+        assert fk.handle.status() == tq.TQ_OK
+        over = full.clone()
+        over[which] = 160 + 200
+        got = tq.attn_paged(fk.handle, fv.handle, q, kc, vc, tq.PagedBatch(bt.q_start, over, bt.block_table, bt.ntok), 0.09, causal=causal)
+        assert fk.handle.status() == tq.TQ_EINVAL and fk.handle.status() == tq.TQ_OK
+        mine = torch.zeros(bt.ntok, dtype=torch.bool, device="cuda")
+        mine[sum(news[:which]):sum(news[:which + 1])] = True
+        assert torch.equal(got[mine], want[mine]) and torch.equal(got[~mine], others[~mine])
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("news", [[1, 1, 1], [2, 3, 1], [40, 1, 30], [1, 50, 2]])
+def test_bad_bounds_are_recorded_and_their_rows_kept(tq, news, dtype):
+    """Sequences whose rows leave the batch's, descend, or are more than max_q: recorded, their rows of out as they were."""
+    c = attention_case(tq, 128, "mse4", "mse4", 2, 4, news, [100, 60, 90], 16, dtype)
+    fk, fv, bt, kc, vc, kr, vr, q, pr = c
+    n0, N = news[0], bt.ntok
+
+    def run(start, max_q=None):
+        out = torch.full_like(q, 3.0)
+        b = tq.PagedBatch(torch.tensor(start, dtype=torch.int32).cuda(), bt.len, bt.block_table, N, max_q)
+        tq.attn_paged(fk.handle, fv.handle, q, kc, vc, b, 0.09, out=out)
+        return out
+
+    for start, good, used in (([0, n0, n0, N + 7], [0, n0, n0, n0], n0), ([0, n0, N + 1, 2 ** 31 - 1], [0, n0, n0, n0], n0),
+                              ([-5, 0, n0 + 1, n0], [0, 0, n0 + 1, n0 + 1], n0 + 1), ([-2 ** 31, 0, n0 + 1, n0 - 1], [0, 0, n0 + 1, n0 + 1], n0 + 1)):
+        want = run(good)
+        assert fk.handle.status() == tq.TQ_OK and (want[used:] == 3.0).all() and not (want[:used] == 3.0).all()
+        got = run(start)
+        assert fk.handle.status() == tq.TQ_EINVAL and fk.handle.status() == tq.TQ_OK
+        assert torch.equal(got, want)
+    starts = bt.q_start.tolist()
+    want = run(starts)
+    for b, n in enumerate(news):
+        if n != max(news) or news.count(n) > 1 or n == 1:
+            continue
+        got = run(starts, n - 1)
+        assert fk.handle.status() == tq.TQ_EINVAL
+        rows = torch.arange(N, device="cuda")
+        mine = (rows >= starts[b]) & (rows < starts[b + 1])
+        assert (got[mine] == 3.0).all()
+        room = torch.finfo(q.dtype).eps * 4 * want.abs().amax()   # other splits of the keys: the same sums in another order
+        assert ((got - want)[~mine].abs() <= room).all()
