@@ -259,8 +259,16 @@ __global__ void __launch_bounds__(kAttThreads) paged_attn_simt_kernel(AttnArgs a
         for (int r = 0; r < kTileRows; ++r) acc[c * kTileRows + r] *= al[r];
         for (int t = 0; t < kKeyTile; ++t) {
           const float v = kv[t * ld + j];
+          if (fabsf(v) < INFINITY) {
 #pragma unroll
-          for (int r = 0; r < kTileRows; ++r) acc[c * kTileRows + r] = fmaf(sc[r * kKeyTile + t], v, acc[c * kTileRows + r]);
+            for (int r = 0; r < kTileRows; ++r) acc[c * kTileRows + r] = fmaf(sc[r * kKeyTile + t], v, acc[c * kTileRows + r]);
+          } else {   // a row that does not see it has weight 0, and 0 times infinity is not 0
+#pragma unroll
+            for (int r = 0; r < kTileRows; ++r) {
+              const float p = sc[r * kKeyTile + t];
+              if (p != 0.f) acc[c * kTileRows + r] = fmaf(p, v, acc[c * kTileRows + r]);
+            }
+          }
         }
       }
     }

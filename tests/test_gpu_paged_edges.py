@@ -158,3 +158,37 @@ def test_bad_bounds_are_recorded_and_their_rows_kept(tq, news, dtype):
         assert (got[mine] == 3.0).all()
         room = torch.finfo(q.dtype).eps * 4 * want.abs().amax()   # other splits of the keys: the same sums in another order
         assert ((got - want)[~mine].abs() <= room).all()
+
+
+# ------------------------------------------------------------------ norms far apart
+
+
+@pytest.mark.parametrize("dtype", ["fp32"])
+@pytest.mark.parametrize("what", [float("inf"), float("nan")])
+@pytest.mark.parametrize("kf,vf", [("mse4", "mse4"), ("prod3", "prod3"), ("mse3", "qjl")])
+@pytest.mark.parametrize("news,lens,window", [([5], [40], 0), ([3, 1], [200, 17], 20), ([60, 70], [90, 300], 0), ([80], [400], 50)])
+def test_rows_that_are_not_finite_and_not_seen(tq, news, lens, window, kf, vf, what, dtype):
+    """The newest key and value, and (with a window) one just behind the window of the later tokens, have a norm of infinity or
+    NaN: the rows that do not see them are as if they were not there."""
+    fk, fv = fmt(tq, 128, kf, 0), fmt(tq, 128, vf, 1)
+    k, v = [heads(1 + b, L, 2, 128) for b, L in enumerate(lens)], [heads(9 + b, L, 2, 128) for b, L in enumerate(lens)]
+    bt, kc, vc, kr, vr = cached(tq, fk, fv, news, lens, 16, 2, k, v)
+    q = heads(3, bt.ntok, 4, 128, DT[dtype], outliers=False)
+    want = check_case(tq, (fk, fv, bt, kc, vc, kr, vr, q, None), 0.09, True, window, h_of(dtype))
+    ref, tol = pu.attention_ref(bt, q, fk, fv, kr, vr, 0.09, True, window, None, h_of(dtype))
+    keep = torch.ones(bt.ntok, dtype=torch.bool, device="cuda")
+    for b, (n, L) in enumerate(zip(news, lens)):
+        t0 = sum(news[:b])
+        for p in [L - 1] + ([L - n - window + 1] if window and L - n - window + 1 >= 0 else []):
+            page, slot = pu.slots(bt, b, p, p + 1)
+            for c in (kc, vc):
+                c.norms[page, :, slot] = what
+                if c.rnorms is not None:
+                    c.rnorms[page, :, slot] = what
+            for i in range(n):
+                pos = L - n + i
+                if p <= pos and not (window and p <= pos - window):
+                    keep[t0 + i] = False
+    got = tq.attn_paged(fk.handle, fv.handle, q, kc, vc, bt, 0.09, window=window)
+    assert got[keep].isfinite().all()
+    pu.check_attention(got[keep], ref[keep], tol[keep], q.dtype)
