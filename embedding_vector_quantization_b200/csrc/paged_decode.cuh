@@ -15,8 +15,9 @@
 // coordinates of one token, which a table turns out of one packed byte (a copy of the table for each bank, so that no two
 // lanes meet). Coordinates are numbered so that a lane's share of a token's row is contiguous. The value product has
 // coordinates as rows and tokens as its inner dimension: two tokens' table entries, interleaved; its weights are the scores'
-// registers, transposed across the warp (movmatrix). Weights carry the value norms (times a power of two that keeps them
-// below 2^12), the sums stay in the codes' domain and the merge rotates them back.
+// registers, transposed across the warp (movmatrix). Weights carry the value norms, and each query row its own power of two
+// that keeps its largest product of the two between 2^-13 and 2^12: norms of tokens that the row does not see, or hardly, cost
+// it no digits. The sums stay in the codes' domain and the merge rotates them back.
 //
 // Work is cut evenly: CTA c of P takes units [c U / P, (c + 1) U / P) of the batch's U chunks (sequence by sequence, head by
 // head), whatever the sequences' lengths; a CTA's part of one (sequence, head) is one partial result.
@@ -480,8 +481,7 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
 #pragma unroll
       for (int j = 0; j < 4; ++j) os[x][j] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    int ve = 0;           // value norms are taken times 2^-ve
-    float vdn = 0.f;      // 2^-ve; 0: no value yet
+    float sv[2] = {0.f, 0.f};   // what weight times value norm is multiplied by, a power of two; 0: no value yet
 
     uint32_t use = 0;         // the offset of the stage in use
     auto next = [](uint32_t at) -> uint32_t { return at + L::kStage == L::kWarpRing ? 0 : at + L::kStage; };
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
         }
         float vA = norm_at(L::kNormV, tk), vB = norm_at(L::kNormV, tk + 8), wA = 0.f, wB = 0.f;
         if (SG) wA = lds_half(st + L::kNormV + 64 + 2 * tk), wB = lds_half(st + L::kNormV + 64 + 2 * (tk + 8));
-        if (!here || key0 < lo_w || key0 + kChunk > hi_w) {   // some row does not see all of the chunk
+        if (!here || key0 < lo_w || key0 + kChunk > hi_w) {
           const int kA = key0 + tk, kB = kA + 8;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
@@ -562,6 +562,17 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
           // a token behind the sequence's end counts for nothing, whatever its slot holds
           if (!here || kA >= hi_all) vA = wA = 0.f;
           if (!here || kB >= hi_all) vB = wB = 0.f;
+          // One that is not finite makes the rows that see it NaN by their scores: weight 0 times it would not be 0 for the others.
+          const bool okA = fabsf(vA) + fabsf(wA) < INFINITY, okB = fabsf(vB) + fabsf(wB) < INFINITY;
+          if (!okA || !okB) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              if (!okA && kA >= lo[j] && kA < hi[j]) x[j] = NAN;
+              if (!okB && kB >= lo[j] && kB < hi[j]) x[2 + j] = NAN;
+            }
+            if (!okA) vA = wA = 0.f;
+            if (!okB) vB = wB = 0.f;
+          }
         }
         vn[c][0] = vA, vn[c][1] = vB, wn[c][0] = wA, wn[c][1] = wB;
       }
@@ -570,35 +581,41 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
         vt = fmaxf(vt, fmaxf(vn[CN - 1][0], vn[CN - 1][1]));
         tops[0] = fmaxf(tops[0], fmaxf(xs[CN - 1][0], xs[CN - 1][2])), tops[1] = fmaxf(tops[1], fmaxf(xs[CN - 1][1], xs[CN - 1][3]));
       }
-      const bool up0 = tops[0] > m[0] + 8.f || tops[1] > m[1] + 8.f || vt * vdn > 16.f || vdn == 0.f;
-      if (__any_sync(0xffffffffu, up0)) {   // rarely: a reference moves
+      auto of_all = [](float x) -> float {   // the largest of a query row's eight lanes
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+        return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+      };
+      // Rarely: the reference of the weights moves, or the unit of the sums may have to (weights are below 2^8).
+      if (__any_sync(0xffffffffu, tops[0] > m[0] + 8.f || tops[1] > m[1] + 8.f || vt * fmaxf(sv[0], sv[1]) > 16.f)) {
         float f[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float top = tops[j];
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-          f[j] = 1.f;
-          if (top > m[j]) f[j] = m[j] == -INFINITY ? 0.f : ex2(m[j] - top), m[j] = top;
-          l[j] *= f[j];
-        }
-        float vm = vt < INFINITY ? vt : 0.f;
-        for (int o = 16; o; o >>= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
-        if (vdn == 0.f || vm * vdn > 16.f) {
-          int e = -126;
-          if (vm > 0.f) frexpf(vm, &e);
-          e = max(-126, min(126, e));
-          if (vdn != 0.f) {
-            const float fv = ex2((float)max(ve - e, -126));
-            f[0] *= fv, f[1] *= fv;
-          }
-          ve = e, vdn = ldexpf(1.f, -e);
-        }
+          const float top = of_all(tops[j]), old = m[j];
+          float back = 1.f;   // 2^(the old reference - the new)
+          if (top > old) back = old == -INFINITY ? 0.f : ex2(old - top), m[j] = top;
+          l[j] *= back;
+          const float ref = m[j] == -INFINITY ? 0.f : m[j];
+          float z = 0.f;
 #pragma unroll
-        for (int y = 0; y < KS; ++y) {
-          oc[y][0] *= f[0], oc[y][1] *= f[1], oc[y][2] *= f[0], oc[y][3] *= f[1];
-          if (SG) os[y][0] *= f[0], os[y][1] *= f[1], os[y][2] *= f[0], os[y][3] *= f[1];
+          for (int c = 0; c < CN; ++c)
+            z = fmaxf(z, fmaxf(ex2(xs[c][j] - ref) * vn[c][0], ex2(xs[c][2 + j] - ref) * vn[c][1]));
+          z = of_all(z);
+          f[j] = 1.f;
+          if (m[j] > old || z * sv[j] > 4096.f) {   // the largest product to about one
+            int e = -100;
+            if (z > 0.f && z < INFINITY) frexpf(z, &e);
+            float now = z < INFINITY ? ldexpf(1.f, -max(-100, min(126, e))) : 0.f;
+            if (sv[j] > 0.f) now = fminf(now, sv[j] * 1.1529215e18f);   // 2^60: the sums stay finite
+            f[j] = sv[j] > 0.f ? now / sv[j] * back : 0.f, sv[j] = now;
+          }
+        }
+        if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+#pragma unroll
+          for (int y = 0; y < KS; ++y) {
+            oc[y][0] *= f[0], oc[y][1] *= f[1], oc[y][2] *= f[0], oc[y][3] *= f[1];
+            if (SG) os[y][0] *= f[0], os[y][1] *= f[1], os[y][2] *= f[0], os[y][3] *= f[1];
+          }
         }
       }
       const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
@@ -610,8 +627,9 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
         for (int j = 0; j < 2; ++j) {
           x[j] = ex2(x[j] - ref[j]), x[2 + j] = ex2(x[2 + j] - ref[j]);
           l[j] += x[j] + x[2 + j];
+          x[j] *= sv[j], x[2 + j] *= sv[j];
         }
-        const float vA = vn[c][0] * vdn, vB = vn[c][1] * vdn;
+        const float vA = vn[c][0], vB = vn[c][1];
         const uint32_t b0 = movmatrix(half2_bits(x[0] * vA, x[1] * vA)), b1 = movmatrix(half2_bits(x[2] * vB, x[3] * vB));
         // ---- values: lane (g, t) holds coordinates g D/8 .. of tokens t, t + 4, t + 8, t + 12
         {
@@ -647,7 +665,7 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
             }
           }
           if (SG) {   // lane (g, t): signs of projections g D/8 .. of its four tokens; two tokens in one word
-            const float wA = wn[c][0] * vdn, wB = wn[c][1] * vdn;
+            const float wA = wn[c][0], wB = wn[c][1];
             const uint32_t r0 = movmatrix(half2_bits(x[0] * wA, x[1] * wA)), r1 = movmatrix(half2_bits(x[2] * wB, x[3] * wB));
             uint32_t sg[4];
 #pragma unroll
@@ -685,13 +703,12 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
     __syncthreads();   // every warp is done with the ring
     float top[2];
     {
-      const float upv = vdn == 0.f ? 0.f : ex2((float)ve);
       float f[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         top[j] = -INFINITY;
         for (int w = 0; w < kDcWarps; ++w) top[j] = fmaxf(top[j], stat[w * 8 + 2 * t + j]);
-        f[j] = m[j] == -INFINITY ? 0.f : ex2(m[j] - top[j]) * upv;
+        f[j] = m[j] == -INFINITY || sv[j] == 0.f ? 0.f : ex2(m[j] - top[j]) / sv[j];
       }
       // sums [warp][coordinate][row]
       float* o = reinterpret_cast<float*>(smem_dc + ring_off);
