@@ -5,8 +5,10 @@
 //   plan    one CTA lists the sequences that come here (more than `small_rows` query rows), their key tiles of 128 tokens
 //           and their items of 256 query rows, with the running sum of the items' key tiles;
 //   expand  key tiles -> f16 rows x_hat = Pi^T c[idx] + rnorm / norm * sqrt(pi/2) / m S^T (2 sigma - 1), as a
-//           128 x d x (d + m) contraction per tile on the tensor cores, times norm 2^-E with 2^E >= every norm of the tile,
-//           so that f16 holds any norm; stored as the very shared-memory images the attention wants, 32 KB a tile;
+//           128 x d x (d + m) contraction per tile on the tensor cores; stored as the very shared-memory images the attention
+//           wants, 32 KB a tile. Norms: a tile whose norms lie within 2^8 of each other has its rows times norm 2^-E, with
+//           2^E >= every norm of it, which costs f16 nothing; any other tile ("apart") keeps rows of length about one, and the
+//           attention multiplies scores and weights by the norms of its 128 tokens;
 //   flash   softmax(scale q k^T) v over those tiles with the running maximum and sum of each row;
 //   merge   items that several CTAs shared.
 // Keys and values come back in the original basis, so queries and outputs need no rotation, and signs cost no wider
@@ -48,6 +50,7 @@ using etc::wait_bar;
 constexpr int kKT = 128;          // tokens of a key tile
 constexpr int kItemRows = 256;    // query rows of an item: two tiles of 128
 constexpr int kItemCost = 3;      // an item's fixed cost in key tiles (query preparation, epilogue)
+constexpr int kApart = 1 << 20;   // in place of an exponent: the tile's norms are apart from its rows
 constexpr uint32_t kAtomRows = 128 * 128;   // 128 rows of 64 f16: one swizzle atom column
 
 // Plan, in the workspace (ints): what plan_kernel writes.
@@ -56,14 +59,16 @@ struct Plan {
   int* tile_start;   // [B + 1] first key tile of a sequence
   int* item_start;   // [B + 1] first item of a sequence
   int* unit;         // [items + 1] running sum of the items' costs, within one head
-  int* ke;           // [heads of a round][max_tiles] exponents of key tiles
+  int* ke;           // [heads of a round][max_tiles] exponents of key tiles, or kApart
   int* ve;           // ... of value tiles
+  float* kn;         // [heads of a round][max_tiles][128] norms of the key tiles that are kApart
+  float* vn;         // ... of the value tiles
   uint32_t* seen;    // [max_tiles][4] tokens of the tile that exist and lie on a valid page
   uint8_t* krows;    // [heads of a round][max_tiles] f16 key tiles
   uint8_t* vrows;
   uint8_t* qrows;    // [heads of a round][max_items][2] f16 query tiles
   float* qfactor;    // [heads of a round][max_items][256] what a row's scores are multiplied by (log2), -1: it sees nothing
-  float* part;       // [2 * CTAs][256 rows][d + 2] results of cut items
+  float* part;       // [2 * CTAs][d / 4 + 1][256 rows] float4: results of cut items
   int max_tiles, max_items;
 };
 
@@ -220,8 +225,8 @@ struct ExLayout {
   static constexpr uint32_t kLut = kA + kABytes;                        // 32 KB
   static constexpr uint32_t kScale = kLut + 32768;                      // float [4][128]
   static constexpr uint32_t kBars = kScale + 2048;                      // op_full, a_full[4], a_empty[4], d_full[4], d_empty[4]
-  static constexpr uint32_t kMisc = kBars + 17 * 8;                     // tmem slot, abort, maxima[2 groups][2][4]
-  static constexpr uint32_t kBytes = kMisc + 8 + 64;
+  static constexpr uint32_t kMisc = kBars + 17 * 8;                     // tmem slot, abort, extremes[2 groups][2][8]
+  static constexpr uint32_t kBytes = kMisc + 8 + 128;
 };
 static_assert(ExLayout<128>::kBytes <= 232448, "expand layout exceeds the shared memory of one CTA");
 
@@ -442,7 +447,7 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
   const uint32_t stage_bytes = L::kABytes / NS;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
-  float* maxima = reinterpret_cast<float*>(smem + L::kMisc + 8);   // [4]
+  uint32_t* extremes = reinterpret_cast<uint32_t*>(smem + L::kMisc + 8);
   float* scale_s = reinterpret_cast<float*>(smem + L::kScale);
   if ((base & 1023u) != 0) {
     if (tid == 0) report_error(a.err, kErrInternal);
@@ -479,7 +484,7 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
   if (warp < 8) {
     // ---- operand rows: thread = token of the tile. Under way at a time: the page of the token after next, the next row.
     const int g = warp >> 2, r = tid & 127;
-    float* const top_s = maxima + 8 * g;
+    uint32_t* const extremes_g = extremes + 16 * g;
     TileCursor c{(int)(w0 / tiles), (int)(w0 % tiles), 0, 0, 0, 0, 0, 0};
     // The cursor's token: its page as loaded (nothing waits for it yet), and where in the page.
     struct Spot {
@@ -527,23 +532,34 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
         cursor_seek(a, tiles, c, 2);
         s1 = spot();
       }
-      const float norm = Q.norm_dtype == TQ_F16 ? __half2float(__ushort_as_half((uint16_t)cur.norm)) : __uint_as_float(cur.norm);
+      float norm = Q.norm_dtype == TQ_F16 ? __half2float(__ushort_as_half((uint16_t)cur.norm)) : __uint_as_float(cur.norm);
       if (here == -1) report_error(a.err, kErrPaged);
       const unsigned there = __ballot_sync(0xffffffffu, cur.ok);
       if (kind == 0 && h == 0 && lane == 0) a.p.seen[4 * tile + (warp & 3)] = there;
-      // the tile's exponent: 2^E >= every finite norm
-      float top = fabsf(norm) < INFINITY ? fabsf(norm) : 0.f;
-      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      float* const mt = top_s + (i & 2) * 2;   // two sets in turn: one barrier a tile is enough
-      if (lane == 0) mt[warp & 3] = top;
+      float ratio = 1.f;   // of the residual norm to the norm
+      if (Q.m > 0 && Q.bits > 0) {
+        ratio = norm != 0.f ? __half2float(__ushort_as_half(cur.rnorm)) / norm : 0.f;
+        if (!(fabsf(ratio) <= 65504.f)) {   // the row stays finite, its norm tells that it is not
+          ratio = 0.f;
+          if (fabsf(norm) < INFINITY) norm = NAN;
+        }
+      }
+      // the tile's largest and smallest norm other than 0: as bits, which are ordered like them (NaN above all)
+      const uint32_t bits = cur.ok ? __float_as_uint(norm) & 0x7fffffffu : 0u;
+      const uint32_t top_w = __reduce_max_sync(0xffffffffu, bits), low_w = __reduce_min_sync(0xffffffffu, bits ? bits : 0xffffffffu);
+      uint32_t* const ext = extremes_g + (i & 2) * 4;   // two sets in turn: one barrier a tile is enough
+      if (lane == 0) ext[warp & 3] = top_w, ext[4 + (warp & 3)] = low_w;
       named_sync(1 + g, 128);
-      top = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
+      const uint32_t top = max(max(ext[0], ext[1]), max(ext[2], ext[3])), low = min(min(ext[4], ext[5]), min(ext[6], ext[7]));
+      // Above a quotient of 2^8 the smallest rows would lose digits to f16's least exponent, which norms apart cost none.
+      const bool apart = top >= 0x7f800000u || (top > 0 && top - low > 8u << 23);
       int e = -126;
-      if (top > 0.f) frexpf(top, &e);
+      if (top > 0) frexpf(__uint_as_float(top), &e);
       e = max(-126, min(126, e));
       if (i >= NS) wait(a_empty(s), (i / NS - 1) & 1);
-      scale_s[s * 128 + r] = cur.ok ? ldexpf(norm, -e) : 0.f;
-      if (r == 0) (kind ? a.p.ve : a.p.ke)[(int64_t)h * a.p.max_tiles + tile] = e;
+      scale_s[s * 128 + r] = !cur.ok ? 0.f : apart ? 1.f : ldexpf(norm, -e);
+      if (r == 0) (kind ? a.p.ve : a.p.ke)[(int64_t)h * a.p.max_tiles + tile] = apart ? kApart : e;
+      if (apart) (kind ? a.p.vn : a.p.kn)[((int64_t)h * a.p.max_tiles + tile) * kKT + r] = cur.ok ? norm : 0.f;
       const uint32_t row = base + L::kA + s * stage_bytes + r * 128;
       if (Q.bits > 0) {
 #pragma unroll
@@ -556,7 +572,6 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
         for (int ch = 0; ch < D / 8; ++ch) sts128(row + (ch >> 3) * kAtomRows + (((ch & 7) ^ (r & 7)) << 4), 0, 0, 0, 0);
       }
       if (Q.m > 0) {
-        const float ratio = Q.bits == 0 ? 1.f : norm != 0.f ? __half2float(__ushort_as_half(cur.rnorm)) / norm : 0.f;   // relative to the norm
         const uint32_t r2 = half2_bits(ratio, ratio);
 #pragma unroll
         for (int ch = 0; ch < D / 8; ++ch) {
@@ -787,8 +802,8 @@ struct FlLayout {
   static constexpr uint32_t kBars = kRing + kFlStages * kTile;
   // full[4], empty[4], q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], o_free[2]
   static constexpr int kNumBars = 2 * kFlStages + 12;
-  static constexpr uint32_t kRow = kBars + 8 * kNumBars;     // float [2][256]: what the two threads of a row tell each other
-  static constexpr uint32_t kMisc = kRow + 2048;
+  static constexpr uint32_t kRow = kBars + 8 * kNumBars;     // float2 [2][256]: what the two threads of a row tell each other
+  static constexpr uint32_t kMisc = kRow + 4096;
   static constexpr uint32_t kBytes = kMisc + 16;
 };
 static_assert(FlLayout<128>::kBytes <= 232448, "flash layout exceeds the shared memory of one CTA");
@@ -892,6 +907,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float r;
+  asm("lg2.approx.f32 %0, %1;\n" : "=f"(r) : "f"(x));
   return r;
 }
 // 2^x for two values on the fused multiply-add pipe (the exponential unit alone would bind the kernel: 16 results a cycle
@@ -1075,8 +1095,8 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n");
     // ---- softmax: thread = half a query row
     const int i = warp >> 3, half = (warp >> 2) & 1, r = tid & 127;
-    float* const mine = reinterpret_cast<float*>(smem + L::kRow) + 256 * i + 128 * half + r;
-    const float* const theirs = reinterpret_cast<float*>(smem + L::kRow) + 256 * i + 128 * (half ^ 1) + r;
+    float2* const mine = reinterpret_cast<float2*>(smem + L::kRow) + 256 * i + 128 * half + r;
+    const float2* const theirs = reinterpret_cast<float2*>(smem + L::kRow) + 256 * i + 128 * (half ^ 1) + r;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t cs = col_s[i] + lanes, co = col_o[i] + lanes + half * (D / 2);   // scores; this thread's value sums
     int tile = 0;   // tiles of this CTA so far
@@ -1114,18 +1134,16 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
       int lo_all, hi_all;
       flash_range(a, s.b, 0, s.n - 1, s.n, lo_all, hi_all);
       const int key_first = (lo_all / kKT + s.lo_tile) * kKT;
-      float m = -INFINITY, l = 0.f;   // running reference (log2) and sum of weights
-      int vref = 0;                   // the value sums are in units of 2^vref
+      // Running reference (log2) and sum of the weights. The value sums have a unit of their own, 2^(m + b), which follows what the
+      // row's weights and the value tiles' exponents make together: a large value that the row hardly sees costs it nothing.
+      // m and b are whole numbers, and what is formed of them stays exact.
+      float m = -INFINITY, l = 0.f, b = -INFINITY;
       int ke = a.p.ke[te + s.t0], ve = a.p.ve[te + s.t0];
       uint4 seen = *reinterpret_cast<const uint4*>(a.p.seen + 4 * (tile0 + s.t0));
       for (int j = s.t0; j < s.t1; ++j, ++tile) {
-        const float c = fmaxf(qscale * exp2f((float)ke), 1e-37f);   // above 0: c times the mask's -infinity stays -infinity
-        // value tiles come in units of 2^ve: their weights take the difference along. The unit moves up when a tile would
-        // bring weights above 2^(8 + 4); a tile 2^100 below it keeps its place in the sum of weights and adds nothing.
-        const int vnow = j == s.t0 || ve > vref + 4 ? ve : vref;
-        const float fv = exp2f((float)max(j == s.t0 ? 0 : vref - vnow, -126));
-        vref = vnow;
-        const float dv = (float)max(ve - vref, -100);
+        const int ke_now = ke, ve_now = ve;
+        // above 0: c times the mask's -infinity stays -infinity
+        const float c = fmaxf(ke_now == kApart ? qscale : qscale * exp2f((float)ke_now), 1e-37f);
         const uint4 seen_now = seen;
         if (j + 1 < s.t1) {
           ke = a.p.ke[te + j + 1], ve = a.p.ve[te + j + 1];
@@ -1142,6 +1160,16 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
         for (int q4 = 0; q4 < 2; ++q4) tmem_ld32(cs + 64 * half, v[q4], 32 * q4);
 #pragma unroll
         for (int q4 = 0; q4 < 2; ++q4) tmem_wait_ld(v[q4]);
+        if (ke_now == kApart) {
+          const float4* n = reinterpret_cast<const float4*>(a.p.kn + (te + j) * kKT + 64 * half);
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            const float4 w = n[x];
+            uint32_t* y = &v[x >> 3][4 * (x & 7)];
+            y[0] = __float_as_uint(__uint_as_float(y[0]) * w.x), y[1] = __float_as_uint(__uint_as_float(y[1]) * w.y);
+            y[2] = __float_as_uint(__uint_as_float(y[2]) * w.z), y[3] = __float_as_uint(__uint_as_float(y[3]) * w.w);
+          }
+        }
         if (masked) {
 #pragma unroll
           for (int q4 = 0; q4 < 2; ++q4) {
@@ -1161,18 +1189,46 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
           for (int x = 1; x < 15; x += 2) mx4[q] = fmaxf(mx4[q], fmaxf(__uint_as_float(w[x0 + x]), __uint_as_float(w[x0 + x + 1])));
           mx4[q] = fmaxf(mx4[q], __uint_as_float(w[x0 + 15]));
         }
-        float top = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;
-        // The reference moves only when a score exceeds it by 2^8: weights stay below 256, and the sums are rarely scaled.
-        // All threads of the tile learn here whether any row moves; from here on no score is needed in tensor memory.
-        if (bar_any(1 + i, 256, top > m + 8.f || fv != 1.f)) {
-          *mine = top;
+        const float top = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c, top_ref = top == -INFINITY ? 0.f : top;
+        const bool v_apart = ve_now == kApart;
+        float top_o = (float)ve_now, sum = 0.f;   // the largest weight times value norm, log2, relative to the largest weight
+        if (v_apart) {   // from here on scores are relative to this half's largest and have their value norm with them; the sum is without
+          const float4* n = reinterpret_cast<const float4*>(a.p.vn + (te + j) * kKT + 64 * half);
+          top_o = -INFINITY;
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            const float4 w4 = n[x];
+            const float w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t& y = v[x >> 3][4 * (x & 7) + k];
+              const float s1 = __fmul_rn(__uint_as_float(y), c) - top_ref, s2 = s1 == -INFINITY ? s1 : s1 + lg2(w[k]);
+              sum += ex2(s1);
+              top_o = fmaxf(top_o, s2);
+              y = __float_as_uint(s2);
+            }
+          }
+        }
+        // The reference moves only when a score exceeds it by 2^8, the unit when a product exceeds it by 2^12: weights stay within
+        // f16, and the sums are rarely scaled. All threads of the tile learn here whether any row moves; from here on no score is
+        // needed in tensor memory.
+        if (bar_any(1 + i, 256, top > m + 8.f || (top - m) + top_o > b + 12.f)) {
+          *mine = make_float2(top, top_o);
           named_sync(1 + i, 256);
-          top = fmaxf(top, *theirs);
-          const bool move = top > m + 8.f;
-          float f = !move ? 1.f : m == -INFINITY ? 0.f : ex2(m - top);
-          if (move) m = top;
-          l *= f;
-          f *= fv;
+          const float2 other = *theirs;
+          const float both = fmaxf(top, other.x);
+          if (both > m + 8.f) {
+            const float now = ceilf(both);
+            if (m > -INFINITY) l *= ex2(m - now), b += m - now;
+            m = now;
+          }
+          const float most = m == -INFINITY ? -INFINITY : fmaxf((top - m) + top_o, (other.x - m) + other.y);
+          float f = 1.f;
+          if (most > b + 12.f) {
+            const float now = ceilf(most);
+            if (b > -INFINITY) f = ex2(b - now);   // (sums without a unit are zeros)
+            b = now;
+          }
           if (j > s.t0 && __any_sync(0xffffffffu, f != 1.f)) {
             wait(pv_done(i), (tile - 1) & 1);
             tc_fence_after();
@@ -1189,8 +1245,24 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
           }
           named_sync(1 + i, 256);   // the exchanged maxima have been read
         }
-        const float ref = (m == -INFINITY ? 0.f : m) - dv;   // weights come out times 2^(E - reference exponent)
-        const uint64_t c2 = pair2(c, c), r2 = pair2(-ref, -ref);
+        const float m_ref = m == -INFINITY ? 0.f : m, b_ref = b == -INFINITY ? 0.f : b;
+        float cw = v_apart ? 1.f : c;                                            // weights in the sums' unit: 2^(cw v + rv)
+        float rv = v_apart ? (top_ref - m_ref) - b_ref : ((float)ve_now - b_ref) - m_ref;
+        const float gap = v_apart || b == -INFINITY ? 0.f : b - (float)ve_now;   // from those to the sum's weights, log2
+        // Hardly ever: the tile's values are so small that its weights would be too small to add up, or the scores so large that
+        // their products with c have to be rounded before the reference is taken off, as the reference was.
+        const bool apart = !v_apart && __any_sync(0xffffffffu, gap > 40.f || fabsf(m_ref) > 1048576.f);
+        if (apart) {
+#pragma unroll
+          for (int x = 0; x < 64; ++x) {
+            uint32_t& y = v[x >> 5][x & 31];
+            const float s1 = __fmul_rn(__uint_as_float(y), c) - m_ref;
+            sum += ex2(s1);
+            y = __float_as_uint(s1);
+          }
+          cw = 1.f, rv = (float)ve_now - b_ref;
+        }
+        const uint64_t c2 = pair2(cw, cw), r2 = pair2(rv, rv);
         uint64_t sums[2] = {0, 0};
 #pragma unroll
         for (int q4 = 0; q4 < 2; ++q4) {
@@ -1206,11 +1278,14 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
           tmem_st16(cs + 32 * half + 16 * q4, p);
         }
         const float2 sum2 = unpair2(add2(sums[0], sums[1]));
-        const float sum = sum2.x + sum2.y;
+        float unit = exp2f(gap);
+        if (v_apart) unit = ex2(top_ref - m_ref);
+        else if (apart) unit = 1.f;
+        else sum = sum2.x + sum2.y;
         etc::tmem_wait_st();
         // A row that has seen nothing has no weights: its masked scores leave 2^-126 each in a quarter of the exponentials, and a
         // sum of those is not a sum to divide by.
-        l = fmaf(m == -INFINITY ? 0.f : sum, exp2f(-dv), l);
+        l = fmaf(m == -INFINITY ? 0.f : sum, unit, l);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) bar_arrive(p_full(i));
@@ -1219,13 +1294,12 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
       wait(pv_done(i), (tile - 1) & 1);
       tc_fence_after();
       const bool cut = s.t0 > 0 || s.t1 < s.nt;
-      *mine = l;
+      mine->x = l;
       named_sync(1 + i, 256);
-      l += *theirs;
+      l += theirs->x;
       named_sync(1 + i, 256);
-      const float up = exp2f((float)vref);
       if (!cut) {
-        const float f = l > 0.f ? up / l : 0.f;
+        const float up = exp2f(0.5f * b), f = l > 0.f ? up / l : 0.f;   // in two steps: no overflow
         uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + oat + half * (D / 2));
 #pragma unroll 1
         for (int q4 = 0; q4 < D / 64; ++q4) {
@@ -1238,7 +1312,7 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
               uint32_t w[4];
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
-                const float y0 = __uint_as_float(v[8 * k + 2 * x]) * f, y1 = __uint_as_float(v[8 * k + 2 * x + 1]) * f;
+                const float y0 = __uint_as_float(v[8 * k + 2 * x]) * f * up, y1 = __uint_as_float(v[8 * k + 2 * x + 1]) * f * up;
                 w[x] = a.q_dtype == TQ_F16 ? half2_bits(y0, y1) : etc::bf16x2_bits(y0, y1);
               }
               o[4 * q4 + k] = make_uint4(w[0], w[1], w[2], w[3]);
@@ -1257,7 +1331,7 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
             part[(D / 8 * half + 8 * q4 + k) * kItemRows + 128 * i + r] =
                 make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]), __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]));
         }
-        if (half == 0) part[(D / 4) * kItemRows + 128 * i + r] = make_float4(m, l, up, 0.f);
+        if (half == 0) part[(D / 4) * kItemRows + 128 * i + r] = make_float4(m, l, b, 0.f);
       }
       tc_fence_before();
       __syncwarp();
@@ -1286,7 +1360,7 @@ __global__ void __launch_bounds__(kItemRows) paged_flash_merge_kernel(FlashArgs 
   if (r >= s.nrows) return;
   const float4* part = reinterpret_cast<const float4*>(a.p.part);
   constexpr int kSlot = (D / 4 + 1) * kItemRows;
-  float M = -INFINITY;
+  float M = -INFINITY, unit = -INFINITY;   // the largest reference and the largest unit
   int slots = 0;
   for (int e = c; e < P; ++e) {
     const Span q = span_of(U, e, P);
@@ -1294,7 +1368,9 @@ __global__ void __launch_bounds__(kItemRows) paged_flash_merge_kernel(FlashArgs 
     const int t0 = max(0, (int)(max(q.u0, s.first) - s.first) - kItemCost), t1 = max(0, (int)(min(q.u1, s.next) - s.first) - kItemCost);
     if (t1 <= t0) continue;
     if (t0 == 0 && t1 == s.nt) return;   // one CTA had all of its tiles and wrote the result
-    M = fmaxf(M, part[(int64_t)(2 * e + (t0 == 0 ? 1 : 0)) * kSlot + (D / 4) * kItemRows + r].x);
+    const float4 st = part[(int64_t)(2 * e + (t0 == 0 ? 1 : 0)) * kSlot + (D / 4) * kItemRows + r];
+    if (st.x > M) unit += M == -INFINITY ? 0.f : M - st.x, M = st.x;   // relative to M
+    unit = fmaxf(unit, st.x == -INFINITY ? -INFINITY : st.x - M + st.z);
     ++slots;
   }
   if (slots == 0) return;
@@ -1310,7 +1386,7 @@ __global__ void __launch_bounds__(kItemRows) paged_flash_merge_kernel(FlashArgs 
     const float4 st = p[(D / 4) * kItemRows + r];
     const float w = st.x == -INFINITY ? 0.f : exp2f(st.x - M);
     l = fmaf(w, st.y, l);
-    const float wv = w * st.z;
+    const float wv = st.x == -INFINITY || st.z == -INFINITY ? 0.f : exp2f((st.x - M + st.z) - unit);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float4 v = p[(4 * blockIdx.y + k) * kItemRows + r];
@@ -1318,7 +1394,7 @@ __global__ void __launch_bounds__(kItemRows) paged_flash_merge_kernel(FlashArgs 
       acc[4 * k + 2] = fmaf(wv, v.z, acc[4 * k + 2]), acc[4 * k + 3] = fmaf(wv, v.w, acc[4 * k + 3]);
     }
   }
-  const float f = l > 0.f ? 1.f / l : 0.f;
+  const float up = exp2f(0.5f * unit), f = l > 0.f ? up / l : 0.f;
   const int row = s.row0 + r, tok = row / a.G, hq = (a.head0 + s.h) * a.G + row - tok * a.G;
   uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (((int64_t)a.bt.q_start[s.b] + tok) * a.Hq + hq) * D + 16 * blockIdx.y);
 #pragma unroll
@@ -1326,7 +1402,7 @@ __global__ void __launch_bounds__(kItemRows) paged_flash_merge_kernel(FlashArgs 
     uint32_t w[4];
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      const float y0 = acc[8 * k + 2 * x] * f, y1 = acc[8 * k + 2 * x + 1] * f;
+      const float y0 = acc[8 * k + 2 * x] * f * up, y1 = acc[8 * k + 2 * x + 1] * f * up;
       w[x] = a.q_dtype == TQ_F16 ? half2_bits(y0, y1) : etc::bf16x2_bits(y0, y1);
     }
     o[k] = make_uint4(w[0], w[1], w[2], w[3]);

@@ -308,7 +308,7 @@ bool flash_formats(const tq_view& k, const tq_view& v) { return k.ops16 && v.ops
 struct FlashPlan {
   int64_t max_seqs, max_tiles, max_items;
   int heads, ctas;      // KV heads of a round
-  size_t head, tile_start, item_start, unit, ke, ve, seen, part, krows, vrows, qrows, qfactor, total;
+  size_t head, tile_start, item_start, unit, ke, ve, kn, vn, seen, part, krows, vrows, qrows, qfactor, total;
 };
 
 constexpr size_t kRowsCap = (size_t)1 << 30;   // f16 rows held at a time, unless one KV head needs more
@@ -337,6 +337,8 @@ FlashPlan flash_plan(const tq_view& k, const Batch& b, int Hq, int Hkv, bool oth
   p.unit = take((size_t)(p.max_items + 1) * 4);
   p.ke = take((size_t)Hkv * p.max_tiles * 4);
   p.ve = take((size_t)Hkv * p.max_tiles * 4);
+  p.kn = take(rows / tile * kKT * 4);
+  p.vn = take(rows / tile * kKT * 4);
   p.seen = take((size_t)p.max_tiles * 16);
   p.part = take((size_t)2 * p.ctas * kItemRows * (k.d + 4) * 4);
   p.krows = take(rows);
@@ -362,7 +364,8 @@ int attn_flash(const AttnArgs& g, const tq_view& k, const tq_view& v, const Flas
   a.out = g.out, a.err = g.err;
   auto ints = [&](size_t off) { return reinterpret_cast<int*>(ws + off); };
   a.p.head = ints(p.head), a.p.tile_start = ints(p.tile_start), a.p.item_start = ints(p.item_start), a.p.unit = ints(p.unit);
-  a.p.ke = ints(p.ke), a.p.ve = ints(p.ve), a.p.seen = reinterpret_cast<uint32_t*>(ws + p.seen);
+  a.p.ke = ints(p.ke), a.p.ve = ints(p.ve);
+  a.p.kn = reinterpret_cast<float*>(ws + p.kn), a.p.vn = reinterpret_cast<float*>(ws + p.vn), a.p.seen = reinterpret_cast<uint32_t*>(ws + p.seen);
   a.p.part = reinterpret_cast<float*>(ws + p.part);
   a.p.krows = reinterpret_cast<uint8_t*>(ws + p.krows), a.p.vrows = reinterpret_cast<uint8_t*>(ws + p.vrows);
   a.p.qrows = reinterpret_cast<uint8_t*>(ws + p.qrows), a.p.qfactor = reinterpret_cast<float*>(ws + p.qfactor);

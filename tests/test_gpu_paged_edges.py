@@ -163,11 +163,11 @@ def test_bad_bounds_are_recorded_and_their_rows_kept(tq, news, dtype):
 # ------------------------------------------------------------------ norms far apart
 
 
-FAR = [([1], [300]), ([5, 1], [300, 40])]
+FAR = [([1], [300]), ([5, 1], [300, 40]), ([40], [41]), ([200, 3], [400, 150])]
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
-@pytest.mark.parametrize("d,kf,vf,norm", [(128, "mse4", "mse4", "f16"), (128, "prod3", "prod3", "f16")])
+@pytest.mark.parametrize("d,kf,vf,norm", [(128, "mse4", "mse4", "f16"), (128, "prod3", "prod3", "f16"), (64, "mse4", "mse4", "f32"), (128, "mse3", "prod3", "f16")])
 @pytest.mark.parametrize("news,lens", FAR)
 def test_values_that_a_row_does_not_see_cost_it_nothing(tq, news, lens, d, kf, vf, norm, dtype):
     """The newest token's value is 4e6 times (fp32 norms: 1e20 times) its neighbours': rows that come before it are as exact as
@@ -187,7 +187,7 @@ def test_values_that_a_row_does_not_see_cost_it_nothing(tq, news, lens, d, kf, v
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
-@pytest.mark.parametrize("kf,norm", [("mse4", "f16")])
+@pytest.mark.parametrize("kf,norm", [("mse4", "f16"), ("prod3", "f16"), ("mse3", "f32")])
 @pytest.mark.parametrize("news,lens", FAR)
 def test_keys_that_a_row_does_not_see_cost_it_nothing(tq, news, lens, kf, norm, dtype):
     """The same for the newest token's key."""
@@ -209,7 +209,7 @@ def test_keys_that_a_row_does_not_see_cost_it_nothing(tq, news, lens, kf, norm, 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
 @pytest.mark.parametrize("norm", ["f16", "f32"])
-@pytest.mark.parametrize("news", [[1, 2]])
+@pytest.mark.parametrize("news", [[1, 2], [100, 50]])
 def test_norms_spread_over_their_type(tq, news, norm, dtype):
     """Keys and values whose norms are spread evenly over 2^26 (fp16 norms) or 2^120 (fp32), in no order; causal and not."""
     fk, fv = fmt(tq, 128, "mse4", 0, norm), fmt(tq, 128, "prod3", 1) if norm == "f16" else fmt(tq, 128, "mse4", 1, norm)
@@ -233,8 +233,8 @@ def test_norms_spread_over_their_type(tq, news, norm, dtype):
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("what", [float("inf"), float("nan")])
-@pytest.mark.parametrize("kf,vf", [("mse4", "mse4"), ("prod3", "prod3")])
-@pytest.mark.parametrize("news,lens,window", [([5], [40], 0), ([3, 1], [200, 17], 20)])
+@pytest.mark.parametrize("kf,vf", [("mse4", "mse4"), ("prod3", "prod3"), ("mse3", "qjl")])
+@pytest.mark.parametrize("news,lens,window", [([5], [40], 0), ([3, 1], [200, 17], 20), ([60, 70], [90, 300], 0), ([80], [400], 50)])
 def test_rows_that_are_not_finite_and_not_seen(tq, news, lens, window, kf, vf, what, dtype):
     """The newest key and value, and (with a window) one just behind the window of the later tokens, have a norm of infinity or
     NaN: the rows that do not see them are as if they were not there."""
