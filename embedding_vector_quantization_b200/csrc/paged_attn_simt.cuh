@@ -237,8 +237,8 @@ __global__ void __launch_bounds__(kAttThreads) paged_attn_simt_kernel(AttnArgs a
     for (int r = warp; r < kTileRows; r += kAttThreads / 32) {
       const float s = sc[r * kKeyTile + lane];
       float top = s;
-      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float old = mx[r], now = fmaxf(old, top);
+      for (int o = 16; o; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float old = mx[r], now = max_nan(old, top);
       const float p = now == -INFINITY || s == -INFINITY ? 0.f : exp2f(s - now);
       float sum = p;
       for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kAppThreads) paged_combine_simt_kernel(AttnArg
   for (int e = tid; e < R * dv; e += kAppThreads) {
     const int r = e / dv, j = e - r * dv;
     float top = -INFINITY;
-    for (int s = 0; s < a.nsplit; ++s) top = fmaxf(top, part[(s * R + r) * (dv + 2) + dv]);
+    for (int s = 0; s < a.nsplit; ++s) top = max_nan(top, part[(s * R + r) * (dv + 2) + dv]);
     float v = 0.f, sum = 0.f;
     if (top != -INFINITY)
       for (int s = 0; s < a.nsplit; ++s) {

@@ -89,6 +89,18 @@ __device__ __forceinline__ int64_t place_of(const Batch& bt, int b, int64_t p, i
   return (page * Hkv + h) * bt.page_size + slot;
 }
 
+// The larger one, NaN if either is: a row's running maximum takes a NaN score along, and everything after it becomes NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Squares above this are summed again of vectors times 2^-70 (exact): the sum of 256 stays within fp32. eps is nothing to them.
 constexpr float kManySquares = 1e37f;
 constexpr float kSmaller = 8.4703295e-22f;   // 2^-70

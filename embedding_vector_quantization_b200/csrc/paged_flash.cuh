@@ -1186,10 +1186,10 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
           const int x0 = 16 * (q & 1);
           mx4[q] = __uint_as_float(w[x0]);
 #pragma unroll
-          for (int x = 1; x < 15; x += 2) mx4[q] = fmaxf(mx4[q], fmaxf(__uint_as_float(w[x0 + x]), __uint_as_float(w[x0 + x + 1])));
-          mx4[q] = fmaxf(mx4[q], __uint_as_float(w[x0 + 15]));
+          for (int x = 1; x < 15; x += 2) mx4[q] = max_nan(mx4[q], __uint_as_float(w[x0 + x]), __uint_as_float(w[x0 + x + 1]));
+          mx4[q] = max_nan(mx4[q], __uint_as_float(w[x0 + 15]));
         }
-        const float top = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c, top_ref = top == -INFINITY ? 0.f : top;
+        const float top = max_nan(max_nan(mx4[0], mx4[1], mx4[2]), mx4[3]) * c, top_ref = top == -INFINITY ? 0.f : top;
         const bool v_apart = ve_now == kApart;
         float top_o = (float)ve_now, sum = 0.f;   // the largest weight times value norm, log2, relative to the largest weight
         if (v_apart) {   // from here on scores are relative to this half's largest and have their value norm with them; the sum is without
@@ -1204,27 +1204,27 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
               uint32_t& y = v[x >> 3][4 * (x & 7) + k];
               const float s1 = __fmul_rn(__uint_as_float(y), c) - top_ref, s2 = s1 == -INFINITY ? s1 : s1 + lg2(w[k]);
               sum += ex2(s1);
-              top_o = fmaxf(top_o, s2);
+              top_o = max_nan(top_o, s2);
               y = __float_as_uint(s2);
             }
           }
         }
         // The reference moves only when a score exceeds it by 2^8, the unit when a product exceeds it by 2^12: weights stay within
         // f16, and the sums are rarely scaled. All threads of the tile learn here whether any row moves; from here on no score is
-        // needed in tensor memory.
-        if (bar_any(1 + i, 256, top > m + 8.f || (top - m) + top_o > b + 12.f)) {
+        // needed in tensor memory. (A NaN moves them, and the row is NaN from there on.)
+        if (bar_any(1 + i, 256, !(top <= m + 8.f && (top - (m == -INFINITY ? 0.f : m)) + top_o <= b + 12.f))) {
           *mine = make_float2(top, top_o);
           named_sync(1 + i, 256);
           const float2 other = *theirs;
-          const float both = fmaxf(top, other.x);
-          if (both > m + 8.f) {
+          const float both = max_nan(top, other.x);
+          if (!(both <= m + 8.f)) {
             const float now = ceilf(both);
             if (m > -INFINITY) l *= ex2(m - now), b += m - now;
             m = now;
           }
-          const float most = m == -INFINITY ? -INFINITY : fmaxf((top - m) + top_o, (other.x - m) + other.y);
+          const float most = m == -INFINITY ? -INFINITY : max_nan((top - m) + top_o, (other.x - m) + other.y);
           float f = 1.f;
-          if (most > b + 12.f) {
+          if (!(most <= b + 12.f)) {
             const float now = ceilf(most);
             if (b > -INFINITY) f = ex2(b - now);   // (sums without a unit are zeros)
             b = now;

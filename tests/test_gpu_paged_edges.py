@@ -260,3 +260,47 @@ def test_rows_that_are_not_finite_and_not_seen(tq, news, lens, window, kf, vf, w
     got = tq.attn_paged(fk.handle, fv.handle, q, kc, vc, bt, 0.09, window=window)
     assert got[keep].isfinite().all()
     pu.check_attention(got[keep], ref[keep], tol[keep], q.dtype)
+
+
+# ------------------------------------------------------------------ NaN that is seen
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("kf", ["mse4", "prod3", "mse3"])
+@pytest.mark.parametrize("side", ["key", "value", "query"])
+@pytest.mark.parametrize("news", [[1], [5], [70]])
+def test_nan_goes_to_the_rows_that_see_it(tq, news, side, kf, dtype):
+    """A NaN key, value or query makes the rows that use it NaN, wherever it stands, and no others."""
+    fk, fv = fmt(tq, 128, kf, 0), fmt(tq, 128, kf, 1)
+    n, L = news[0], 300
+    c = attention_case(tq, 128, kf, kf, 1, 4, news, [L], 16, dtype)
+    _, _, bt, kc, vc, kr, vr, q, pr = c
+    want = check_case(tq, c, 0.09, True, 0, h_of(dtype))
+    if side == "query":
+        q[0, 1] = float("nan")
+        got = tq.attn_paged(fk.handle, fv.handle, q, kc, vc, bt, 0.09)
+        assert got[0, 1].isnan().all()
+        got[0, 1] = want[0, 1]
+        assert torch.equal(got, want)
+        return
+    cache = kc if side == "key" else vc
+    for p in [0, 1, 2, 3, 4, 5, 6, 7, 14, 15, 126, 127, 128, 134, L - n] + list(range(L - 9, L)):
+        page, slot = pu.slots(bt, 0, p, p + 1)
+        old = cache.norms[page, :, slot].clone()
+        cache.norms[page, :, slot] = float("nan")
+        got = tq.attn_paged(fk.handle, fv.handle, q, kc, vc, bt, 0.09)
+        cache.norms[page, :, slot] = old
+        sees = torch.arange(L - n, L, device="cuda") >= p
+        assert got[sees].isnan().all(), f"position {p}"
+        room = torch.finfo(q.dtype).eps * 4 * want.abs().amax() + 0.02 * (dtype != "fp32")
+        assert ((got - want)[~sees].abs() <= room).all(), f"position {p}"
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("n", [1, 70])
+def test_rows_of_nan_alone(tq, n, dtype):
+    """Every key that a row sees is NaN: NaN, not the zeros of a row without keys."""
+    c = attention_case(tq, 128, "mse4", "mse4", 2, 4, [n], [n], 16, dtype)
+    fk, fv, bt, kc, vc, kr, vr, q, pr = c
+    kc.norms.fill_(float("nan"))
+    assert tq.attn_paged(fk.handle, fv.handle, q, kc, vc, bt, 0.09).isnan().all()
