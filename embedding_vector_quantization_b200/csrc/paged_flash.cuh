@@ -1136,14 +1136,15 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
       const int key_first = (lo_all / kKT + s.lo_tile) * kKT;
       // Running reference (log2) and sum of the weights. The value sums have a unit of their own, 2^(m + b), which follows what the
       // row's weights and the value tiles' exponents make together: a large value that the row hardly sees costs it nothing.
-      // m and b are whole numbers, and what is formed of them stays exact.
-      float m = -INFINITY, l = 0.f, b = -INFINITY;
+      // m and b are whole numbers, and what is formed of them stays exact. limit: what a score may be without moving m (-infinity
+      // while there is no unit; NaN where |m| is above 2^20, whose tiles all take the rare part below); rest: -(m + b), or 0.
+      float m = -INFINITY, l = 0.f, b = -INFINITY, limit = -INFINITY, rest = 0.f;
       int ke = a.p.ke[te + s.t0], ve = a.p.ve[te + s.t0];
       uint4 seen = *reinterpret_cast<const uint4*>(a.p.seen + 4 * (tile0 + s.t0));
       for (int j = s.t0; j < s.t1; ++j, ++tile) {
-        const int ke_now = ke, ve_now = ve;
-        // above 0: c times the mask's -infinity stays -infinity
-        const float c = fmaxf(ke_now == kApart ? qscale : qscale * exp2f((float)ke_now), 1e-37f);
+        const bool k_apart = ke == kApart, v_apart = ve == kApart;
+        const float ev = (float)ve;
+        float c = fmaxf(qscale * exp2f((float)ke), 1e-37f);   // above 0: c times the mask's -infinity stays -infinity
         const uint4 seen_now = seen;
         if (j + 1 < s.t1) {
           ke = a.p.ke[te + j + 1], ve = a.p.ve[te + j + 1];
@@ -1160,16 +1161,6 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
         for (int q4 = 0; q4 < 2; ++q4) tmem_ld32(cs + 64 * half, v[q4], 32 * q4);
 #pragma unroll
         for (int q4 = 0; q4 < 2; ++q4) tmem_wait_ld(v[q4]);
-        if (ke_now == kApart) {
-          const float4* n = reinterpret_cast<const float4*>(a.p.kn + (te + j) * kKT + 64 * half);
-#pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            const float4 w = n[x];
-            uint32_t* y = &v[x >> 3][4 * (x & 7)];
-            y[0] = __float_as_uint(__uint_as_float(y[0]) * w.x), y[1] = __float_as_uint(__uint_as_float(y[1]) * w.y);
-            y[2] = __float_as_uint(__uint_as_float(y[2]) * w.z), y[3] = __float_as_uint(__uint_as_float(y[3]) * w.w);
-          }
-        }
         if (masked) {
 #pragma unroll
           for (int q4 = 0; q4 < 2; ++q4) {
@@ -1189,30 +1180,53 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
           for (int x = 1; x < 15; x += 2) mx4[q] = max_nan(mx4[q], __uint_as_float(w[x0 + x]), __uint_as_float(w[x0 + x + 1]));
           mx4[q] = max_nan(mx4[q], __uint_as_float(w[x0 + 15]));
         }
-        const float top = max_nan(max_nan(mx4[0], mx4[1], mx4[2]), mx4[3]) * c, top_ref = top == -INFINITY ? 0.f : top;
-        const bool v_apart = ve_now == kApart;
-        float top_o = (float)ve_now, sum = 0.f;   // the largest weight times value norm, log2, relative to the largest weight
-        if (v_apart) {   // from here on scores are relative to this half's largest and have their value norm with them; the sum is without
-          const float4* n = reinterpret_cast<const float4*>(a.p.vn + (te + j) * kKT + 64 * half);
-          top_o = -INFINITY;
+        float top = max_nan(max_nan(mx4[0], mx4[1], mx4[2]), mx4[3]) * c;
+        float rv = ev + rest;         // weights in the sums' unit: 2^(c score + rv)
+        const float gap = b - ev;     // from those to the sum's weights, log2
+        bool odd = false;             // rv and the sum of weights are made in the rare part below
+        // The reference moves only when a score exceeds it by 2^8, the unit when a product of weight and value norm exceeds it by
+        // 2^12: weights stay within f16, and the sums are rarely scaled. All threads of the tile learn here whether any row moves;
+        // from here on no score is needed in tensor memory. (A NaN moves them, and the row is NaN from there on.) Rare as well:
+        // tiles whose norms are apart; values so small that the weights would be too small to add up; scores so large that their
+        // products with c have to be rounded before the reference is taken off, as the reference was.
+        if (bar_any(1 + i, 256, k_apart || v_apart || !(top <= limit && top + rv <= 12.f && gap <= 40.f))) {
+          if (k_apart) {
+            const float4* n = reinterpret_cast<const float4*>(a.p.kn + (te + j) * kKT + 64 * half);
+            c = fmaxf(qscale, 1e-37f);
+            top = -INFINITY;
 #pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            const float4 w4 = n[x];
-            const float w[4] = {w4.x, w4.y, w4.z, w4.w};
+            for (int x = 0; x < 16; ++x) {
+              const float4 w4 = n[x];
+              const float w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t& y = v[x >> 3][4 * (x & 7) + k];
-              const float s1 = __fmul_rn(__uint_as_float(y), c) - top_ref, s2 = s1 == -INFINITY ? s1 : s1 + lg2(w[k]);
-              sum += ex2(s1);
-              top_o = max_nan(top_o, s2);
-              y = __float_as_uint(s2);
+              for (int k = 0; k < 4; ++k) {
+                uint32_t& y = v[x >> 3][4 * (x & 7) + k];
+                if (y != 0xff800000u) y = __float_as_uint(__uint_as_float(y) * w[k]);   // (masked)
+                top = max_nan(top, __uint_as_float(y));
+              }
+            }
+            top *= c;
+          }
+          // the largest weight times value norm, log2, relative to this half's largest weight
+          float top_o = ev, sum = 0.f;
+          const float top_ref = top == -INFINITY ? 0.f : top;
+          if (v_apart) {   // from here on scores are relative to this half's largest and have their value norm with them; the sum is without
+            const float4* n = reinterpret_cast<const float4*>(a.p.vn + (te + j) * kKT + 64 * half);
+            top_o = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              const float4 w4 = n[x];
+              const float w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                uint32_t& y = v[x >> 3][4 * (x & 7) + k];
+                const float s1 = __fmul_rn(__uint_as_float(y), c) - top_ref, s2 = s1 == -INFINITY ? s1 : s1 + lg2(w[k]);
+                sum += ex2(s1);
+                top_o = max_nan(top_o, s2);
+                y = __float_as_uint(s2);
+              }
             }
           }
-        }
-        // The reference moves only when a score exceeds it by 2^8, the unit when a product exceeds it by 2^12: weights stay within
-        // f16, and the sums are rarely scaled. All threads of the tile learn here whether any row moves; from here on no score is
-        // needed in tensor memory. (A NaN moves them, and the row is NaN from there on.)
-        if (bar_any(1 + i, 256, !(top <= m + 8.f && (top - (m == -INFINITY ? 0.f : m)) + top_o <= b + 12.f))) {
           *mine = make_float2(top, top_o);
           named_sync(1 + i, 256);
           const float2 other = *theirs;
@@ -1244,25 +1258,26 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
             }
           }
           named_sync(1 + i, 256);   // the exchanged maxima have been read
-        }
-        const float m_ref = m == -INFINITY ? 0.f : m, b_ref = b == -INFINITY ? 0.f : b;
-        float cw = v_apart ? 1.f : c;                                            // weights in the sums' unit: 2^(cw v + rv)
-        float rv = v_apart ? (top_ref - m_ref) - b_ref : ((float)ve_now - b_ref) - m_ref;
-        const float gap = v_apart || b == -INFINITY ? 0.f : b - (float)ve_now;   // from those to the sum's weights, log2
-        // Hardly ever: the tile's values are so small that its weights would be too small to add up, or the scores so large that
-        // their products with c have to be rounded before the reference is taken off, as the reference was.
-        const bool apart = !v_apart && __any_sync(0xffffffffu, gap > 40.f || fabsf(m_ref) > 1048576.f);
-        if (apart) {
+          const float m_ref = m == -INFINITY ? 0.f : m, b_ref = b == -INFINITY ? 0.f : b;
+          rest = b == -INFINITY ? 0.f : -(m + b);
+          limit = b == -INFINITY ? -INFINITY : fabsf(m) <= 1048576.f ? m + 8.f : NAN;
+          rv = ev + rest;
+          if (v_apart) {
+            odd = true, c = 1.f, rv = (top_ref - m_ref) - b_ref, sum *= ex2(top_ref - m_ref);
+          } else if (__any_sync(0xffffffffu, b - ev > 40.f || fabsf(m_ref) > 1048576.f)) {
+            odd = true, rv = ev - b_ref;
 #pragma unroll
-          for (int x = 0; x < 64; ++x) {
-            uint32_t& y = v[x >> 5][x & 31];
-            const float s1 = __fmul_rn(__uint_as_float(y), c) - m_ref;
-            sum += ex2(s1);
-            y = __float_as_uint(s1);
+            for (int x = 0; x < 64; ++x) {
+              uint32_t& y = v[x >> 5][x & 31];
+              const float s1 = __fmul_rn(__uint_as_float(y), c) - m_ref;
+              sum += ex2(s1);
+              y = __float_as_uint(s1);
+            }
+            c = 1.f;
           }
-          cw = 1.f, rv = (float)ve_now - b_ref;
+          l += m == -INFINITY ? 0.f : sum;
         }
-        const uint64_t c2 = pair2(cw, cw), r2 = pair2(rv, rv);
+        const uint64_t c2 = pair2(c, c), r2 = pair2(rv, rv);
         uint64_t sums[2] = {0, 0};
 #pragma unroll
         for (int q4 = 0; q4 < 2; ++q4) {
@@ -1278,14 +1293,11 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
           tmem_st16(cs + 32 * half + 16 * q4, p);
         }
         const float2 sum2 = unpair2(add2(sums[0], sums[1]));
-        float unit = exp2f(gap);
-        if (v_apart) unit = ex2(top_ref - m_ref);
-        else if (apart) unit = 1.f;
-        else sum = sum2.x + sum2.y;
+        const float sum = sum2.x + sum2.y;
         etc::tmem_wait_st();
         // A row that has seen nothing has no weights: its masked scores leave 2^-126 each in a quarter of the exponentials, and a
         // sum of those is not a sum to divide by.
-        l = fmaf(m == -INFINITY ? 0.f : sum, unit, l);
+        l = fmaf(sum, odd ? 0.f : exp2f(b - ev), l);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) bar_arrive(p_full(i));
