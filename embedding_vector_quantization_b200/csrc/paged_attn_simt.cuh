@@ -104,6 +104,7 @@ __global__ void __launch_bounds__(kAppThreads) paged_qprep_kernel(AttnArgs a) {
   float* part_s = ys + (size_t)R * w;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   __shared__ int blind[R];
+  __shared__ float back[R];   // of tame_head
   const int64_t row0 = (int64_t)blockIdx.x * R, rows = a.bt.ntok * a.Hq;
   if (tid < R) blind[tid] = 0;
   __syncthreads();
@@ -124,6 +125,8 @@ __global__ void __launch_bounds__(kAppThreads) paged_qprep_kernel(AttnArgs a) {
         prep_head<float, 8>(a.q, a.q_dtype, t * a.q_stride + (int64_t)h * d, d, a.prep, p, z);
       }
     }
+    const float f = tame_head<8>(z);
+    if (lane == 0) back[r] = f;
 #pragma unroll
     for (int c = 0; c < 8; ++c)
       if (lane + 32 * c < d) zf[r * d + lane + 32 * c] = z[c];
@@ -133,14 +136,14 @@ __global__ void __launch_bounds__(kAppThreads) paged_qprep_kernel(AttnArgs a) {
   rows_matvec<R>(zf, d, a.k.PiT, d, part_s, ys);
   for (int e = tid; e < R * d; e += kAppThreads) {
     const int r = e / d;
-    if (row0 + r < rows) a.qr[(row0 + r) * dk + (e - r * d)] = blind[r] ? kBlind : ys[e] * s1;
+    if (row0 + r < rows) a.qr[(row0 + r) * dk + (e - r * d)] = blind[r] ? kBlind : ys[e] * (s1 * back[r]);
   }
   if (m == 0) return;
   __syncthreads();
   rows_matvec<R>(zf, d, a.k.ST, m, part_s, ys);
   for (int e = tid; e < R * m; e += kAppThreads) {
     const int r = e / m;
-    if (row0 + r < rows) a.qr[(row0 + r) * dk + d + (e - r * m)] = ys[e] * s2;
+    if (row0 + r < rows) a.qr[(row0 + r) * dk + d + (e - r * m)] = ys[e] * (s2 * back[r]);
   }
 }
 

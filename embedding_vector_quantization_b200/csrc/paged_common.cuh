@@ -172,5 +172,18 @@ __device__ __forceinline__ void prep_head(const void* x, int x_dtype, int64_t at
   for (int c = 0; c < MAXC; ++c) z[c] = y[c];
 }
 
+// A prepared head whose products with S (128 of a few each) could pass fp32 is taken times 2^-64; returns what makes up for it. The
+// whole warp calls it.
+template <int MAXC>
+__device__ __forceinline__ float tame_head(float (&z)[MAXC]) {
+  float top = 0.f;
+#pragma unroll
+  for (int c = 0; c < MAXC; ++c) top = fmaxf(top, fabsf(z[c]));
+  if (!__any_sync(0xffffffffu, top > 1e30f)) return 1.f;
+#pragma unroll
+  for (int c = 0; c < MAXC; ++c) z[c] *= 5.421011e-20f;
+  return 1.8446744e19f;
+}
+
 }  // namespace paged
 }  // namespace tqk

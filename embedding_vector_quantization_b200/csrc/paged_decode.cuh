@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
       float* part_s = zf + 8 * D;                       // [8][256]
       float* o = part_s + 8 * 256;                      // [8][D]
       float* qq = o + 8 * D;                            // [8][DK]
-      float z[D / 32];
+      float z[D / 32], f1 = a.scale * 1.44269504089f;
       bool blind = false;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) z[c] = 0.f;
@@ -384,10 +384,10 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
           prep_head<float, D / 32>(a.q, a.q_dtype, t0 * a.q_stride + (int64_t)(h * a.G + strip.row0 + warp - i * a.G) * D, D, a.prep, p, z);
         }
       }
+      f1 *= tame_head<D / 32>(z);
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) zf[warp * D + lane + 32 * c] = z[c];
       __syncthreads();
-      const float f1 = a.scale * 1.44269504089f;
       rows_at_once<D>(zf, rows, a.k.PiT, part_s, o);
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) qq[warp * DK + lane + 32 * c] = blind ? kBlind : o[warp * D + lane + 32 * c] * f1;
@@ -431,6 +431,7 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       int e = 0;
       if (top > 0.f && top < INFINITY) frexpf(top, &e);
+      e = max(-126, min(126, e));   // 2^-e is a number too
       float dn = ldexpf(1.f, -e), upf = ldexpf(1.f, e);
 #pragma unroll
       for (int s = 0; s < KS; ++s)
@@ -450,6 +451,7 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         e = 0;
         if (top > 0.f && top < INFINITY) frexpf(top, &e);
+        e = max(-126, min(126, e));
         dn = ldexpf(1.f, -e), upf = ldexpf(1.f, e);
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
@@ -843,12 +845,13 @@ __global__ void __launch_bounds__(256) paged_qslice_kernel(DecodeArgs da) {
       prep_head<float, 4>(a.q, a.q_dtype, t * a.q_stride + (int64_t)(l.h * a.G + l.row0 + r - i * a.G) * d, d, a.prep, p, z);
     }
   }
+  const float back = tame_head<4>(z);
 #pragma unroll
   for (int c = 0; c < 4; ++c)
     if (lane + 32 * c < d) zf[r * d + lane + 32 * c] = z[c];
   __syncthreads();
   rows_slice(zf, d, T, part_s, ys);
-  const float f = a.scale * 1.44269504089f * (code ? 1.f : kQjlScale / (float)m);
+  const float f = a.scale * 1.44269504089f * back * (code ? 1.f : kQjlScale / (float)m);
   a.qr[((int64_t)blockIdx.x * 8 + r) * dk + col + lane] = blind ? kBlind : ys[tid] * f;
 }
 

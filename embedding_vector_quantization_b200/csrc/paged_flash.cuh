@@ -702,12 +702,13 @@ __global__ void __launch_bounds__(kQtThreads) paged_qtile_kernel(FlashArgs a) {
       z[8 * c + 2 * e] = v.x, z[8 * c + 2 * e + 1] = v.y;
     }
   }
-  float ss = 0.f, rms = 1.f;
-#pragma unroll
-  for (int x = 0; x < 8 * C; ++x) ss = fmaf(z[x], z[x], ss);
-  ss += __shfl_xor_sync(0xffffffffu, ss, 1);
-  ss += __shfl_xor_sync(0xffffffffu, ss, 2);
+  float rms = 1.f;
   if (a.prep.weight) {
+    float ss = 0.f;
+#pragma unroll
+    for (int x = 0; x < 8 * C; ++x) ss = fmaf(z[x], z[x], ss);
+    ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+    ss += __shfl_xor_sync(0xffffffffu, ss, 2);
     rms = rsqrtf(ss / (float)D + a.prep.eps);
     const bool many = !(ss < kManySquares);
     if (__any_sync(0xffffffffu, many)) {
@@ -718,15 +719,14 @@ __global__ void __launch_bounds__(kQtThreads) paged_qtile_kernel(FlashArgs a) {
       s2 += __shfl_xor_sync(0xffffffffu, s2, 2);
       if (many) rms = kSmaller * rsqrtf(s2 / (float)D);
     }
-    ss = 0.f;
 #pragma unroll
-    for (int x = 0; x < 8 * C; ++x) {
-      z[x] *= rms * load_any(a.prep.weight, a.prep.weight_dtype, 8 * (ql + 4 * (x >> 3)) + (x & 7));
-      ss = fmaf(z[x], z[x], ss);
-    }
-    ss += __shfl_xor_sync(0xffffffffu, ss, 1);
-    ss += __shfl_xor_sync(0xffffffffu, ss, 2);
+    for (int x = 0; x < 8 * C; ++x) z[x] *= rms * load_any(a.prep.weight, a.prep.weight_dtype, 8 * (ql + 4 * (x >> 3)) + (x & 7));
   }
+  float top = 0.f;
+#pragma unroll
+  for (int x = 0; x < 8 * C; ++x) top = fmaxf(top, fabsf(z[x]));
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
   if (ok && rot == D && !a.prep.interleaved) {
 #pragma unroll
     for (int c = 0; c < C / 2; ++c)
@@ -768,10 +768,10 @@ __global__ void __launch_bounds__(kQtThreads) paged_qtile_kernel(FlashArgs a) {
         }
       }
   }
-  // |q_i| <= |q|, which the rotation keeps: the power of two that brings all of them below one
+  // the power of two that brings every coordinate below one; a rotation makes none larger than 2^(1/2) times the largest
   int e = 0;
-  const float nq = sqrtf(ss);
-  if (nq > 0.f && nq < INFINITY) frexpf(nq, &e);
+  if (top > 0.f && top < INFINITY) frexpf(top, &e);
+  e = max(-126, min(126, e + 1));
   const float sc = a.scale < 0.f ? -ldexpf(1.f, -e) : ldexpf(1.f, -e);
   if (ql == 0) a.p.qfactor[slot * kItemRows + r] = ok || !live ? ldexpf(fabsf(a.scale) * 1.44269504089f, e) : -1.f;
 #pragma unroll

@@ -304,3 +304,21 @@ def test_rows_of_nan_alone(tq, n, dtype):
     fk, fv, bt, kc, vc, kr, vr, q, pr = c
     kc.norms.fill_(float("nan"))
     assert tq.attn_paged(fk.handle, fv.handle, q, kc, vc, bt, 0.09).isnan().all()
+
+
+# ------------------------------------------------------------------ queries at the ends of their range
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("kf", ["mse4", "prod3"])
+@pytest.mark.parametrize("size", [1e-38, 3e-39, 1e-30, 1e20, 1e37])
+@pytest.mark.parametrize("news,prep", [([1, 1], "none"), ([5, 2], "half"), ([70, 1], "none"), ([70, 40], "half"), ([70, 2], "partial")])
+def test_queries_of_any_size(tq, news, prep, size, kf, dtype):
+    """Tiny queries average the values; large ones with a scale as small give ordinary scores."""
+    c = attention_case(tq, 128, kf, kf, 2, 4, news, [300, 90], 16, dtype, prep)
+    fk, fv, bt, kc, vc, kr, vr, q, pr = c
+    q = (q.double() * size).to(q.dtype)
+    if dtype == "fp32" and size < 1e-37:
+        q = q.to(torch.bfloat16).float()   # (subnormal inputs lose their own digits)
+    scale = 0.09 if size < 1 else 0.09 / size
+    check_case(tq, (fk, fv, bt, kc, vc, kr, vr, q, pr), scale, True, 0, h_of(dtype))
