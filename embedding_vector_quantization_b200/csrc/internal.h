@@ -22,6 +22,7 @@ struct tq_view {
   const uint8_t* ops16;    // d = 64 or 128 (m = 0 or d): f16 operands, of the paged expansion (tq_api.cu); NULL otherwise
   const uint8_t* ops_app;  // d = 64 or 128 (m = 0 or d), with codes: f16 pairs of Pi and M (tq_api.cu); NULL otherwise
   float m_abs, m_norm;     // largest row of M in the 1-norm and the 2-norm
+  float cent_up;           // the factor in [1, 2) with which the centroids come nearest to f16 (table_factor in tq_api.cu)
   int* err;                // device error word
   const double *cent_h, *bnd_h;   // host copies
 };

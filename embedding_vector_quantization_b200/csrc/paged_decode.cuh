@@ -436,6 +436,7 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
 #pragma unroll
       for (int s = 0; s < KS; ++s)
         qc[2 * s] = half2_bits(z[4 * s] * dn, z[4 * s + 1] * dn), qc[2 * s + 1] = half2_bits(z[4 * s + 2] * dn, z[4 * s + 3] * dn);
+      upf /= a.k.cent_up;   // the tables' factor, out again
       fc[0] = __shfl_sync(0xffffffffu, upf, 8 * t), fc[1] = __shfl_sync(0xffffffffu, upf, 8 * t + 4);
       if (SG) {
         // this lane's signs are those of projections t D/4 .. : step s takes pairs (i, i + D/8), i = 2 s, 2 s + 1
@@ -712,13 +713,14 @@ __global__ void __launch_bounds__(kDcThreads, 2) paged_decode_kernel(DecodeArgs 
         for (int w = 0; w < kDcWarps; ++w) top[j] = fmaxf(top[j], stat[w * 8 + 2 * t + j]);
         f[j] = m[j] == -INFINITY || sv[j] == 0.f ? 0.f : ex2(m[j] - top[j]) / sv[j];
       }
+      const float fv[2] = {f[0] / a.v.cent_up, f[1] / a.v.cent_up};
       // sums [warp][coordinate][row]
       float* o = reinterpret_cast<float*>(smem_dc + ring_off);
 #pragma unroll
       for (int y = 0; y < KS; ++y) {
         const int c = g * (D / 8) + 2 * y;
-        *reinterpret_cast<float2*>(o + c * 8 + 2 * t) = make_float2(oc[y][0] * f[0], oc[y][1] * f[1]);
-        *reinterpret_cast<float2*>(o + (c + 1) * 8 + 2 * t) = make_float2(oc[y][2] * f[0], oc[y][3] * f[1]);
+        *reinterpret_cast<float2*>(o + c * 8 + 2 * t) = make_float2(oc[y][0] * fv[0], oc[y][1] * fv[1]);
+        *reinterpret_cast<float2*>(o + (c + 1) * 8 + 2 * t) = make_float2(oc[y][2] * fv[0], oc[y][3] * fv[1]);
         if (SG) {
           *reinterpret_cast<float2*>(o + (D + c) * 8 + 2 * t) = make_float2(os[y][0] * f[0], os[y][1] * f[1]);
           *reinterpret_cast<float2*>(o + (D + c + 1) * 8 + 2 * t) = make_float2(os[y][2] * f[0], os[y][3] * f[1]);

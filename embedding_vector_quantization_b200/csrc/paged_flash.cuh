@@ -15,7 +15,7 @@
 // contraction: 4 d flops per (query row, key) for every format, where contracting the codes themselves would take
 // 2 (2 d + m_k + m_v). The f16 rows are written and read once through L2 (512 B per token and head at d = 128).
 //
-// Roundings: c[idx], Pi, S, rnorm / norm, x_hat, the prepared query (scaled by a power of two below 1) and the weights
+// Roundings: c[idx] (hardly: table_factor in tq_api.cu), Pi, S, rnorm / norm, x_hat, the prepared query (scaled by a power of two below 1) and the weights
 // to f16 (11 bits; outputs have 8 or 11); every sum, maximum and exponent in fp32.
 //
 // Measured at 8 KV heads, 32 query heads, d = 128: a chunk of 1024 tokens over 32768 with signs takes 680 us (expansion 80,
@@ -287,14 +287,14 @@ __device__ __forceinline__ void load_row(const Quant& Q, const CacheView& c, int
   }
 }
 
-// Table of f16 centroids for one packed byte (3 bits: for one pair of fields), a copy for each bank so that no two lanes
+// Table of f16 centroids (times cent_up, which brings them next to f16's values) for one packed byte (3 bits: for one pair of fields), a copy for each bank so that no two lanes
 // of a phase meet: 4 bits 4 B x 32 copies, 2 bits 8 B x 16, 1 bit 16 B x 8, 3 bits 64 pairs x 32.
 __device__ __forceinline__ void build_lut(const Quant& Q, uint8_t* lut, int tid, int nthreads) {
   if (Q.bits == 0) return;
   // a warp per entry, a lane per word: lane l writes the pair l mod (words of an entry)
   const int per = Q.bits == 3 ? 2 : 8 / Q.bits, n = Q.bits == 3 ? 64 : 256, mask = (1 << Q.bits) - 1;
   const int lane = tid & 31, p = (lane & (per / 2 - 1)) * 2 * Q.bits;
-  const uint32_t own = __half_as_ushort(__float2half_rn(lane <= mask ? Q.cent[lane] : 0.f));   // lane i: centroid i
+  const uint32_t own = __half_as_ushort(__float2half_rn(lane <= mask ? Q.cent[lane] * Q.cent_up : 0.f));   // lane i: centroid i
   for (int v = tid >> 5; v < n; v += nthreads >> 5) {
     const uint32_t x = __shfl_sync(0xffffffffu, own, v >> p & mask), y = __shfl_sync(0xffffffffu, own, v >> (p + Q.bits) & mask);
     *reinterpret_cast<uint32_t*>(lut + v * 128 + 4 * lane) = x | y << 16;
@@ -484,6 +484,7 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
   if (warp < 8) {
     // ---- operand rows: thread = token of the tile. Under way at a time: the page of the token after next, the next row.
     const int g = warp >> 2, r = tid & 127;
+    const float down = 1.f / Q.cent_up;   // the tables' factor, out again
     uint32_t* const extremes_g = extremes + 16 * g;
     TileCursor c{(int)(w0 / tiles), (int)(w0 % tiles), 0, 0, 0, 0, 0, 0};
     // The cursor's token: its page as loaded (nothing waits for it yet), and where in the page.
@@ -539,6 +540,7 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
       float ratio = 1.f;   // of the residual norm to the norm
       if (Q.m > 0 && Q.bits > 0) {
         ratio = norm != 0.f ? __half2float(__ushort_as_half(cur.rnorm)) / norm : 0.f;
+        ratio *= Q.cent_up;
         if (!(fabsf(ratio) <= 65504.f)) {   // the row stays finite, its norm tells that it is not
           ratio = 0.f;
           if (fabsf(norm) < INFINITY) norm = NAN;
@@ -557,7 +559,7 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
       if (top > 0) frexpf(__uint_as_float(top), &e);
       e = max(-126, min(126, e));
       if (i >= NS) wait(a_empty(s), (i / NS - 1) & 1);
-      scale_s[s * 128 + r] = !cur.ok ? 0.f : apart ? 1.f : ldexpf(norm, -e);
+      scale_s[s * 128 + r] = !cur.ok ? 0.f : down * (apart ? 1.f : ldexpf(norm, -e));
       if (r == 0) (kind ? a.p.ve : a.p.ke)[(int64_t)h * a.p.max_tiles + tile] = apart ? kApart : e;
       if (apart) (kind ? a.p.vn : a.p.kn)[((int64_t)h * a.p.max_tiles + tile) * kKT + r] = cur.ok ? norm : 0.f;
       const uint32_t row = base + L::kA + s * stage_bytes + r * 128;

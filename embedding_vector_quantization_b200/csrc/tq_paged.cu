@@ -73,7 +73,7 @@ Quant quant_of(const tq_view& v) {
   Quant q{};
   q.d = v.d, q.bits = v.bits, q.m = v.m, q.norm_dtype = v.norm_dtype, q.codes_B = v.codes_B, q.signs_B = v.signs_B;
   q.PiT = v.PiT, q.Pi = v.Pi, q.MT = v.MT, q.ST = v.ST, q.S = v.S, q.cent = v.cent, q.bnd = v.bnd, q.t64 = v.t64;
-  q.m_abs = v.m_abs, q.m_norm = v.m_norm;
+  q.m_abs = v.m_abs, q.m_norm = v.m_norm, q.cent_up = v.cent_up;
   return q;
 }
 

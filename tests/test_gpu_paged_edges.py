@@ -322,3 +322,23 @@ def test_queries_of_any_size(tq, news, prep, size, kf, dtype):
         q = q.to(torch.bfloat16).float()   # (subnormal inputs lose their own digits)
     scale = 0.09 if size < 1 else 0.09 / size
     check_case(tq, (fk, fv, bt, kc, vc, kr, vr, q, pr), scale, True, 0, h_of(dtype))
+
+
+# ------------------------------------------------------------------ precision
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [1, 8])
+def test_one_key_gives_its_value_rounded_once(tq, d, G):
+    """One key has weight one: the output is its value. Four centroids are next to exact in the tables (below a hundredth of
+    2^-12, which Pi, keeping lengths, makes 2.4e-6 of the value's length at most), sums of d products in fp32 cost at most
+    23 * 2^-24 of it; beyond that the output may only be rounded to its type."""
+    fk, fv = fmt(tq, d, "mse2", 0), fmt(tq, d, "mse2", 1)
+    lens = [1] * 40
+    bt, kc, vc, kr, vr = cached(tq, fk, fv, [1] * 40, lens, 16, 2, [heads(b, 1, 2, d) for b in range(40)], [heads(99 + b, 1, 2, d) for b in range(40)])
+    q = heads(3, bt.ntok, 2 * G, d, torch.float16, outliers=False)
+    got = tq.attn_paged(fk.handle, fv.handle, q, kc, vc, bt, 0.09)
+    assert fk.handle.status() == tq.TQ_OK
+    want = torch.stack([fv.rotated(*r)[0][0] @ fv.Pi for r in vr]).repeat_interleave(G, 1)
+    room = 2.0 ** -11 * want.abs() + (2.4e-6 + 23 * 2.0 ** -24) * want.norm(dim=-1, keepdim=True) + 2.0 ** -25
+    assert ((got.double() - want).abs() <= room).all()
