@@ -19,7 +19,8 @@ struct tq_view {
   int d, bits, m, norm_dtype, codes_B, signs_B, device, polar;
   const float *PiT, *Pi, *MT, *ST, *S, *cent, *bnd;   // fp32: [d][d], [d][d], [d][m], [d][m], [m][d], centroids, boundaries
   const double* t64;       // d <= 256: Pi [d][d], S [m][d], M [m][d], 16 boundaries (+inf padded), 16 centroids
-  const uint8_t* ops16;    // d = 64 or 128 (m = 0 or d): f16 operands, of the paged expansion (tq_api.cu); NULL otherwise
+  // d = 64 or 128 (m = 0 or d): f16 operands of the paged expansion, for keys and for values (tq_api.cu); NULL otherwise
+  const uint8_t *ops16k, *ops16v;
   const uint8_t* ops_app;  // d = 64 or 128 (m = 0 or d), with codes: f16 pairs of Pi and M (tq_api.cu); NULL otherwise
   float m_abs, m_norm;     // largest row of M in the 1-norm and the 2-norm
   float cent_up;           // the factor in [1, 2) with which the centroids come nearest to f16 (table_factor in tq_api.cu)

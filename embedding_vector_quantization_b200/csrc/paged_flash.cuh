@@ -11,11 +11,12 @@
 //           attention multiplies scores and weights by the norms of its 128 tokens;
 //   flash   softmax(scale q k^T) v over those tiles with the running maximum and sum of each row;
 //   merge   items that several CTAs shared.
-// Keys and values come back in the original basis, so queries and outputs need no rotation, and signs cost no wider
-// contraction: 4 d flops per (query row, key) for every format, where contracting the codes themselves would take
+// Values come back in the original basis, so outputs need no rotation; keys times a Hadamard matrix, as the queries are: a channel
+// far larger than the others would have its coordinate's rounding to f16 decide the scores, which the Hadamard matrix spreads
+// over all coordinates. Signs cost no wider contraction: 4 d flops per (query row, key) for every format, where contracting the codes themselves would take
 // 2 (2 d + m_k + m_v). The f16 rows are written and read once through L2 (512 B per token and head at d = 128).
 //
-// Roundings: c[idx] (hardly: table_factor in tq_api.cu), Pi, S, rnorm / norm, x_hat, the prepared query (scaled by a power of two below 1) and the weights
+// Roundings: c[idx] (hardly: table_factor in tq_api.cu), Pi with signs (an f16 pair without), S, rnorm / norm, x_hat, the prepared query (scaled by a power of two below 1) and the weights
 // to f16 (11 bits; outputs have 8 or 11); every sum, maximum and exponent in fp32.
 //
 // Measured at 8 KV heads, 32 query heads, d = 128: a chunk of 1024 tokens over 32768 with signs takes 680 us (expansion 80,
@@ -479,7 +480,7 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
     *abort_flag = 1;
     report_error(a.err, kErrTimeout);
   };
-  const int katoms = (D + Q.m) / 64;   // 64-wide slices of the contraction
+  constexpr int katoms = 2 * (D / 64);   // 64-wide slices of the contraction: codes and signs, or codes twice
 
   if (warp < 8) {
     // ---- operand rows: thread = token of the tile. Under way at a time: the page of the token after next, the next row.
@@ -641,7 +642,8 @@ __global__ void __launch_bounds__(kExThreads, 1) paged_expand_kernel(FlashArgs a
       for (int k = 0; k < katoms; ++k)
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-          const uint64_t x = ad + ((k * kAtomRows + kk * 32) >> 4), y = b_desc + ((k * kAtomOp + kk * 32) >> 4);
+          const int ka = Q.m > 0 ? k : k & (D / 64 - 1);
+          const uint64_t x = ad + ((ka * kAtomRows + kk * 32) >> 4), y = b_desc + ((k * kAtomOp + kk * 32) >> 4);
           if (k == 0 && kk == 0) mma_ss<false>(lead, tmem + s * 128, x, y, flash_idesc(D, false));
           else mma_ss<true>(lead, tmem + s * 128, x, y, flash_idesc(D, false));
         }
@@ -774,15 +776,33 @@ __global__ void __launch_bounds__(kQtThreads) paged_qtile_kernel(FlashArgs a) {
   int e = 0;
   if (top > 0.f && top < INFINITY) frexpf(top, &e);
   e = max(-126, min(126, e + 1));
+  // Coordinates below one, then times the Hadamard matrix (over the bits of the coordinate's number: three within a chunk, two of
+  // the lane, the rest of the chunk), as the keys' rows are.
   const float sc = a.scale < 0.f ? -ldexpf(1.f, -e) : ldexpf(1.f, -e);
-  if (ql == 0) a.p.qfactor[slot * kItemRows + r] = ok || !live ? ldexpf(fabsf(a.scale) * 1.44269504089f, e) : -1.f;
+  if (ql == 0) a.p.qfactor[slot * kItemRows + r] = ok || !live ? ldexpf(fabsf(a.scale) * (0.125f * 1.44269504089f), e) : -1.f;
+#pragma unroll
+  for (int x = 0; x < 8 * C; ++x) z[x] *= sc;
+#pragma unroll
+  for (int w = 1; w < 8 * C; w *= 2)
+#pragma unroll
+    for (int x = 0; x < 8 * C; ++x)
+      if (!(x & w)) {
+        const float p = z[x], o = z[x + w];
+        z[x] = p + o, z[x + w] = p - o;
+      }
+#pragma unroll
+  for (int w = 1; w < 4; w *= 2) {
+    const float sign = ql & w ? -1.f : 1.f;
+#pragma unroll
+    for (int x = 0; x < 8 * C; ++x) z[x] = fmaf(sign, z[x], __shfl_xor_sync(0xffffffffu, z[x], w));
+  }
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int ch = ql + 4 * c;
     *reinterpret_cast<uint4*>(a.p.qrows + ((2 * slot + (r >> 7)) * (D / 64) + (ch >> 3)) * kAtomRows + (r & 127) * 128 +
                               (((ch & 7) ^ (r & 7)) << 4)) =
-        make_uint4(half2_bits(z[8 * c] * sc, z[8 * c + 1] * sc), half2_bits(z[8 * c + 2] * sc, z[8 * c + 3] * sc),
-                   half2_bits(z[8 * c + 4] * sc, z[8 * c + 5] * sc), half2_bits(z[8 * c + 6] * sc, z[8 * c + 7] * sc));
+        make_uint4(half2_bits(z[8 * c], z[8 * c + 1]), half2_bits(z[8 * c + 2], z[8 * c + 3]),
+                   half2_bits(z[8 * c + 4], z[8 * c + 5]), half2_bits(z[8 * c + 6], z[8 * c + 7]));
   }
   if (item == 0 && h == 0) grid_dep_wait();   // what follows may count on the expansion: this kernel ends behind it
 }
@@ -1138,8 +1158,10 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
       const int key_first = (lo_all / kKT + s.lo_tile) * kKT;
       // Running reference (log2) and sum of the weights. The value sums have a unit of their own, 2^(m + b), which follows what the
       // row's weights and the value tiles' exponents make together: a large value that the row hardly sees costs it nothing.
-      // m and b are whole numbers, and what is formed of them stays exact. limit: what a score may be without moving m (-infinity
-      // while there is no unit; NaN where |m| is above 2^20, whose tiles all take the rare part below); rest: -(m + b), or 0.
+      // Where b is set it is a whole number, so that a row's largest weight comes out as a power of two, exact in f16; where m
+      // moves, b makes up for it (sums that kept to whole numbers would have to be scaled then: 565 -> 609 us). limit: what a
+      // score may be without moving m (-infinity while there is no unit; NaN where |m| is above 2^14, whose tiles all take the
+      // rare part below); rest: -(m + b), or 0.
       float m = -INFINITY, l = 0.f, b = -INFINITY, limit = -INFINITY, rest = 0.f;
       int ke = a.p.ke[te + s.t0], ve = a.p.ve[te + s.t0];
       uint4 seen = *reinterpret_cast<const uint4*>(a.p.seen + 4 * (tile0 + s.t0));
@@ -1234,9 +1256,8 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
           const float2 other = *theirs;
           const float both = max_nan(top, other.x);
           if (!(both <= m + 8.f)) {
-            const float now = ceilf(both);
-            if (m > -INFINITY) l *= ex2(m - now), b += m - now;
-            m = now;
+            if (m > -INFINITY) l *= ex2(m - both), b += m - both;
+            m = both;
           }
           const float most = m == -INFINITY ? -INFINITY : max_nan((top - m) + top_o, (other.x - m) + other.y);
           float f = 1.f;
@@ -1262,11 +1283,11 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
           named_sync(1 + i, 256);   // the exchanged maxima have been read
           const float m_ref = m == -INFINITY ? 0.f : m, b_ref = b == -INFINITY ? 0.f : b;
           rest = b == -INFINITY ? 0.f : -(m + b);
-          limit = b == -INFINITY ? -INFINITY : fabsf(m) <= 1048576.f ? m + 8.f : NAN;
+          limit = b == -INFINITY ? -INFINITY : fabsf(m) <= 16384.f ? m + 8.f : NAN;
           rv = ev + rest;
           if (v_apart) {
             odd = true, c = 1.f, rv = (top_ref - m_ref) - b_ref, sum *= ex2(top_ref - m_ref);
-          } else if (__any_sync(0xffffffffu, b - ev > 40.f || fabsf(m_ref) > 1048576.f)) {
+          } else if (__any_sync(0xffffffffu, b - ev > 40.f || fabsf(m_ref) > 16384.f)) {
             odd = true, rv = ev - b_ref;
 #pragma unroll
             for (int x = 0; x < 64; ++x) {

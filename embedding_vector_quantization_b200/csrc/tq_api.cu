@@ -366,17 +366,36 @@ int create_common(int d, int bits_mse, int m, uint64_t seed, int norm_dtype, tq_
   std::vector<double> t64;
   std::vector<uint8_t> ops16;
   if ((d == 64 || d == 128) && (m == 0 || m == d)) {
-    // f16 operand of the paged expansion: x_hat_i = sum_k A_k B[i][k], k < d: Pi[k][i]; then sqrt(pi/2)/m S[j][i] with
-    // the projections j of each 32 in the order 0 16 1 17 ... 15 31; slices of 64 k: d rows of 128 swizzled bytes
-    ops16.resize((size_t)(d + m) / 64 * d * 128);
-    for (int i = 0; i < d; ++i)
-      for (int k = 0; k < d + m; ++k) {
-        const int p = k - d, j = p < 0 ? 0 : (p & ~31) + ((p & 31) >> 1) + 16 * (p & 1);
-        const double v = p < 0 ? h->Pi[(size_t)k * d + i] : std::sqrt(M_PI / 2.0) / m * h->S[(size_t)j * d + i];
-        const uint16_t bits = __half_as_ushort(__double2half(v));
-        const size_t off = (size_t)(k >> 6) * d * 128 + (size_t)i * 128 + (size_t)((((k & 63) >> 3) ^ (i & 7)) << 4) + (k & 7) * 2;
-        std::memcpy(&ops16[off], &bits, 2);
+    // f16 operands of the paged expansion: x_hat_i = sum_k A_k B[i][k], k < d: Pi[k][i]. Then, with signs, sqrt(pi/2)/m S[j][i]
+    // for the projections j of each 32 in the order 0 16 1 17 ... 15 31; without, what Pi's rounding to f16 left of it.
+    // Slices of 64 k: d rows of 128 swizzled bytes. The values' come first; the keys' have every row of Pi and S times the
+    // Hadamard matrix and 2^-3 (d = 64) or 2^-4 (paged_flash.cuh).
+    const size_t half = (size_t)2 * (d / 64) * d * 128;
+    ops16.resize(2 * half);
+    std::vector<double> Pi(h->Pi), S(h->S);
+    auto hadamard = [&](std::vector<double>& rows) {
+      for (size_t r = 0; r < rows.size(); r += d) {
+        for (int w = 1; w < d; w *= 2)
+          for (int i = 0; i < d; ++i)
+            if (!(i & w)) {
+              const double x = rows[r + i], y = rows[r + i + w];
+              rows[r + i] = x + y, rows[r + i + w] = x - y;
+            }
+        for (int i = 0; i < d; ++i) rows[r + i] *= d == 64 ? 0.125 : 0.0625;
       }
+    };
+    for (int keys = 0; keys < 2; ++keys) {
+      if (keys) hadamard(Pi), hadamard(S);
+      for (int i = 0; i < d; ++i)
+        for (int k = 0; k < 2 * d; ++k) {
+          const int p = k - d, j = p < 0 ? 0 : (p & ~31) + ((p & 31) >> 1) + 16 * (p & 1);
+          double v = Pi[(size_t)(k % d) * d + i];
+          if (p >= 0) v = m ? std::sqrt(M_PI / 2.0) / m * S[(size_t)j * d + i] : v - (double)__half2float(__double2half(v));
+          const uint16_t bits = __half_as_ushort(__double2half(v));
+          const size_t off = (size_t)(k >> 6) * d * 128 + (size_t)i * 128 + (size_t)((((k & 63) >> 3) ^ (i & 7)) << 4) + (k & 7) * 2;
+          std::memcpy(&ops16[keys * half + off], &bits, 2);
+        }
+    }
   }
   // f16 pairs of the paged append, K-major in slices of 64 k as above: Pi 2^8 (high, low), M 2^5 (high, low)
   std::vector<uint8_t> ops_app;
@@ -1115,7 +1134,7 @@ void tq_internal_view(const tq_handle* h, tq_view* v) {
   v->d = h->d, v->bits = h->bits, v->m = h->m, v->norm_dtype = h->norm_dtype;
   v->codes_B = h->codes_B, v->signs_B = h->signs_B, v->device = h->device, v->polar = h->polar;
   v->PiT = h->dPiT, v->Pi = h->dPi, v->MT = h->dMT, v->ST = h->dST, v->S = h->dS, v->cent = h->dcent, v->bnd = h->dbnd;
-  v->t64 = h->d64, v->ops16 = h->dOps16, v->ops_app = h->dOpsApp, v->m_abs = h->m_abs, v->m_norm = h->m_norm, v->cent_up = h->cent_up, v->err = h->derr;
+  v->t64 = h->d64, v->ops16v = h->dOps16, v->ops16k = h->dOps16 ? h->dOps16 + (size_t)2 * (h->d / 64) * h->d * 128 : nullptr, v->ops_app = h->dOpsApp, v->m_abs = h->m_abs, v->m_norm = h->m_norm, v->cent_up = h->cent_up, v->err = h->derr;
   v->cent_h = h->cent.data(), v->bnd_h = h->bnd.data();
 }
 int tq_internal_ok() { return ok(); }

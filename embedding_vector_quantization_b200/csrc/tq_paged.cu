@@ -303,7 +303,7 @@ int attn_simt(AttnArgs& a, const tq_view& k, const tq_view& v, const SimtPlan& p
 // ---------------------------------------------------------------- attention of chunks, tensor cores
 
 // 16-bit queries, d = 64 or 128, d signs or none (those handles hold the operands).
-bool flash_formats(const tq_view& k, const tq_view& v) { return k.ops16 && v.ops16 && !simt_forced(); }
+bool flash_formats(const tq_view& k, const tq_view& v) { return k.ops16k && v.ops16v && !simt_forced(); }
 
 struct FlashPlan {
   int64_t max_seqs, max_tiles, max_items;
@@ -359,7 +359,7 @@ int attn_flash(const AttnArgs& g, const tq_view& k, const tq_view& v, const Flas
     return st;
   FlashArgs a{};
   a.q = g.q, a.q_stride = g.q_stride, a.q_dtype = g.q_dtype, a.Hq = g.Hq, a.Hkv = g.Hkv, a.G = g.G;
-  a.bt = g.bt, a.prep = g.prep, a.kq = g.k, a.vq = g.v, a.kc = g.kc, a.vc = g.vc, a.kops = k.ops16, a.vops = v.ops16;
+  a.bt = g.bt, a.prep = g.prep, a.kq = g.k, a.vq = g.v, a.kc = g.kc, a.vc = g.vc, a.kops = k.ops16k, a.vops = v.ops16v;
   a.scale = g.scale, a.causal = g.causal, a.window = g.window, a.small_rows = small_rows, a.ctas = p.ctas;
   a.out = g.out, a.err = g.err;
   auto ints = [&](size_t off) { return reinterpret_cast<int*>(ws + off); };
