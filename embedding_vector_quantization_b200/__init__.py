@@ -296,7 +296,7 @@ def _head_rows(x, name, ntok, d):
 
 def _check_paged(hk, hv, kcache, vcache, batch, prep):
     for h, own in ((hk, kcache.handle), (hv, vcache.handle)):
-        if h is not own and (h.codes_B, h.signs_B, h.norm_dtype, h.prod) != (own.codes_B, own.signs_B, own.norm_dtype, own.prod):
+        if h is not own and (h.d, h.bits_mse, h.m, h.norm_dtype) != (own.d, own.bits_mse, own.m, own.norm_dtype):
             _need(False, "a cache was made for rows of another format than its handle's")
     d = hk.d
     if kcache.Hkv != vcache.Hkv:

@@ -324,6 +324,21 @@ def test_queries_of_any_size(tq, news, prep, size, kf, dtype):
     check_case(tq, (fk, fv, bt, kc, vc, kr, vr, q, pr), scale, True, 0, h_of(dtype))
 
 
+# ------------------------------------------------------------------ handles and caches
+
+
+def test_caches_of_another_shape_with_rows_as_wide_are_refused(tq):
+    """64 coordinates of 4 bits and 128 of 2 have rows of one size and are still not the same rows."""
+    fa, fb = fmt(tq, 128, "mse2", 0), fmt(tq, 64, "mse4", 0)
+    bt = pu.make_batch(tq, [1], [20], 16)
+    q = heads(1, 1, 4, 128, torch.bfloat16)
+    ca, cb = pu.garbage_cache(tq, fa, bt, 2, 1), pu.garbage_cache(tq, fb, bt, 2, 1)
+    assert fa.handle.codes_B == fb.handle.codes_B
+    for kc, vc in ((cb, ca), (ca, cb), (cb, cb)):
+        with pytest.raises(tq.TQError, match="another format"):
+            tq.attn_paged(fa.handle, fa.handle, q, kc, vc, bt, 0.09)
+        with pytest.raises(tq.TQError, match="another format"):
+            tq.append_paged(fa.handle, fa.handle, q[:, :2], q[:, 2:], kc, vc, bt)
 # ------------------------------------------------------------------ precision
 
 
