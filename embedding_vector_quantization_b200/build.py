@@ -6,6 +6,8 @@ The shared library lands next to this file so the Python binding (and any
 copy of the repository) finds it without installation.
 """
 
+import fcntl
+import hashlib
 import os
 import subprocess
 import sys
@@ -16,6 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libtq.so")
 SOURCES = ["tq_api.cu", "tq_noalloc.cu", "tq_paged.cu", "host_math.cpp"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
+FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3", "--expt-relaxed-constexpr"]
 
 
 def _nvcc():
@@ -32,48 +35,88 @@ def _newest_source_mtime():
     return newest
 
 
-def _stale(obj, dep):
-    """Whether an object file is missing or older than a file it was made from (nvcc's dependency file)."""
-    if not (os.path.exists(obj) and os.path.exists(dep)):
+def _key():
+    """What an object depends on besides its files: the compiler's version and the flags (None: there is no compiler)."""
+    try:
+        version = subprocess.run([_nvcc(), "--version"], check=True, capture_output=True, text=True).stdout
+    except (OSError, subprocess.CalledProcessError):
+        return None
+    return hashlib.sha256("\n".join([version, *ARCH, *FLAGS]).encode()).hexdigest()
+
+
+def _read(path):
+    try:
+        with open(path) as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
+def _stale(obj, dep, key):
+    """Whether an object file is missing, made with other flags or another compiler, or older than a file it was made from
+    (nvcc's dependency file)."""
+    if not (os.path.exists(obj) and os.path.exists(dep)) or _read(obj + ".key") != key:
         return True
-    with open(dep) as f:
-        names = f.read().replace("\\\n", " ").split(":", 1)[1].split()
+    names = _read(dep).replace("\\\n", " ").split(":", 1)[1].split()
     at = os.path.getmtime(obj)
     return any(not os.path.exists(n) or os.path.getmtime(n) > at for n in names)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compiles libtq.so if missing or older than any source; returns its path.
+def _fresh(key):
+    return (os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest_source_mtime()
+            and (key is None or _read(os.path.join(HERE, "_build", "libtq.key")) == key))
 
-    Each source has its own object file under _build/, compiled at the same time as the others and only
-    when something it includes is newer.
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Compiles libtq.so if it is missing, older than any source or made with other flags or another compiler; returns its path.
+
+    Each source has its own object file under _build/, compiled at the same time as the others and only when something it
+    includes is newer. One process at a time builds (others wait, and find it done); every file appears under its name
+    only when it is whole.
     """
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest_source_mtime():
+    key = _key()
+    if not force and _fresh(key):
         return LIB
+    if key is None:
+        raise RuntimeError(f"{LIB} is missing or older than its sources, and there is no nvcc to build it")
     objs = os.path.join(HERE, "_build")
     os.makedirs(objs, exist_ok=True)
-    flags = [*ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
-             "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include"), "-I", CSRC]
+    with open(os.path.join(objs, "lock"), "w") as lock:
+        fcntl.flock(lock, fcntl.LOCK_EX)
+        if not force and _fresh(key):
+            return LIB
+        _compile(objs, key, force, verbose)
+    return LIB
+
+
+def _compile(objs, key, force, verbose):
+    flags = [*ARCH, *FLAGS, "-I", os.path.join(ROOT, "include"), "-I", CSRC]
     running, made = [], []
     for src in SOURCES:
         obj = os.path.join(objs, src + ".o")
-        dep = obj + ".d"
         made.append(obj)
-        if not force and not _stale(obj, dep):
+        if not force and not _stale(obj, obj + ".d", key):
             continue
-        cmd = [_nvcc(), *flags, "-MD", "-MF", dep, "-c", os.path.join(CSRC, src), "-o", obj]
+        cmd = [_nvcc(), *flags, "-MD", "-MF", obj + ".d.tmp", "-c", os.path.join(CSRC, src), "-o", obj + ".tmp"]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
             print(" ".join(cmd), file=sys.stderr)
-        if os.path.exists(obj):
-            os.remove(obj)
-        running.append((cmd, subprocess.Popen(cmd)))
-    failed = [cmd for cmd, p in running if p.wait() != 0]
+        running.append((obj, cmd, subprocess.Popen(cmd)))
+    failed = []
+    for obj, cmd, p in running:
+        if p.wait() != 0:
+            failed.append(cmd)
+            continue
+        os.replace(obj + ".d.tmp", obj + ".d")
+        os.replace(obj + ".tmp", obj)
+        with open(obj + ".key", "w") as f:
+            f.write(key)
     if failed:
         raise subprocess.CalledProcessError(1, failed[0])
     subprocess.run([_nvcc(), *ARCH, "-shared", *made, "-o", LIB + ".tmp"], check=True)
     os.replace(LIB + ".tmp", LIB)
-    return LIB
+    with open(os.path.join(objs, "libtq.key"), "w") as f:
+        f.write(key)
 
 
 if __name__ == "__main__":
