@@ -25,7 +25,6 @@ struct tq_view {
   float m_abs, m_norm;     // largest row of M in the 1-norm and the 2-norm
   float cent_up;           // the factor in [1, 2) with which the centroids come nearest to f16 (table_factor in tq_api.cu)
   int* err;                // device error word
-  const double *cent_h, *bnd_h;   // host copies
 };
 __attribute__((visibility("hidden"))) void tq_internal_view(const tq_handle* h, tq_view* v);
 __attribute__((visibility("hidden"))) int tq_internal_ok();

@@ -155,7 +155,6 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(AppendArgs a) {
 
   rows_matvec<R, NT>(zf, d, Q.PiT, d, part_s, ys);
   // indices; a coordinate within the band of a border is computed again by the whole warp
-  const float* one = cf;
   for (int e0 = warp * 32; e0 < R * d; e0 += NT) {   // d % 32 = 0: the warp stays in one row
     const int e = e0 + lane, r = e / d;
     const double n = nrm[r];
@@ -179,7 +178,7 @@ __global__ void __launch_bounds__(NT) paged_append_kernel(AppendArgs a) {
       }
     }
     idx[e] = (uint8_t)k;
-    const float err = n > 0.0 ? y - one[k] : 0.f;
+    const float err = n > 0.0 ? y - cf[k] : 0.f;
     zf[e] = err;                 // e: every read of z (fp32) is behind the product's barrier
     if (m > 0) {
       float q = err * err;

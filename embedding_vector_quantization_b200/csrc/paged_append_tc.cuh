@@ -68,18 +68,6 @@ struct AppendTcArgs {
   int* err;
 };
 
-// Whether a barrier's phase has ended, without waiting (the caller counts its polls; as many as a second takes).
-constexpr int kPollLimit = 1 << 23;
-__device__ __forceinline__ bool test_bar(uint32_t bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(done)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return done;
-}
-
 // The sum of squares of a row that four lanes hold, times f^2. Eights are summed in fp32 and those in fp64: a norm stored in fp32 is off
 // by half a step for the root, a quarter for this result's rounding and about 0.15 for the eights (one sum of 32 in fp32: a
 // step more).

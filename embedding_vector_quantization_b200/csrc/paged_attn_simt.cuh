@@ -29,7 +29,7 @@ struct AttnArgs {
   Quant k, v;
   CacheView kc, vc;
   float scale;
-  int causal, window, nsplit, tile_rows;
+  int causal, window, nsplit;
   int small_rows;  // the single-token kernels: sequences with at most this many query rows
   float* qr;       // [ntok * Hq][dk] rotated queries (general kernels)
   float* part;     // partial results
@@ -152,7 +152,6 @@ __global__ void __launch_bounds__(kAppThreads) paged_qprep_kernel(AttnArgs a) {
 __device__ __forceinline__ void expand_rows(const Quant& Q, const CacheView& c, const int64_t* at, const float* cf, float* dst,
                                             int ld) {
   const int d = Q.d, m = Q.m, wd = (d + m) / 32;   // 32 coordinates at a time
-  const float tail = 1.f;
   for (int e = threadIdx.x; e < kKeyTile * wd; e += kAttThreads) {
     const int t = e / wd, u = e - t * wd;
     const int64_t row = at[t];
@@ -170,7 +169,7 @@ __device__ __forceinline__ void expand_rows(const Quant& Q, const CacheView& c, 
         for (int i = 0; i < 32; ++i) o[i] = n * cf[packed_field(words, 32 * u + i, Q.bits)];
       }
     } else {
-      const float w = (Q.bits == 0 ? n : __half2float(c.rnorms[row])) * tail;
+      const float w = Q.bits == 0 ? n : __half2float(c.rnorms[row]);
       const uint32_t s = reinterpret_cast<const uint32_t*>(c.signs + row * Q.signs_B)[u - d / 32];
       for (int i = 0; i < 32; ++i) o[i] = (s >> i) & 1 ? w : -w;
     }
@@ -298,7 +297,7 @@ __device__ __forceinline__ void store_any(void* p, int dtype, int64_t i, float v
 __global__ void __launch_bounds__(kAppThreads) paged_combine_simt_kernel(AttnArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   constexpr int R = kTileRows;
-  const int d = a.v.d, m = a.v.m, dv = d + m, w = max(d, m);
+  const int d = a.v.d, m = a.v.m, dv = d + m;
   float* acc = reinterpret_cast<float*>(smem);        // [8][d], then [8][m]
   float* acc2 = acc + R * d;
   float* o1 = acc2 + R * m;                           // [8][d]
@@ -336,7 +335,6 @@ __global__ void __launch_bounds__(kAppThreads) paged_combine_simt_kernel(AttnArg
     if (m > 0) v = fmaf(kQjlScale / (float)m, o2[e], v);
     store_any(a.out, a.q_dtype, ((tok0 + row / a.G) * a.Hq + hk * a.G + row % a.G) * d + i, v * f[r]);
   }
-  (void)w;
 }
 
 }  // namespace paged

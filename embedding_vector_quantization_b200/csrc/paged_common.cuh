@@ -38,7 +38,6 @@ struct Quant {
   const float *PiT, *Pi, *MT, *ST, *S, *cent, *bnd;
   const double* t64;
   float m_abs, m_norm, cent_up;
-  __host__ __device__ bool qjl_only() const { return m > 0 && bits == 0; }
   __device__ const double* Pi64() const { return t64; }
   __device__ const double* S64() const { return t64 + (size_t)d * d; }
   __device__ const double* M64() const { return t64 + (size_t)d * d + (size_t)m * d; }

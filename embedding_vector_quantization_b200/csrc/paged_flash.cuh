@@ -37,8 +37,6 @@ using etc::bar_arrive;
 using etc::bulk_load;
 using etc::expect_tx;
 using etc::lds128;
-using etc::mma_commit;
-using etc::mma_f16;
 using etc::named_sync;
 using etc::sts128;
 using etc::sw128_desc;

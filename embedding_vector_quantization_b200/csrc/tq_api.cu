@@ -1135,7 +1135,6 @@ void tq_internal_view(const tq_handle* h, tq_view* v) {
   v->codes_B = h->codes_B, v->signs_B = h->signs_B, v->device = h->device, v->polar = h->polar;
   v->PiT = h->dPiT, v->Pi = h->dPi, v->MT = h->dMT, v->ST = h->dST, v->S = h->dS, v->cent = h->dcent, v->bnd = h->dbnd;
   v->t64 = h->d64, v->ops16v = h->dOps16, v->ops16k = h->dOps16 ? h->dOps16 + (size_t)2 * (h->d / 64) * h->d * 128 : nullptr, v->ops_app = h->dOpsApp, v->m_abs = h->m_abs, v->m_norm = h->m_norm, v->cent_up = h->cent_up, v->err = h->derr;
-  v->cent_h = h->cent.data(), v->bnd_h = h->bnd.data();
 }
 int tq_internal_ok() { return ok(); }
 bool tq_internal_fault(const char* what) { return fault_is(what); }

@@ -283,7 +283,6 @@ int attn_simt(AttnArgs& a, const tq_view& k, const tq_view& v, const SimtPlan& p
   a.qr = reinterpret_cast<float*>(ws + p.qr);
   a.part = reinterpret_cast<float*>(ws + p.part);
   a.nsplit = p.nsplit;
-  a.tile_rows = kTileRows;
   {
     tq_launch_scope scope("paged_qprep", s);
     paged_qprep_kernel<R><<<(unsigned)((a.bt.ntok * a.Hq + R - 1) / R), kAppThreads, qprep_smem_bytes(k.d, k.m, R), s>>>(a);
