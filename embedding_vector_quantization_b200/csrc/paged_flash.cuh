@@ -1214,8 +1214,7 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
         if (bar_any(1 + i, 256, k_apart || v_apart || !(top <= limit && top + rv <= 12.f && gap <= 40.f))) {
           if (k_apart) {
             const float4* n = reinterpret_cast<const float4*>(a.p.kn + (te + j) * kKT + 64 * half);
-            c = fmaxf(qscale, 1e-37f);
-            top = -INFINITY;
+            c = 1.f, top = -INFINITY;
 #pragma unroll
             for (int x = 0; x < 16; ++x) {
               const float4 w4 = n[x];
@@ -1223,11 +1222,10 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 uint32_t& y = v[x >> 3][4 * (x & 7) + k];
-                if (y != 0xff800000u) y = __float_as_uint(__uint_as_float(y) * w[k]);   // (masked)
+                if (y != 0xff800000u) y = __float_as_uint(__uint_as_float(y) * (w[k] * qscale));   // (masked)
                 top = max_nan(top, __uint_as_float(y));
               }
             }
-            top *= c;
           }
           // the largest weight times value norm, log2, relative to this half's largest weight
           float top_o = ev, sum = 0.f;

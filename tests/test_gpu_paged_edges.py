@@ -232,6 +232,20 @@ def test_norms_spread_over_their_type(tq, news, norm, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("scale", [0.0, 1e-38, -3e-38])
+@pytest.mark.parametrize("news", [[1, 2], [100, 50]])
+def test_scales_that_make_up_for_the_keys_norms(tq, news, scale, dtype):
+    """Keys of norms up to 1e37 under a scale as small, or of zero, which averages."""
+    fk, fv = fmt(tq, 128, "mse4", 0, "f32"), fmt(tq, 128, "mse4", 1, "f32")
+    lens, g = [700, 130], torch.Generator().manual_seed(6)
+    k = [heads(1 + b, L, 2, 128, outliers=False) * torch.exp2(120 * torch.rand(L, 2, 1, generator=g).double()).cuda() for b, L in enumerate(lens)]
+    v = [heads(9 + b, L, 2, 128, outliers=False) for b, L in enumerate(lens)]
+    bt, kc, vc, kr, vr = cached(tq, fk, fv, news, lens, 16, 2, k, v)
+    q = heads(3, bt.ntok, 4, 128, DT[dtype], outliers=False)
+    check_case(tq, (fk, fv, bt, kc, vc, kr, vr, q, None), scale, True, 0, h_of(dtype))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("what", [float("inf"), float("nan")])
 @pytest.mark.parametrize("kf,vf", [("mse4", "mse4"), ("prod3", "prod3"), ("mse3", "qjl")])
 @pytest.mark.parametrize("news,lens,window", [([5], [40], 0), ([3, 1], [200, 17], 20), ([60, 70], [90, 300], 0), ([80], [400], 50)])
