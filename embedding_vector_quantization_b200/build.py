@@ -52,14 +52,14 @@ def _read(path):
         return ""
 
 
-def _stale(obj, dep, key):
-    """Whether an object file is missing, made with other flags or another compiler, or older than a file it was made from
-    (nvcc's dependency file)."""
+def _stale(src, obj, dep, key):
+    """Whether a source's object file is missing, made with other flags, by another compiler or from another copy of the tree, or
+    older than a file it was made from (nvcc's dependency file)."""
     if not (os.path.exists(obj) and os.path.exists(dep)) or _read(obj + ".key") != key:
         return True
     names = _read(dep).replace("\\\n", " ").split(":", 1)[1].split()
     at = os.path.getmtime(obj)
-    return any(not os.path.exists(n) or os.path.getmtime(n) > at for n in names)
+    return src not in names or any(not os.path.exists(n) or os.path.getmtime(n) > at for n in names)
 
 
 def _fresh(key):
@@ -93,11 +93,11 @@ def _compile(objs, key, force, verbose):
     flags = [*ARCH, *FLAGS, "-I", os.path.join(ROOT, "include"), "-I", CSRC]
     running, made = [], []
     for src in SOURCES:
-        obj = os.path.join(objs, src + ".o")
+        path, obj = os.path.join(CSRC, src), os.path.join(objs, src + ".o")
         made.append(obj)
-        if not force and not _stale(obj, obj + ".d", key):
+        if not force and not _stale(path, obj, obj + ".d", key):
             continue
-        cmd = [_nvcc(), *flags, "-MD", "-MF", obj + ".d.tmp", "-c", os.path.join(CSRC, src), "-o", obj + ".tmp"]
+        cmd = [_nvcc(), *flags, "-MD", "-MF", obj + ".d.tmp", "-c", path, "-o", obj + ".tmp"]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
             print(" ".join(cmd), file=sys.stderr)

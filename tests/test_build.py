@@ -120,6 +120,18 @@ def test_two_processes_build_once(tree):
         assert (pkg / "_build" / (name + ".o")).read_text().startswith("whole")
 
 
+def test_a_copied_tree_compiles_its_own_sources(tree, tmp_path):
+    pkg, cuda = tree
+    load(pkg).build()
+    compiled(cuda)
+    shutil.copytree(tmp_path / "repo", tmp_path / "copy")   # objects and their lists of files too
+    other = tmp_path / "copy" / "pkg"
+    now = time.time() + 5
+    os.utime(other / "csrc" / "common.cuh", (now, now))
+    load(other).build()
+    assert compiled(cuda) == ALL
+
+
 def test_without_a_compiler_a_fresh_library_is_taken(tree, monkeypatch):
     pkg, cuda = tree
     b = load(pkg)
