@@ -8,9 +8,10 @@
 //   indices (thread = row), e = y - c[idx]; sign rows: e times 2^10 as an f16 pair into tensor memory,
 //   D2 = e M^T         three contractions again, the e pair as the operand in tensor memory;
 //   signs of D2.
-// Bound by the preparation: its loads of positions, pages, cosines and vectors depend on one another, and two tiles of two
-// stages do not hide them (tensor pipe 21 %, ALU 45 % busy). 8 heads x 16384 tokens of bf16 with rotation and signs, keys and values:
-// 126 us warm, 131 cold, where the bytes alone would take 14.
+// Bound by the preparation: its loads of positions, pages, cosines and vectors depend on one another, and one tile's places and
+// vectors ahead (two without signs or at d = 64) do not hide them (tensor pipe 21 %, ALU 45 % busy). 8 heads x 16384 tokens of
+// bf16 with rotation and signs, keys and values: 122 us warm, 131 cold, 9 us for each of a CTA's 14 tiles, where the bytes
+// alone would take 14. The contractions are issued in a fixed order, the next tile's first before this tile's second.
 // Two tiles are under way at a time, each with its own 256 columns: D1, then D2 in the same 128; e_h and e_l in the others.
 //
 // Exactness. A coordinate closer to a border than kTcBandY, and a sign closer to 0 than kTcBandS, is computed again by its

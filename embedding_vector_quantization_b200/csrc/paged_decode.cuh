@@ -6,9 +6,9 @@
 // share a pass over the packed rows; more come in eights, each with its own pass.
 //
 // What has to be moved are the packed rows, so they go from the page to the tensor cores' registers with as few
-// instructions as possible. Even so it is the instructions that bound it, about 490 per 16 tokens (mse4, d = 128): 32
-// sequences of up to 16384 keys, 4 KV heads, take 71 us with issue slots 58 %, ALU 51 % and LSU 50 % busy, tensor pipe
-// 16 %, where the bytes alone would take 25; 128 registers a thread leave 16 warps on an SM.
+// instructions as possible. Even so it is the instructions that bound it, about 510 per 16 tokens (mse4, d = 128): 32
+// sequences of up to 16384 keys, 4 KV heads, take 73 us with issue slots 57 %, ALU 50 % and LSU 48 % busy, tensor pipe
+// 15 %, where the bytes alone would take 25; 128 registers a thread leave 16 warps on an SM.
 // A chunk is 16 tokens of one page (pages are multiples of 16): its codes, signs and norms are contiguous, and a warp
 // streams its chunks through a ring of its own with 16-byte asynchronous copies. Scores are
 // m16n8k16 products with the 16 tokens as rows and the query rows as columns: a lane's operand registers are pairs of

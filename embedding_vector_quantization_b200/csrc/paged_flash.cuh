@@ -19,10 +19,10 @@
 // Roundings: c[idx] (hardly: table_factor in tq_api.cu), Pi with signs (an f16 pair without), S, rnorm / norm, x_hat, the prepared query (scaled by a power of two below 1) and the weights
 // to f16 (11 bits; outputs have 8 or 11); every sum, maximum and exponent in fp32.
 //
-// Measured at 8 KV heads, 32 query heads, d = 128: a chunk of 1024 tokens over 32768 with signs takes 680 us (expansion 80,
-// flash 550: 1.05 PFLOP/s, 0.64 of what a plain matrix product reaches); four prompts of up to 4096 tokens 362 us (flash 265).
-// The flash kernel is bound by the softmax between its two products: a tile's exponents, scales and conversions occupy the
-// issue slots as long as its contractions the tensor pipe (46 % busy with the triangles' half tiles counted, XU 37 %, ALU 29 %).
+// Measured at 8 KV heads, 32 query heads, d = 128: a chunk of 1024 tokens over 32768 with signs takes 690 us (expansion 77,
+// flash 570: 0.98 PFLOP/s, 0.60 of what a plain matrix product reaches); four prompts of up to 4096 tokens 380 us (flash 278).
+// Nothing in the flash kernel is busy more than half the time (prompts: tensor pipe 43 % with the triangles' half tiles counted,
+// issue slots 46 %, XU 35 %): it waits on each tile's chain of scores, maximum, barrier of 256 threads and weights.
 #pragma once
 
 #include <climits>
@@ -960,8 +960,8 @@ __device__ __forceinline__ bool bar_any(int id, int n, bool pred) {
       : "memory");
   return r != 0;
 }
-// Of so many pairs of exponentials one goes to the polynomial: 546 us with a fourth for a chunk of 1024 tokens over 32768
-// (8 KV heads, 32 query heads, d = 128), 549 with a third, 559 with half and 557 without.
+// Of so many pairs of exponentials one goes to the polynomial: 579 us with a fourth for a chunk of 1024 tokens over 32768
+// (8 KV heads, 32 query heads, d = 128), 577 with a third, 597 with half and 584 without; four prompts 276, 274, 282 and 281.
 constexpr int kPolyEvery = 4;
 
 template <int D>
@@ -1157,7 +1157,7 @@ __global__ void __launch_bounds__(kFlThreads, 1) paged_flash_kernel(FlashArgs a)
       // Running reference (log2) and sum of the weights. The value sums have a unit of their own, 2^(m + b), which follows what the
       // row's weights and the value tiles' exponents make together: a large value that the row hardly sees costs it nothing.
       // Where b is set it is a whole number, so that a row's largest weight comes out as a power of two, exact in f16; where m
-      // moves, b makes up for it (sums that kept to whole numbers would have to be scaled then: 565 -> 609 us). limit: what a
+      // moves, b makes up for it (sums that kept to whole numbers would have to be scaled then: 562 -> 609 us). limit: what a
       // score may be without moving m (-infinity while there is no unit; NaN where |m| is above 2^14, whose tiles all take the
       // rare part below); rest: -(m + b), or 0.
       float m = -INFINITY, l = 0.f, b = -INFINITY, limit = -INFINITY, rest = 0.f;

@@ -339,7 +339,10 @@ typedef struct tq_head_prep {
  *  hk, hv        MSE, prod or QJL-only handles of one d <= 256 (m <= 256), on one device
  * The indices and signs are those of exact arithmetic: a coordinate that lies within the rounding of the fast
  * path of a border is computed again in 64 bits, so a token's codes and signs depend neither on the batch it
- * came in nor on the kernel that wrote it (norms may differ by one step of fp16, two of fp32).
+ * came in nor on the kernel that wrote it (norms may differ by one step of fp16, two of fp32). The rounding inside
+ * the tensor cores (many vectors, d 64 or 128, m 0 or d) is not specified: what is allowed for it is 2.6 times (signs)
+ * and 2.8 times (indices) the largest seen in 6.7e7 coordinates; the other kernels' bound is proven. Of a vector that is
+ * not finite only the norm is defined; a norm past the norms' type is stored as infinity.
  * A token whose page (outside 0 .. num_pages - 1, position outside 0 .. max_pages * page_size - 1) or rotation
  * position (outside 0 .. max_pos - 1) is out of range is skipped and recorded in hk's error word (TQ_EINVAL
  * from tq_last_status). Two tokens with the same place race; which one stays is undefined. */
@@ -347,8 +350,10 @@ int tq_append_paged(const tq_handle* hk, const tq_handle* hv, const void* k_new,
                     int64_t k_stride, int64_t v_stride, int Hkv, const tq_paged_batch* batch,
                     const tq_head_prep* prep, const tq_paged_cache* k, const tq_paged_cache* v, void* stream);
 
-/* Workspace (bytes) of tq_attn_paged for batches of at most this B, ntok, max_q and max_pages; never 0 for a
- * valid call. */
+/* Workspace (bytes) of tq_attn_paged for batches of at most this B, ntok, max_q and max_pages, whatever the queries'
+ * type; never 0 for a valid call. With 16-bit queries it grows with sequences times max_pages, not with the tokens cached:
+ * up to 1 GiB and what one KV head's share beyond that takes (4.2 GiB for 64 sequences, one of them with a chunk, under a
+ * block table for 131072 tokens, 8 KV heads of d = 128). */
 size_t tq_attn_paged_workspace_bytes(const tq_handle* hk, const tq_handle* hv, const tq_paged_batch* batch, int Hq,
                                      int Hkv, const tq_paged_cache* k);
 
@@ -366,8 +371,15 @@ size_t tq_attn_paged_workspace_bytes(const tq_handle* hk, const tq_handle* hv, c
  * A query that sees no key (len[b] == 0, or a position < 0) gets zeros, as does one whose rotation position is out
  * of range (recorded as above); keys on a page out of range, or at positions behind the block table's last column, are
  * not seen (recorded). A sequence whose token rows leave 0 .. ntok - 1, descend or are more than max_q is left out
- * (recorded): its rows of out, like those of padding, keep what they held. Arithmetic: fp32 queries in fp32 throughout; 16-bit queries with f16 operands on the tensor cores where
- * the formats allow (d 64 or 128, m 0 or d), sums and softmax statistics in fp32. */
+ * (recorded): its rows of out, like those of padding, keep what they held. What a query does not see has no part in
+ * its row, whatever it holds; a NaN that it sees makes the row NaN.
+ * Arithmetic: fp32 queries in fp32 throughout. 16-bit queries on the tensor cores where the formats allow (d 64 or 128,
+ * m 0 or d): queries, weights and the keys and values of chunks are rounded to f16, sums and softmax statistics are fp32.
+ * Against 64 bits, relative to the outputs (2-norm), that is 4e-4 to 6e-4 for single tokens (4/4, 4/2, 2/2 bits, 2 + 1 on
+ * both sides) and 0.8e-3 to 1.1e-3 for chunks and for other formats, 1.5e-3 at most in a chunk's worst head, measured with
+ * scores of standard deviation 2 and channels of ten times the others' size; more with wider scores; bf16 outputs' own rounding
+ * is 1.7e-3. A caller who wants fp32's precision passes fp32 queries, at about ten times the time for single tokens and
+ * hundreds of times for chunks. */
 int tq_attn_paged(const tq_handle* hk, const tq_handle* hv, const void* q, int q_dtype, int64_t q_stride, int Hq,
                   int Hkv, const tq_paged_batch* batch, const tq_head_prep* prep, const tq_paged_cache* k,
                   const tq_paged_cache* v, float scale, int causal, int window, void* out, void* workspace,
