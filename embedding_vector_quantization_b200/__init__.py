@@ -46,6 +46,7 @@ class Handle:
         self.d, self.bits_mse, self.m, self.norm_dtype = tq_get_info(self._h)
         self.codes_B, self.signs_B = tq_code_bytes(self._h)
         self.seed = seed
+        self.index = _torch().cuda.current_device()   # where its tables are
 
     @property
     def prod(self):
@@ -139,6 +140,7 @@ class PolarHandle(Handle):
         self.codes_B, self.signs_B = tq_code_bytes(self._h)
         self.levels, self.bits_level1, self.bits_upper = tq_polar_info(self._h)
         self.seed = seed
+        self.index = _torch().cuda.current_device()
 
     def level_bits(self):
         return [self.bits_level1] + [self.bits_upper] * (self.levels - 1)
@@ -301,8 +303,8 @@ def _check_paged(hk, hv, kcache, vcache, batch, prep):
     d = hk.d
     if kcache.Hkv != vcache.Hkv:
         _need(False, "the caches differ in Hkv")
-    if not kcache.index == vcache.index == batch.index:
-        _need(False, "caches and batch are on different devices")
+    if not hk.index == hv.index == kcache.index == vcache.index == batch.index:
+        _need(False, "handles, caches and batch are on different devices")
     if prep is not None:
         if prep.index is not None and prep.index != kcache.index:
             _need(False, "prep is on another device")
@@ -328,6 +330,7 @@ def _on(stream, device):
     torch = _torch()
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device)
+    _need(stream.device_index == device.index, "the stream and the caches are on different devices")
     return torch.cuda.stream(stream)
 
 

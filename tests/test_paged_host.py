@@ -82,3 +82,21 @@ def test_binding_refuses_host_tensors_and_shapes(tq):
         tq.HeadPrep(cos_sin=torch.zeros(4, 64))
     with pytest.raises(tq.TQError):
         tq.HeadPrep(weight=torch.zeros(64))
+
+
+def test_binding_refuses_other_devices(tq):
+    """A handle, a cache, a batch or a stream of another device would have a kernel follow addresses that are not its own."""
+    from types import SimpleNamespace as obj
+    mod = tq
+
+    def things(**at):
+        h = [obj(d=128, bits_mse=4, m=0, norm_dtype=1, index=at.get(n, 0)) for n in ("hk", "hv")]
+        c = [obj(handle=h[i], Hkv=2, index=at.get(n, 0)) for i, n in enumerate(("kcache", "vcache"))]
+        return (*h, *c, obj(index=at.get("batch", 0), ntok=1), obj(index=at.get("prep", 0), weight=None, pos=None))
+
+    mod._check_paged(*things())
+    for name in ("hk", "hv", "kcache", "vcache", "batch", "prep"):
+        with pytest.raises(tq.TQError, match="device"):
+            mod._check_paged(*things(**{name: 1}))
+    with pytest.raises(tq.TQError, match="device"):
+        mod._on(obj(device_index=1), torch.device("cuda", 0))
