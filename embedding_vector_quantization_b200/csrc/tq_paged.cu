@@ -583,7 +583,8 @@ int tq_attn_paged(const tq_handle* hk, const tq_handle* hv, const void* q, int q
   if ((st = tq_internal_pre_launch(hk, s))) return st;
   a.q = q, a.q_stride = q_stride, a.q_dtype = q_dtype, a.Hq = Hq, a.Hkv = Hkv, a.G = Hq / Hkv;
   a.k = quant_of(kw), a.v = quant_of(vw), a.kc = view_of(kw, k), a.vc = view_of(vw, v);
-  a.scale = scale, a.causal = causal, a.window = window, a.out = out, a.err = kw.err;
+  // Positions are above -2^24 and below 2^31: a window this wide is none, and what is taken off a position stays an int.
+  a.scale = scale, a.causal = causal, a.window = std::min(window, 0x7e000000), a.out = out, a.err = kw.err;
   char* ws = reinterpret_cast<char*>(up(reinterpret_cast<size_t>(workspace), 256));
   const int sms = device_sms(kw.device);
   if (q_dtype != TQ_F32 && flash_formats(kw, vw)) {

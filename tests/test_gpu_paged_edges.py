@@ -96,6 +96,16 @@ def test_pages_behind_the_window_may_be_freed(tq, news, lens, window, kf, vf, dt
         assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("news,lens", [([8, 1], [3, 300]), ([340, 45], [300, 20])])
+def test_a_window_as_wide_as_its_type_is_none(tq, news, lens, dtype):
+    """Also where the first tokens stand before the first position."""
+    c = attention_case(tq, 128, "mse4", "mse4", 2, 4, news, lens, 16, dtype)
+    want = check_case(tq, c, 0.09, True, 0, h_of(dtype))
+    for window in (2 ** 31 - 1, 2 ** 31 - 5, 2 ** 30):
+        assert torch.equal(check_case(tq, c, 0.09, True, window, h_of(dtype)), want)
+
+
 # ------------------------------------------------------------------ lengths and bounds that are not what they say
 
 
