@@ -63,8 +63,12 @@ def _stale(src, obj, dep, key):
 
 
 def _fresh(key):
-    return (os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest_source_mtime()
-            and (key is None or _read(os.path.join(HERE, "_build", "libtq.key")) == key))
+    """Whether the library is newer than its sources and, where it came with its record (_build/libtq.key), made as it would be
+    here."""
+    if not os.path.exists(LIB) or os.path.getmtime(LIB) < _newest_source_mtime():
+        return False
+    made = _read(os.path.join(HERE, "_build", "libtq.key"))
+    return key is None or not made or made == key
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

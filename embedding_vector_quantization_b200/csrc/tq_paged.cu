@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <cstdint>
 #include <cstdlib>
 #include <cstring>
 
@@ -574,6 +575,12 @@ int tq_attn_paged(const tq_handle* hk, const tq_handle* hv, const void* q, int q
   if ((st = check_rows(q, q_dtype, q_stride, Hq, kw.d, "q"))) return st;
   if (!out || !aligned(out, 16)) return fail(TQ_EINVAL, "out is NULL or misaligned (16 bytes)");
   if (!workspace || !aligned(workspace, 16)) return fail(TQ_EINVAL, "workspace is NULL or misaligned (16 bytes)");
+  // The chunks' plan counts (item, key tile) pairs of one KV head in 32 bits.
+  const int64_t items = batch->ntok * (Hq / Hkv) / kItemRows + std::min<int64_t>(batch->B, batch->ntok);
+  const int64_t most_tiles = ((int64_t)batch->max_pages * k->page_size + kKT - 1) / kKT + kItemCost;
+  if (q_dtype != TQ_F32 && flash_formats(kw, vw) && items > INT32_MAX / most_tiles)
+    return fail(TQ_EUNSUPPORTED, "%lld query tiles of up to %lld key tiles: more than 2^31 pairs, split the batch", (long long)items,
+                (long long)most_tiles);
   const size_t need = attn_workspace(kw, vw, a.bt, Hq, Hkv);
   if (ws_bytes < need) return fail(TQ_EINVAL, "workspace of %zu bytes, %zu needed", ws_bytes, need);
   if (tq_internal_fault("launch")) return fail(TQ_ECUDA, "injected launch failure (TQ_FAULT=launch)");

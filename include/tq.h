@@ -370,7 +370,8 @@ size_t tq_attn_paged_workspace_bytes(const tq_handle* hk, const tq_handle* hv, c
  *  workspace   device scratch, 16-byte aligned; calls that overlap need one each
  * A query that sees no key (len[b] == 0, or a position < 0) gets zeros, as does one whose rotation position is out
  * of range (recorded as above); keys on a page out of range, or at positions behind the block table's last column, are
- * not seen (recorded). A sequence whose token rows leave 0 .. ntok - 1, descend or are more than max_q is left out
+ * not seen (recorded). More than 2^31 pairs of 256 query rows and 128 keys (by the table's width) of a KV head are
+ * TQ_EUNSUPPORTED with 16-bit queries on the tensor cores. A sequence whose token rows leave 0 .. ntok - 1, descend or are more than max_q is left out
  * (recorded): its rows of out, like those of padding, keep what they held. What a query does not see has no part in
  * its row, whatever it holds; a NaN that it sees makes the row NaN.
  * Arithmetic: fp32 queries in fp32 throughout. 16-bit queries on the tensor cores where the formats allow (d 64 or 128,

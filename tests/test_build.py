@@ -132,6 +132,16 @@ def test_a_copied_tree_compiles_its_own_sources(tree, tmp_path):
     assert compiled(cuda) == ALL
 
 
+def test_a_library_that_came_without_its_objects_is_taken(tree):
+    pkg, cuda = tree
+    b = load(pkg)
+    b.build()
+    compiled(cuda)
+    shutil.rmtree(pkg / "_build")
+    b.build()
+    assert compiled(cuda) == []
+
+
 def test_without_a_compiler_a_fresh_library_is_taken(tree, monkeypatch):
     pkg, cuda = tree
     b = load(pkg)

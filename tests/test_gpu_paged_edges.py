@@ -170,6 +170,17 @@ def test_bad_bounds_are_recorded_and_their_rows_kept(tq, news, dtype):
         assert ((got - want)[~mine].abs() <= room).all()
 
 
+def test_more_tile_pairs_than_are_counted_are_refused(tq):
+    """2^24 tokens of 64 query heads over 2^30 positions: refused before the workspace is looked at."""
+    h = fmt(tq, 128, "mse4", 0).handle
+    cache = tq._lib.tq_paged_cache(1 << 12, None, 1 << 12, None, 1 << 20, 1024)
+    batch = tq._lib.tq_paged_batch(1 << 12, 1 << 12, 1 << 12, 1, 1 << 20, 1 << 24, 1 << 24)
+    r = tq._lib.ctypes.byref
+    st = tq._lib.lib.tq_attn_paged(h.ptr, h.ptr, 4096, tq.TQ_BF16, 64 * 128, 64, 1, r(batch), None, r(cache), r(cache), 0.1, 1, 0,
+                                   4096, 4096, 16, None)
+    assert st == tq.TQ_EUNSUPPORTED and "split the batch" in tq.tq_last_error()
+
+
 # ------------------------------------------------------------------ norms far apart
 
 
