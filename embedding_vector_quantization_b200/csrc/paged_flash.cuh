@@ -5,19 +5,21 @@
 //   plan    one CTA lists the sequences that come here (more than `small_rows` query rows), their key tiles of 128 tokens
 //           and their items of 256 query rows, with the running sum of the items' key tiles;
 //   expand  key tiles -> f16 rows x_hat = Pi^T c[idx] + rnorm / norm * sqrt(pi/2) / m S^T (2 sigma - 1), as a
-//           128 x d x (d + m) contraction per tile on the tensor cores; stored as the very shared-memory images the attention
+//           128 x d x 2 d contraction per tile on the tensor cores (with no signs Pi as an f16 pair); stored as the very shared-memory images the attention
 //           wants, 32 KB a tile. Norms: a tile whose norms lie within 2^8 of each other has its rows times norm 2^-E, with
 //           2^E >= every norm of it, which costs f16 nothing; any other tile ("apart") keeps rows of length about one, and the
 //           attention multiplies scores and weights by the norms of its 128 tokens;
 //   flash   softmax(scale q k^T) v over those tiles with the running maximum and sum of each row;
 //   merge   items that several CTAs shared.
-// Values come back in the original basis, so outputs need no rotation; keys times a Hadamard matrix, as the queries are: a channel
-// far larger than the others would have its coordinate's rounding to f16 decide the scores, which the Hadamard matrix spreads
-// over all coordinates. Signs cost no wider contraction: 4 d flops per (query row, key) for every format, where contracting the codes themselves would take
-// 2 (2 d + m_k + m_v). The f16 rows are written and read once through L2 (512 B per token and head at d = 128).
+// Values come back in the original basis, so outputs need no rotation; keys times a Hadamard matrix, as the queries are: a
+// channel far larger than the others would have its coordinate's rounding to f16 decide the scores, which the Hadamard matrix
+// spreads over all coordinates. Signs cost no wider contraction: 4 d flops per (query row, key) for every format, where
+// contracting the codes themselves would take 2 (2 d + m_k + m_v). The f16 rows are written and read once through L2 (512 B
+// per token and head at d = 128).
 //
-// Roundings: c[idx] (hardly: table_factor in tq_api.cu), Pi with signs (an f16 pair without), S, rnorm / norm, x_hat, the prepared query (scaled by a power of two below 1) and the weights
-// to f16 (11 bits; outputs have 8 or 11); every sum, maximum and exponent in fp32.
+// Roundings: c[idx] (hardly: table_factor in tq_api.cu), Pi with signs (an f16 pair without), S, rnorm / norm, x_hat, the
+// prepared query (scaled by a power of two below 1) and the weights to f16 (11 bits; outputs have 8 or 11); every sum, maximum
+// and exponent in fp32.
 //
 // Measured at 8 KV heads, 32 query heads, d = 128: a chunk of 1024 tokens over 32768 with signs takes 690 us (expansion 77,
 // flash 570: 0.98 PFLOP/s, 0.60 of what a plain matrix product reaches); four prompts of up to 4096 tokens 380 us (flash 278).
